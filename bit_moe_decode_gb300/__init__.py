@@ -19,6 +19,7 @@ MOE_SRC_BLOCKS, MOE_SRC_F32 = 0, 1
 MOE_LAYOUT_DECODE, MOE_LAYOUT_TC = 0, 1
 MOE_LAYOUT_PREFILL = MOE_LAYOUT_TC
 MOE_MAT_GATE_UP, MOE_MAT_DOWN = 0, 1
+MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_UNSUPPORTED_FORMAT",
           4: "MOE_ERR_UNSUPPORTED_ARCH", 5: "MOE_ERR_WORKSPACE_TOO_SMALL", 6: "MOE_ERR_CUDA",
@@ -32,7 +33,9 @@ EXPORTS = ["moe_status_string", "moe_version", "moe_check_device", "moe_canonica
            "moe_get_device_status", "moe_expert_ffn_decode", "moe_expert_ffn_verify", "moe_route_expert_ffn",
            "moe_debug_unpack", "moe_debug_timeout_probe", "moe_expert_ffn_decode_static", "moe_static_device_status",
            "moe_prefill_workspace_bytes",
-           "moe_expert_grouped_gemm_prefill", "moe_debug_prefill", "moe_spec_accept", "moe_rms_norm_bf16"]
+           "moe_expert_grouped_gemm_prefill", "moe_debug_prefill", "moe_spec_accept", "moe_rms_norm_bf16",
+           "moe_kv_page_bytes", "moe_kv_workspace_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention",
+           "moe_logits_probs"]
 
 
 class MoeError(RuntimeError):
@@ -44,6 +47,23 @@ class MoeError(RuntimeError):
 class moe_layer_t(C.Structure):
     _fields_ = [("fmt", C.c_int), ("layout", C.c_int), ("H", C.c_int32), ("I", C.c_int32), ("E", C.c_int32),
                 ("gate_up", C.c_void_p), ("down", C.c_void_p)]
+
+
+class moe_kv_cache_t(C.Structure):
+    _fields_ = [("fmt", C.c_int), ("head_dim", C.c_int32), ("kv_heads", C.c_int32), ("page_tokens", C.c_int32),
+                ("n_pages", C.c_int64), ("page_stride", C.c_int64), ("pages", C.c_void_p)]
+
+
+class moe_kv_batch_t(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("n_tokens", C.c_int32), ("max_q", C.c_int32), ("table_stride", C.c_int32),
+                ("q_start", C.c_void_p), ("seq_len", C.c_void_p), ("block_table", C.c_void_p)]
+
+
+class moe_logits_t(C.Structure):
+    _fields_ = [("type", C.c_int), ("n_seqs", C.c_int32), ("rows_per_seq", C.c_int32), ("vocab", C.c_int32),
+                ("logits", C.c_void_p), ("logits_stride", C.c_int64), ("params", C.c_void_p), ("counts", C.c_void_p),
+                ("draft", C.c_void_p), ("bias_start", C.c_void_p), ("bias_id", C.c_void_p), ("bias_value", C.c_void_p),
+                ("allowed", C.c_void_p), ("allowed_stride", C.c_int64)]
 
 
 _lib = None
@@ -58,6 +78,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(LIB_PATH)
         P, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         LP = C.POINTER(moe_layer_t)
+        KP, BP = C.POINTER(moe_kv_cache_t), C.POINTER(moe_kv_batch_t)
         sig = {
             "moe_status_string": (C.c_char_p, [C.c_int]),
             "moe_version": (i32, []),
@@ -69,6 +90,12 @@ def lib() -> C.CDLL:
             "moe_route_topk": (C.c_int, [P, P, i32, i32, i32, i32, P, P, i32, P, P, P]),
             "moe_spec_accept": (C.c_int, [P, P, i32, i32, P, P, P, P]),
             "moe_rms_norm_bf16": (C.c_int, [P, i32, i32, C.c_float, P, P]),
+            "moe_kv_page_bytes": (sz, [C.c_int, i32, i32, i32]),
+            "moe_kv_workspace_bytes": (sz, [KP, BP, i32]),
+            "moe_kv_append": (C.c_int, [KP, BP, P, i64, P, i64, P, i64, i32, P, P, P, i32, i32, i32, P, sz, P]),
+            "moe_kv_read": (C.c_int, [KP, BP, P, P, P, sz, P]),
+            "moe_kv_attention": (C.c_int, [KP, BP, P, i64, i32, C.c_float, i32, P, P, P, sz, P]),
+            "moe_logits_probs": (C.c_int, [C.POINTER(moe_logits_t), P, P, P]),
             "moe_workspace_bytes": (sz, [LP, i32, i32]),
             "moe_workspace_init": (C.c_int, [P, sz, P]),
             "moe_get_device_status": (C.c_int, [P, P]),
@@ -156,6 +183,93 @@ def moe_spec_accept(p, q, K: int, V: int, draft, u, result, stream=None):
 def moe_rms_norm_bf16(y, T: int, H: int, eps: float, x_bf16, stream=None):
     """x_bf16[t] = bf16(y[t] / sqrt(mean(y[t]^2) + eps)) (see include/moe.h)."""
     _check(lib().moe_rms_norm_bf16(_ptr(y), T, H, eps, _ptr(x_bf16), _stream(stream)), "moe_rms_norm_bf16")
+
+
+# ------------------------------------------------------------------------------------------------ KV cache and logits
+def _rows(t, heads: int, D: int):
+    """Pointer and row stride (elements) of a bf16 [tokens, heads, D] tensor whose rows may be slices of wider ones."""
+    if t is None:
+        return None, 0
+    assert t.is_cuda and t.element_size() == 2 and t.dim() == 3 and t.shape[1:] == (heads, D), "expected bf16 [tokens, heads, D]"
+    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == D), "heads and dimensions must be contiguous"
+    return C.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * D)
+
+
+def _typed(t, dtype, *shape):
+    """Pointer of a contiguous tensor of this type and shape (None passes)."""
+    if t is None:
+        return None
+    assert t.dtype == dtype and tuple(t.shape) == shape, "expected %s %s, got %s %s" % (dtype, shape, t.dtype, tuple(t.shape))
+    return _ptr(t)
+
+
+def moe_kv_page_bytes(fmt: int, head_dim: int, kv_heads: int, page_tokens: int) -> int:
+    return lib().moe_kv_page_bytes(fmt, head_dim, kv_heads, page_tokens)
+
+
+def moe_kv_workspace_bytes(cache: "KvCache", batch: "KvBatch", q_heads: int) -> int:
+    return lib().moe_kv_workspace_bytes(C.byref(cache.c), C.byref(batch.c), q_heads)
+
+
+def moe_kv_append(cache: "KvCache", batch: "KvBatch", k, v, q=None, q_out=None, cos=None, sin=None,
+                  interleaved: bool = False, ws=None, stream=None):
+    """Rotate q and k by their positions (cos, sin [positions, R / 2] fp32; None: no rotation), write q to q_out and
+    encode k and v into their pages. k, v [tokens, kv_heads, D], q [tokens, q_heads, D] bf16, rows with any stride."""
+    n, D, Hkv = batch.c.n_tokens, cache.head_dim, cache.kv_heads
+    for t in (k, v, q):
+        assert t is None or t.shape[0] == n, "one row a token of the batch"
+    kp, ks = _rows(k, Hkv, D)
+    vp, vs = _rows(v, Hkv, D)
+    Hq = q.shape[1] if q is not None else 0
+    qp, qs = _rows(q, Hq, D)
+    assert q is None or (q_out is not None and tuple(q_out.shape) == (n, Hq, D) and q_out.element_size() == 2)
+    R, rows = (2 * cos.shape[1], cos.shape[0]) if cos is not None else (0, 0)
+    _check(lib().moe_kv_append(C.byref(cache.c), C.byref(batch.c), kp, ks, vp, vs, qp, qs, Hq, _ptr(q_out),
+                               _typed(cos, torch.float32, rows, R // 2), _typed(sin, torch.float32, rows, R // 2), R, rows,
+                               int(interleaved), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_kv_append")
+
+
+def moe_kv_read(cache: "KvCache", batch: "KvBatch", k_out, v_out, ws=None, stream=None):
+    """The values that the batch's tokens have in the cache, fp32 [tokens, kv_heads, D] (either output may be None)."""
+    shape = (batch.c.n_tokens, cache.kv_heads, cache.head_dim)
+    _check(lib().moe_kv_read(C.byref(cache.c), C.byref(batch.c), _typed(k_out, torch.float32, *shape),
+                             _typed(v_out, torch.float32, *shape), _ptr(ws), ws.numel() * ws.element_size(),
+                             _stream(stream)), "moe_kv_read")
+
+
+def moe_kv_attention(cache: "KvCache", batch: "KvBatch", q, scale: float, out, lse=None, window: int = 0, ws=None,
+                     stream=None):
+    """Attention of the batch's rows over their sequences' cache: out [tokens, q_heads, D] bf16, lse [tokens, q_heads]."""
+    n, Hq, D = batch.c.n_tokens, q.shape[1], cache.head_dim
+    assert q.shape[0] == n and tuple(out.shape) == (n, Hq, D) and out.element_size() == 2
+    qp, qs = _rows(q, Hq, D)
+    _check(lib().moe_kv_attention(C.byref(cache.c), C.byref(batch.c), qp, qs, Hq, scale, window, _ptr(out),
+                                  _typed(lse, torch.float32, n, Hq), _ptr(ws), ws.numel() * ws.element_size(),
+                                  _stream(stream)), "moe_kv_attention")
+
+
+def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, draft=None, bias=None, allowed=None,
+                     top=None, stream=None):
+    """Logits [rows, V] (fp32 or bf16; rows with any stride) -> probabilities fp32 [rows, V] after penalties (params
+    [n_seqs, 4]: repetition, presence, frequency, temperature; counts int32 [n_seqs, V]; draft int32 [n_seqs,
+    rows_per_seq - 1]), biases ((start, id, value) per sequence) and the allowed-token bits (int32 [rows, words])."""
+    R, V = logits.shape
+    n = params.shape[0]
+    assert logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16) and logits.stride(1) == 1
+    assert R == n * rows_per_seq, "rows = n_seqs * rows_per_seq"
+    start, ids, vals = bias if bias is not None and bias[1].numel() else (None, None, None)
+    if ids is not None:
+        assert ids.dtype == torch.int32 and vals.dtype == torch.float32 and ids.numel() == vals.numel()
+    if allowed is not None:
+        assert allowed.dtype == torch.int32 and allowed.dim() == 2 and allowed.shape[0] == R
+    c = moe_logits_t(MOE_LOGITS_F32 if logits.dtype == torch.float32 else MOE_LOGITS_BF16, n, rows_per_seq, V,
+                     logits.data_ptr(), logits.stride(0) if R > 1 else max(V, logits.stride(0)),
+                     _typed(params, torch.float32, n, 4),
+                     _typed(counts, torch.int32, n, V), _typed(draft, torch.int32, n, rows_per_seq - 1),
+                     _typed(start, torch.int32, n + 1), _ptr(ids), _ptr(vals), _ptr(allowed),
+                     allowed.shape[1] if allowed is not None else 0)
+    _check(lib().moe_logits_probs(C.byref(c), _typed(probs, torch.float32, R, V), _typed(top, torch.int32, R),
+                                  _stream(stream)), "moe_logits_probs")
 
 
 def moe_workspace_bytes(layer: "Layer", T_max: int, k: int) -> int:
@@ -275,10 +389,49 @@ class Layer:
         return self._ws(moe_prefill_workspace_bytes(self, T_max, k), stream)
 
     def _ws(self, nbytes: int, stream) -> torch.Tensor:
+        return _new_workspace(nbytes, self.gate_up.device, stream)
+
+
+def _new_workspace(nbytes: int, device, stream) -> torch.Tensor:
+    if nbytes == 0:
+        raise MoeError(2, "workspace size")
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + nbytes]
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+# ------------------------------------------------------------------------------------------------ a 4-bit paged KV cache
+class KvCache:
+    """Device-resident pages of a 4-bit KV cache (MOE_FMT_MXFP4 or MOE_FMT_INT4G32) and the moe_kv_cache_t that describes
+    them. pages: an existing uint8 tensor [n_pages, ...] whose pages are contiguous, or None for n_pages new ones."""
+
+    def __init__(self, fmt: int, head_dim: int, kv_heads: int, page_tokens: int, n_pages: int = 0, pages=None, device="cuda"):
+        nbytes = moe_kv_page_bytes(fmt, head_dim, kv_heads, page_tokens)
         if nbytes == 0:
-            raise MoeError(2, "workspace size")
-        ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.gate_up.device)
-        off = (-ws.data_ptr()) % 256
-        ws = ws[off:off + nbytes]
-        moe_workspace_init(ws, stream)
-        return ws
+            raise MoeError(2, "moe_kv_page_bytes")
+        if pages is None:
+            pages = torch.zeros((n_pages, nbytes), dtype=torch.uint8, device=device)
+        assert pages.dtype == torch.uint8 and pages.is_cuda and pages.shape[0] > 0 and pages[0].is_contiguous() and \
+            pages[0].numel() >= nbytes, "pages: uint8 [n_pages, at least %d bytes]" % nbytes
+        self.fmt, self.head_dim, self.kv_heads, self.page_tokens, self.pages = fmt, head_dim, kv_heads, page_tokens, pages
+        self.c = moe_kv_cache_t(fmt, head_dim, kv_heads, page_tokens, pages.shape[0],
+                                max(pages.stride(0), nbytes) if pages.shape[0] == 1 else pages.stride(0), pages.data_ptr())
+
+    def workspace(self, batch: "KvBatch", q_heads: int, stream=None) -> torch.Tensor:
+        """Zeroed, 256-byte aligned workspace for the cache's calls with batches of this size."""
+        return _new_workspace(moe_kv_workspace_bytes(self, batch, q_heads), self.pages.device, stream)
+
+
+class KvBatch:
+    """The sequences of one call: int32 device tensors q_start [n_seqs + 1], seq_len [n_seqs], block_table [n_seqs, pages],
+    which the calls read when they run (update them in place between steps), and the host-side sizes: tokens (rows of
+    q, k and v) and max_q (no sequence has more rows)."""
+
+    def __init__(self, q_start, seq_len, block_table, tokens: int, max_q: int):
+        n = seq_len.numel()
+        assert block_table.dim() == 2
+        self.q_start, self.seq_len, self.block_table = q_start, seq_len, block_table
+        self.c = moe_kv_batch_t(n, tokens, max_q, block_table.shape[1], _typed(q_start, torch.int32, n + 1),
+                                _typed(seq_len, torch.int32, n), _typed(block_table, torch.int32, n, block_table.shape[1]))

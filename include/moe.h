@@ -30,7 +30,8 @@
  *     per device for the others; one process drives one GPU) and the static scratch of
  *     moe_expert_ffn_decode_static.
  *   - Host-side fault injection for tests: if the environment variable MOE_FAULT names a call
- *     ("pack", "route", "decode", "verify", "route_ffn", "prefill", "encode", "spec", "norm"), that call returns
+ *     ("pack", "route", "decode", "verify", "route_ffn", "prefill", "encode", "spec", "norm", "kv_append", "kv_read",
+ *     "kv_attention", "logits"), that call returns
  *     MOE_ERR_FAULT_INJECTED
  *     without launching anything.
  */
@@ -285,6 +286,129 @@ moe_status_t moe_expert_grouped_gemm_prefill(const moe_layer_t* layer, const voi
  *   A token's result does not depend on the other tokens. NaN and infinity propagate.
  *   Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer), MOE_ERR_SHAPE, before any launch. */
 moe_status_t moe_rms_norm_bf16(const float* y, int32_t T, int32_t H, float eps, void* x_bf16, void* stream);
+
+/* ---------------------------------------------------------------- 4-bit paged KV cache --------------------------- */
+
+/* The attention that stands before each MoE layer of a decode or verify step, over a paged cache whose keys and values
+ * are held in the library's 4-bit block formats (MXFP4 or INT4, one scale per 32 values along the head dimension).
+ *
+ * A page holds page_tokens tokens of every KV head. Head h of a page is a run of page_tokens / 16 sub-blocks of 16
+ * tokens: K codes (8 D bytes), V codes (8 D bytes), K scales, V scales (16 nb each, nb = D / 32; E8M0 bytes for MXFP4,
+ * bf16 for INT4). Sub-block s of head h of page p starts at pages + p page_stride + (h page_tokens / 16 + s) * bytes.
+ *   K codes: token i's D / 2 bytes at i D / 2, as 32-bit words (c, b), c = 0..3 outer, b = 0..nb-1 inner; nibble n (low
+ *            first) of word (c, b) is the code of dimension 32 b + 8 c + n.
+ *   V codes: 32-bit words (g, r, c, b), g = 0..1 outermost, r = 0..7, c = 0..3, b = 0..nb-1 innermost, with the codes of
+ *            tokens 8 g + 2 c and 8 g + 2 c + 1 at dimensions 32 b + 4 r + j, j = 0..3. MXFP4: byte j, the even token in
+ *            the low nibble, the odd one in the high nibble. INT4: nibble j for the even token, 4 + j for the odd one.
+ *   Scales:  token-major, nb a token.
+ * What lies past a sequence's end in its last page is never used, whatever its bytes are. */
+typedef struct {
+  moe_format_t fmt;       /* MOE_FMT_MXFP4 or MOE_FMT_INT4G32 */
+  int32_t head_dim;       /* D: 64 or 128 */
+  int32_t kv_heads;       /* 1 .. 256 */
+  int32_t page_tokens;    /* a multiple of 16, 16 .. 1024 */
+  int64_t n_pages;        /* >= 1; page ids are 0 .. n_pages - 1 */
+  int64_t page_stride;    /* bytes from one page to the next: a multiple of 16, >= moe_kv_page_bytes */
+  void* pages;            /* 16-byte aligned device memory */
+} moe_kv_cache_t;
+
+/* The sequences of one call. All arrays are device memory; nothing but the sizes is read on the host, so a captured
+ * graph follows new lengths and tables. Sequence b has the q_start[b + 1] - q_start[b] rows q_start[b] .. of the call's
+ * tensors: its newest tokens, at positions seq_len[b] - (their number) .. seq_len[b] - 1 (seq_len counts them). A row at a
+ * negative position (a padding slot with seq_len 0) is in no sequence: it is not stored, it attends to nothing.
+ * Page of position s: block_table[b * table_stride + s / page_tokens]; only entries up to the sequence's end are read. */
+typedef struct {
+  int32_t n_seqs;         /* 1 .. 1024 */
+  int32_t n_tokens;       /* rows of the call's tensors, >= 1; q_start[n_seqs] <= n_tokens */
+  int32_t max_q;          /* no sequence has more rows than this */
+  int32_t table_stride;   /* entries of a block table row, >= 1; table_stride * page_tokens < 2^30 */
+  const int32_t* q_start;     /* [n_seqs + 1], increasing from 0 */
+  const int32_t* seq_len;     /* [n_seqs] */
+  const int32_t* block_table; /* [n_seqs, table_stride] */
+} moe_kv_batch_t;
+
+/* Bytes of one page (0 for an unsupported format or size). */
+size_t moe_kv_page_bytes(moe_format_t fmt, int32_t head_dim, int32_t kv_heads, int32_t page_tokens);
+
+/* Workspace of moe_kv_append / _read / _attention for batches of up to batch->n_seqs sequences of up to batch->max_q rows
+ * and q_heads query heads (0 for unsupported sizes). Zero it once with moe_workspace_init(); the calls leave it ready for
+ * the next one. Calls that overlap on the GPU must not share a workspace. Its first word is the device status word
+ * (moe_get_device_status): MOE_ERR_INVALID_ARG for device data out of range (rows that are not in the call's tensors,
+ * more rows than max_q, a length beyond the table, a page id outside [0, n_pages), a position beyond the rotation
+ * tables). Nothing out of range is accessed then: such a sequence counts as empty (attention: zeros, lse -inf, as far as
+ * its rows exist), such a page is not written, and reads as page 0. */
+size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t q_heads);
+
+/* Append: rotates q and k, encodes k and v into their places in the cache.
+ *   k, v [n_tokens, kv_heads, D] bf16, q [n_tokens, q_heads, D] bf16 (NULL: none), each with its own row stride in
+ *   elements (a slice of a fused projection's output); heads and dimensions contiguous. q_out [n_tokens, q_heads, D] bf16,
+ *   contiguous (may be q itself if that is contiguous).
+ *   Rotation (rope_dim R > 0, a multiple of 8, <= D; R = 0: none) by position s: cos, sin [rope_rows, R / 2] fp32, pairs
+ *   (i, i + R / 2), or (2i, 2i + 1) if interleaved: y_a = x_a cos_i - x_b sin_i, y_b = x_b cos_i + x_a sin_i in fp32, each
+ *   product and each sum rounded; dimensions from R on are unchanged. Rows at negative positions are rotated by row 0.
+ *   q_out is rounded to bf16 once; the rotated k is encoded from fp32, v from its bf16 values:
+ *   values are clamped to +-2^64 (NaN counts as 0) and encoded by moe_encode_blocks' rules for the format, the INT4
+ *   candidates' squares summed pairwise (i with i + 16, then + 8, + 4, + 2, + 1).
+ *   All pointers 16-byte aligned, strides multiples of 8.
+ *   MXFP4 codes of an even and the following odd token share bytes: append to a sequence from one stream at a time. */
+moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const void* q, int64_t q_stride, int32_t q_heads, void* q_out,
+                           const float* cos, const float* sin, int32_t rope_dim, int32_t rope_rows, int32_t interleaved,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Read back the values that the batch's tokens have in the cache: k_out, v_out [n_tokens, kv_heads, D] fp32 (either may be
+ * NULL; 16-byte aligned); rows at negative positions give zeros. A batch whose q_start counts whole sequences reads whole
+ * sequences; max_q is not limited here, nor in moe_kv_append. */
+moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, float* k_out, float* v_out, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Attention of the batch's rows (decode: one a sequence; verify: up to 8) over their sequences' cache, grouped queries:
+ * query head n reads KV head n / (q_heads / kv_heads).
+ *   x_s = scale * q . k_s over the keys s <= position, and s > position - window if window > 0 (0: no window);
+ *   out [n_tokens, q_heads, D] bf16 = sum_s softmax(x)_s v_s, lse [n_tokens, q_heads] fp32 = log sum_s exp(x_s) (natural;
+ *   NULL: not wanted). A row that sees no key gives zeros and -inf.
+ *   Numerics: q scaled by a power of two into binary16 (exact within 2^-28 of the row's largest), codes exact, block scales
+ *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s times the value scales are scaled by a
+ *   running power of two per (row, 32 dimensions) and rounded to binary16 once (2^-12 relative).
+ *   q 16-byte aligned with a stride multiple of 8; max_q <= 8, max_q * q_heads / kv_heads <= 128. Scales of blocks that
+ *   moe_kv_append writes are finite and below 2^64; other contents must keep to that.
+ *   The result of a row does not depend on when CTAs run (partial results are joined in a fixed order). */
+moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q, int64_t q_stride,
+                              int32_t q_heads, float scale, int32_t window, void* out, float* lse, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- logits to probabilities ------------------------ */
+
+typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_type_t;
+
+/* The rows p that moe_spec_accept reads, from the last layer's logits. n_seqs sequences of rows_per_seq rows each (1 + K
+ * of a verify step; 1 for plain decode); row r belongs to sequence i = r / rows_per_seq and is its row j = r % rows_per_seq.
+ * Every pointer is device memory, and NULL leaves that step out. */
+typedef struct {
+  moe_logits_type_t type;   /* of logits */
+  int32_t n_seqs, rows_per_seq, vocab;   /* n_seqs * rows_per_seq < 2^16; rows_per_seq <= 64; 1 <= vocab <= 2^22 */
+  const void* logits;       /* [rows, vocab], row stride logits_stride elements (>= vocab) */
+  int64_t logits_stride;
+  const float* params;      /* [n_seqs, 4]: repetition (> 0, 1: none), presence, frequency, temperature (>= 0); not NULL */
+  const int32_t* counts;    /* [n_seqs, vocab]: how often each token has occurred */
+  const int32_t* draft;     /* [n_seqs, rows_per_seq - 1]: row j has also seen drafts 0 .. j - 1 (ids outside the
+                               vocabulary count for nothing); used with counts only */
+  const int32_t* bias_start;/* [n_seqs + 1]: sequence i's biases are entries bias_start[i] .. bias_start[i + 1] - 1 of */
+  const int32_t* bias_id;   /*   bias_id (token; outside the vocabulary: ignored; each at most once a sequence) and */
+  const float* bias_value;  /*   bias_value */
+  const uint32_t* allowed;  /* [rows, allowed_stride]: bit v % 32 of word v / 32 set: token v is allowed */
+  int64_t allowed_stride;   /* words, >= ceil(vocab / 32) */
+} moe_logits_t;
+
+/* For each row, in fp32 with each operation rounded, c the count of token v (with earlier drafts):
+ *   x = logit (NaN: -inf); if c > 0: x = x > 0 ? x / repetition : x * repetition, then x = (x - frequency * c) - presence;
+ *   x = x + bias; x = -inf where not allowed;
+ *   probs [rows, vocab] fp32 (contiguous): softmax(x / temperature); temperature 0: 1 at the first largest x, else 0. Where
+ *   the largest x is +inf, the tokens at +inf share the row equally. A row whose x are all -inf gives zeros.
+ *   top [rows] int32 (or NULL): the first largest x's token, -1 if all are -inf.
+ *   Logits and probs may have any alignment of their type; every other pointer 4-byte aligned. probs may be logits itself
+ *   if those are fp32 with stride vocab. Errors are found on the host; runs on `stream`, no workspace. */
+moe_status_t moe_logits_probs(const moe_logits_t* logits, float* probs, int32_t* top, void* stream);
 
 /* ---------------------------------------------------------------- debug (tests only) ----------------------------- */
 
