@@ -3,13 +3,14 @@
 #pragma once
 #include "common.cuh"
 #include "api_internal.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace kv {
 
 constexpr int kMaxSeqs = 1024;
 constexpr int kMaxRows = 128;    // query rows of one KV head in one attention call: max_q * (q_heads / kv_heads)
-constexpr int kMaxCtas = 192;    // CTAs an attention launch uses at most (one per SM of a GB300's 152)
+constexpr int kMaxCtas = 160;    // CTAs an attention launch uses at most (one per SM; a GB300 has 152)
 
 // 16 tokens of one KV head
 template <int FMT, int D>

@@ -1,71 +1,1015 @@
 // kv_attn.cu -- attention of a decode or verify step over the 4-bit paged KV cache.
 //
 // For each query row: x_s = scale q . k_s over the visible keys s, out = sum_s softmax(x)_s v_s, lse = log sum_s exp(x_s), in
-// one pass over the keys with a running maximum m and sum l: when m grows to m', l and the output so far are multiplied by
-// exp(m - m').
+// one pass over the keys with a running maximum m and sum l.
+//
+// What bounds it. A key of one KV head is 136 bytes (MXFP4, D = 128) of HBM traffic and 256 codes to convert. At the
+// measured 6.7 TB/s an SM gets 44 bytes per ns, so it has about 24 issue slots per warp-wide MMA (16 keys x 16
+// dimensions) and half as many in the integer pipe. Everything below serves to convert a code with as few instructions
+// as possible, once per 8 query rows.
+//
+// Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, and the units are dealt out evenly: every
+// warp of the grid streams one contiguous run of them (the prefix sums over the sequences are formed by each CTA from
+// the device's lengths, so a captured graph follows them). A warp copies its units with bulk copies (one per 16-token
+// sub-block, which the layout keeps contiguous) into its own ring and is its own consumer, so there is no barrier
+// between warps until the end. A pair that lies in several warps is joined from partial results, first inside the
+// CTA, then, if it spans CTAs, by the CTA that finishes last (a counter per pair, left at zero); always in the order of
+// the keys, so the bits do not depend on timing. More than 8 NT query rows: RG warps stream the same units, each
+// for its own rows (the copies then hit L2).
+//
+// Arithmetic, for 16 keys x 8 rows at a time on mma.sync.m16n8k16 with the keys (then the dimensions) as the 16 rows,
+// so that a decode step's few query rows fill the 8 columns:
+//   S^T = K Q^T: a K word holds 8 codes of one key whose order in the contraction is free, so a lane's 16 bytes of a key
+//     are its A fragments of all blocks. Codes become exact binary16 (E2M1: one conversion per pair; INT4: the nibble
+//     + 8 as a subnormal n 2^-24 or n 2^-20 by one mask, with -8 sum q as the accumulator's start and 2^-4 in q's
+//     fragments), q is scaled by a power of two into binary16, and each block's scale multiplies its fp32 partial.
+//   O^T += V^T P^T: the V layout puts an even and the following odd token's codes of one dimension side by side, which
+//     is what an A fragment's register holds. movmatrix turns the weights' accumulator layout into a B fragment. V's
+//     scales vary along the contraction, so they go into the weights: p_s vscale_s, rounded to binary16 once.
+//   Range: the weights are carried as 2^14 p, at most 2^15 (m is raised when a score passes m + 1), and the value
+//     scales as v 2^-E in binary16, exact within 2^-7 .. 1, with E per block of 32 dimensions the exponent of the largest
+//     scale; the fp32 accumulators hold 2^(14 - E) times the output. Products keep all 11 bits down to 2^-28 of the
+//     largest possible one. Where scales leave the window, E moves (accumulators rescaled, exactly) and the keys take
+//     passes: each adds the products of the next 26 powers of two at a scale of its own, so that no ratio of scales
+//     costs precision.
+#include <cfloat>
+
 #include "kv.cuh"
 
 namespace moe {
 namespace kv {
 
-constexpr int kThreads = 128;
+constexpr int kUnitSubs = 2;        // sub-blocks per unit
+constexpr int kBatch = 16;          // units whose addresses a warp's lanes hold at a time
+constexpr int kSmemMax = 232448;
+constexpr int kPExp = 14;               // weights are carried times 2^14
+constexpr float kLazy = 1.f;            // a score may pass the running maximum by this (base 2)
+constexpr float kNormal = 6.103515625e-05f;   // 2^-14: binary16 products from here on keep all bits
+constexpr int kPassExp = 26;            // powers of two that a pass covers
 
-// One CTA per (row, query head); its warps take keys in turn, a lane holds D / 32 dimensions.
-template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads) attn_kernel(Args a, const uint16_t* q, int64_t q_stride, int q_heads, float scale,
-                                                        int window, uint16_t* out, float* lse) {
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int32_t q_heads, group, window, row_groups, stages;
+  float scale_log2;                 // scale * log2(e)
+  uint16_t* out;
+  float* lse;
+  uint32_t* counters;               // [n_seqs * kv_heads]
+  float* warp_parts;                // [CTAs][warps] partials of runs that end inside a warp's range
+  float* cta_parts;                 // [CTAs][2]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN loses, as in fmaxf
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // 8 x 8 of 16 bits over the warp
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {   // (selector bit 3: the byte's sign fill)
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {   // N = 1, 2 or 4 words
+  if (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1 % N] = u.y; w[2 % N] = u.z; w[3 % N] = u.w;
+  } else if (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1 % N] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// the scales of one token's blocks in fp32
+template <int FMT, int NB>
+__device__ __forceinline__ void load_scales(float (&s)[NB], const uint8_t* p) {
+  if (FMT == MOE_FMT_MXFP4) {   // 2^(e - 127), e = 0 is zero: the byte is the exponent field
+    const uint32_t w = NB == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t v = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
+      s[b] = __uint_as_float(b == 0 ? v & 0x7F800000u : v & 0x7F800000u);
+    }
+  } else {
+    uint32_t w[NB / 2];
+    load_words<NB / 2>(w, p);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s[b] = __uint_as_float(b & 1 ? w[b / 2] & 0xFFFF0000u : w[b / 2] << 16);
+  }
+}
+
+// Two keys' K words (rows r and r + 8) of one block -> the A fragments of its two k-steps.
+template <int FMT>
+__device__ __forceinline__ void decode_k(uint32_t w0, uint32_t w1, uint32_t (&a)[2][4]) {
+  if (FMT == MOE_FMT_MXFP4) {
+    a[0][0] = e2m1x2_to_f16x2(w0, 0); a[0][1] = e2m1x2_to_f16x2(w1, 0);
+    a[0][2] = e2m1x2_to_f16x2(w0, 1); a[0][3] = e2m1x2_to_f16x2(w1, 1);
+    a[1][0] = e2m1x2_to_f16x2(w0, 2); a[1][1] = e2m1x2_to_f16x2(w1, 2);
+    a[1][2] = e2m1x2_to_f16x2(w0, 3); a[1][3] = e2m1x2_to_f16x2(w1, 3);
+  } else {   // code + 8 as n 2^-24 (first of a pair of steps' registers) and n 2^-20 (second)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      a[s][0] = lop3_and_xor(w0, 0x000F000Fu, 0x00080008u); a[s][1] = lop3_and_xor(w1, 0x000F000Fu, 0x00080008u);
+      a[s][2] = lop3_and_xor(w0, 0x00F000F0u, 0x00800080u); a[s][3] = lop3_and_xor(w1, 0x00F000F0u, 0x00800080u);
+      w0 >>= 8;
+      w1 >>= 8;
+    }
+  }
+}
+
+// V words of tokens 2c, 2c + 1 (w0) and 2c + 8, 2c + 9 (w1) of one block -> the A fragments of its two 16-dimension tiles.
+// INT4 values come out as q 2^-24 in the fragments' first row half, q 2^-20 in the second.
+template <int FMT>
+__device__ __forceinline__ void decode_v(uint32_t w0, uint32_t w1, uint32_t (&a)[2][4]) {
+  if (FMT == MOE_FMT_MXFP4) {
+    a[0][0] = e2m1x2_to_f16x2(w0, 0); a[0][1] = e2m1x2_to_f16x2(w0, 1);
+    a[0][2] = e2m1x2_to_f16x2(w1, 0); a[0][3] = e2m1x2_to_f16x2(w1, 1);
+    a[1][0] = e2m1x2_to_f16x2(w0, 2); a[1][1] = e2m1x2_to_f16x2(w0, 3);
+    a[1][2] = e2m1x2_to_f16x2(w1, 2); a[1][3] = e2m1x2_to_f16x2(w1, 3);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      a[s][0] = hadd2_bits(lop3_and_xor(w0, 0x000F000Fu, 0x00080008u), 0x80088008u);
+      a[s][1] = hadd2_bits(lop3_and_xor(w0, 0x00F000F0u, 0x00800080u), 0x80808080u);
+      a[s][2] = hadd2_bits(lop3_and_xor(w1, 0x000F000Fu, 0x00080008u), 0x80088008u);
+      a[s][3] = hadd2_bits(lop3_and_xor(w1, 0x00F000F0u, 0x00800080u), 0x80808080u);
+      w0 >>= 8;
+      w1 >>= 8;
+    }
+  }
+}
+
+struct SeqInfo { int q0, qn, len, sub0; };   // sub0: first sub-block that a row sees
+
+__device__ __forceinline__ int seq_units(const SeqInfo& s) {
+  return s.qn > 0 && s.len > 0 ? ((s.len + 15) / 16 - s.sub0 + kUnitSubs - 1) / kUnitSubs : 0;
+}
+
+struct Prod {        // a warp's producer: the next batch is n units (subs sub-blocks from `sub` on) at unit u of a pair; left
+  int b, h, u, units, left, n, subs, sub;   // counts the units from it on
+  int ev_run[4];     // and of its consumer, per block: the largest value scale's exponent so far,
+  int ev_ref[4];     // and the E in use
+};
+
+struct Entry {       // a partial result of one warp: flat units [f0, f1) of pair `seg`
+  long long f0, f1;
+  int seg, b;        // seg < 0: none
+};
+struct Run {         // consecutive entries of one pair
+  long long f0, f1;
+  int first, last, b, h, slot, whole;
+};
+
+// One query row's joined result: weighted sum of the parts, written out or stored as a part again.
+template <int D>
+struct Row {
+  static constexpr int E = D / 32;   // values a lane holds: dimensions E lane ..
+  float o[E], m, l;
+  __device__ void clear() {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    l = 0.f;
+  }
+  __device__ void add(const float* po, float pm, float pl) {
+    const float w = ex2(pm - m);
+    l += w * pl;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += w * po[e];
+  }
+  __device__ void write(const AttnArgs& g, int64_t row, int lane) const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const __nv_bfloat162 v = l > 0.f || l != l ? __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
+      w[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(g.out + row * D + E * lane);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
+    if (g.lse && lane == 0) g.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
+  }
+};
+
+template <int FMT, int D, int NT, int NW, int SUBS>
+__global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   using S = Sub<FMT, D>;
-  constexpr int E = D / 32;
-  __shared__ float sm[kThreads / 32], sl[kThreads / 32], so[kThreads / 32][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x, n = blockIdx.y;
-  int b = 0;
-  while (b + 1 < a.n_seqs && a.q_start[b + 1] <= t) ++b;
-  const Seq sq = load_seq(a, b, a.max_q);
-  const int j = t - sq.q0;
-  const int pos = j >= 0 && j < sq.qn && sq.len > 0 ? sq.len - sq.qn + j : -1;
-  const int h = n / (q_heads / a.kv_heads);
-  const int lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-  float qv[E], o[E] = {0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)   // dimension 32 e + lane
-    qv[e] = __uint_as_float((uint32_t)q[(int64_t)t * q_stride + (int64_t)n * D + 32 * e + lane] << 16) * scale;
-  for (int s = lo + warp; s <= pos; s += kThreads / 32) {
-    bool ok;
-    const int pg = s / a.page_tokens, slot = s & 15;
-    const int id = check_page(a, a.block_table[(int64_t)b * a.table_stride + pg], ok);
-    const uint8_t* sb = a.pages + (int64_t)id * a.page_stride +
-                        (int64_t)(h * (a.page_tokens / 16) + ((s - pg * a.page_tokens) >> 4)) * S::BYTES;
-    float x = 0.f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint32_t kc = sb[slot * (D / 2) + ((lane >> 3) * S::NB + e) * 4 + ((lane & 7) >> 1)] >> (4 * (lane & 1)) & 15u;
-      const uint8_t* word = sb + S::VC + ((((slot >> 3) * 8 + (lane >> 2)) * 4 + ((slot >> 1) & 3)) * S::NB + e) * 4;
-      const uint32_t vc = FMT == MOE_FMT_MXFP4 ? word[lane & 3] >> (4 * (slot & 1)) & 15u
-                                               : word[(slot & 1) * 2 + ((lane & 3) >> 1)] >> (4 * (lane & 1)) & 15u;
-      x += qv[e] * (code_value<FMT>(kc) * load_scale<FMT>(sb + S::KS + (slot * S::NB + e) * S::SB));
-      v[e] = code_value<FMT>(vc) * load_scale<FMT>(sb + S::VS + (slot * S::NB + e) * S::SB);
+  constexpr int NB = S::NB, UNIT = kUnitSubs * S::BYTES, ROWS = 8 * NT, E = D / 32;
+  constexpr int PART = ROWS * (D + 2);                   // floats of a warp's partial: o [ROWS][D], m [ROWS], l [ROWS]
+  constexpr int NVC = FMT == MOE_FMT_MXFP4 ? 1 : NB;
+  constexpr float kVal = FMT == MOE_FMT_INT4G32 ? 16777216.f : 1.f;   // 2^24 of the INT4 fragments
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Entry s_entry[2 * NW];
+  __shared__ Run s_run[2 * NW];
+  __shared__ int s_runs, s_last[2];
+  __shared__ long long s_warp[NW], s_total;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+  const int stages = g.stages, RG = g.row_groups, KS = NW / RG, Hkv = a.kv_heads;
+  const int stream = warp / RG, rg = warp % RG;
+  uint8_t* ring = smem + (size_t)warp * stages * UNIT;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)NW * stages * UNIT);
+  uint64_t* bar = bars + warp * stages;
+  long long* prefix = reinterpret_cast<long long*>(bars + NW * stages);           // [n_seqs + 1]
+  SeqInfo* info = reinterpret_cast<SeqInfo*>(prefix + a.n_seqs + 1 + ((a.n_seqs + 1) & 1));
+  Prod* prods = reinterpret_cast<Prod*>(info + a.n_seqs);
+
+  // ---- the sequences: lengths, first visible sub-block, prefix sums of their units over all KV heads
+  if (lane < stages) mbar_init(bar + lane, 1);
+  if (tid < 2 * NW) s_entry[tid].seg = -1;
+  if (tid == 0) { prefix[0] = 0; s_total = 0; }
+  for (int base = 0; base < a.n_seqs; base += NW * 32) {
+    const int b = base + tid;
+    long long x = 0;
+    if (b < a.n_seqs) {
+      const Seq sq = load_seq(a, b, a.max_q);
+      SeqInfo si{sq.q0, sq.qn, sq.len, 0};
+      if (g.window > 0 && sq.len - sq.qn - g.window + 1 > 0) si.sub0 = (sq.len - sq.qn - g.window + 1) / 16;
+      info[b] = si;
+      x = (long long)seq_units(si) * Hkv;
     }
 #pragma unroll
-    for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, i);
-    const float mn = fmaxf(m, x), c = expf(m - mn), p = expf(x - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * v[e];
-    m = mn;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long add = s_total;
+    for (int w = 0; w < warp; ++w) add += s_warp[w];
+    if (b < a.n_seqs) prefix[b + 1] = x + add;
+    __syncthreads();
+    if (tid == NW * 32 - 1) s_total = x + add;
   }
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][32 * e + lane] = o[e];
+  fence_mbar_init();
   __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-  for (int w = 0; w < kThreads / 32; ++w) mm = fmaxf(mm, sm[w]);
-  for (int w = 0; w < kThreads / 32; ++w) ll += sl[w] > 0.f ? sl[w] * expf(sm[w] - mm) : 0.f;
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float y = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) y += sl[w] > 0.f ? so[w][d] * expf(sm[w] - mm) : 0.f;
-    out[((int64_t)t * q_heads + n) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(ll > 0.f ? y / ll : 0.f));
+  const long long W = prefix[a.n_seqs];
+
+  // rows of empty sequences
+  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+    const SeqInfo si = info[b];
+    if (si.qn <= 0 || seq_units(si) > 0) continue;
+    const int64_t r0 = (int64_t)si.q0 * g.q_heads, n = (int64_t)si.qn * g.q_heads;
+    for (int64_t i = tid; i < n * (D / 8); i += NW * 32) reinterpret_cast<uint4*>(g.out + r0 * D)[i] = make_uint4(0, 0, 0, 0);
+    if (g.lse)
+      for (int64_t i = tid; i < n; i += NW * 32) g.lse[r0 + i] = -INFINITY;
   }
-  if (lse && threadIdx.x == 0) lse[(int64_t)t * q_heads + n] = ll > 0.f ? mm + logf(ll) : -INFINITY;
+
+  // ---- this warp's run of units: CTAs beyond G would hold less than a unit per stream
+  const long long G = min((long long)gridDim.x, (W + KS - 1) / KS);
+  if (blockIdx.x >= G) return;
+  const long long N = G * KS, sidx = (long long)blockIdx.x * KS + stream;
+  const long long f_begin = sidx * W / N, f_end = (sidx + 1) * W / N;
+
+  // Position in the list of pairs: unit u of `units` of KV head h of sequence b.
+  int cb = 0, ch = 0, cu = 0, cunits = 0;
+  const int todo = (int)(f_end - f_begin);
+  if (todo > 0) {
+    int lo = 0, hi = a.n_seqs;                 // the last b with prefix[b] <= f_begin
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= f_begin) lo = mid;
+      else hi = mid;
+    }
+    cb = lo;
+    cunits = seq_units(info[lo]);
+    const long long rem = f_begin - prefix[lo];
+    ch = (int)(rem / cunits);
+    cu = (int)(rem - (long long)ch * cunits);
+  }
+  // to the next pair (there is one: units remain)
+  auto next_pair = [&](int& b, int& h, int& u, int& units) {
+    u = 0;
+    if (++h < Hkv) return;
+    h = 0;
+    do units = seq_units(info[++b]); while (units == 0);
+  };
+
+  // ---- producer: addresses of up to 16 units (32 sub-blocks, one a lane) at a time, the next batch's table entries
+  // fetched ahead. The state that only a change of batch needs is kept in shared memory.
+  Prod* pr = prods + warp;
+  const uint8_t* cur_ptr = nullptr;
+  int cur_n = 0, cur_subs = 0, next_id = 0;
+  auto fetch = [&]() {                         // describes the next batch and loads its table entries
+    Prod p = *pr;
+    __syncwarp();
+    if (p.n > 0) {                             // past the batch that was current
+      p.left -= p.n;
+      p.u += p.n;
+      if (p.u == p.units && p.left > 0) next_pair(p.b, p.h, p.u, p.units);
+    }
+    p.n = min(min(kBatch, p.units - p.u), p.left);
+    if (p.n > 0) {
+      const SeqInfo s = info[p.b];
+      const int sub = s.sub0 + p.u * kUnitSubs;
+      p.subs = min(p.n * kUnitSubs, (s.len + 15) / 16 - sub);
+      p.sub = sub;
+      if (lane < p.subs)
+        next_id = __ldg(a.block_table + (int64_t)p.b * a.table_stride + (sub + lane) / (a.page_tokens / 16));
+    }
+    if (lane == 0) {
+      pr->b = p.b; pr->h = p.h; pr->u = p.u; pr->units = p.units;
+      pr->left = p.left; pr->n = p.n; pr->subs = p.subs; pr->sub = p.sub;
+    }
+    __syncwarp();
+  };
+  auto take = [&]() {                          // makes the described batch the current one
+    const Prod p = *pr;
+    cur_n = p.n;
+    cur_subs = p.subs;
+    if (p.n > 0 && lane < p.subs) {
+      const int per_page = a.page_tokens / 16, sub = p.sub + lane;
+      bool ok;
+      const int id = check_page(a, next_id, ok);
+      cur_ptr = a.pages + (int64_t)id * a.page_stride + (int64_t)(p.h * per_page + sub % per_page) * S::BYTES;
+    }
+    __syncwarp();
+    fetch();
+  };
+  if (lane == 0) *pr = Prod{cb, ch, cu, cunits, todo, 0, 0, 0, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  __syncwarp();
+  fetch();
+  take();
+  int bi = 0, issued = 0, istage = 0;       // unit within the batch; units issued in all; stage of the next issue
+  auto issue = [&]() {                      // every lane of the warp has read what the stage held
+    if (issued >= todo) return;
+    const bool mine = (lane >> 1) == bi && lane < cur_subs;
+    if (mine && !(lane & 1)) mbar_arrive_expect_tx(bar + istage, (lane + 1 < cur_subs ? 2 : 1) * S::BYTES);
+    __syncwarp();
+    if (mine) bulk_g2s_plain(ring + istage * UNIT + (lane & 1) * S::BYTES, cur_ptr, S::BYTES, bar + istage);
+    ++issued;
+    if (++istage == stages) istage = 0;
+    if (++bi == cur_n) {
+      bi = 0;
+      take();
+    }
+  };
+  for (int i = 0; i < stages; ++i) issue();
+
+  // ---- consumer
+  uint32_t qf[NT][NB][4];
+  float ci[NT][NB][2], fx[NT][2], m[NT][2], l[NT][2], o[NT][NB][2][4];   // m: the maximum - 14
+  uint32_t vc[NVC];                          // E as the conversion of value scales takes it
+  int lim[NT][2];                            // a row sees keys below this
+  int seg_len = 0, min_lim = 0, key0 = 0;    // the pair's keys, what all rows see, the next unit's first key
+  const int wnd = g.window > 0 ? g.window : 0x3FFFFFFF;
+
+  auto set_ref = [&]() {
+    // minus (E + 127 - 15) per block, in its byte (MXFP4) or, shifted to bf16's exponent, in both halves (INT4); signed
+    // terms, so that an E near the smallest exponent works too
+    if (FMT == MOE_FMT_MXFP4) {
+      int low = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) low += (pr->ev_ref[b] + 112) * (1 << (8 * b));
+      if (NB == 2) low += low * 65536;
+      vc[0] = 0u - (uint32_t)low;
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) vc[b % NVC] = 0u - (uint32_t)((pr->ev_ref[b] + 112) * 0x00800080);
+    }
+  };
+  auto begin_segment = [&]() {
+    const SeqInfo si = info[cb];
+    seg_len = si.len;
+    min_lim = si.len - si.qn + 1;
+    key0 = (si.sub0 + cu * kUnitSubs) * 16;
+    if (lane < NB) {
+      pr->ev_run[lane] = -126;
+      pr->ev_ref[lane] = 2;      // scales up to 4
+    }
+    __syncwarp();
+    set_ref();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // B fragments: this lane holds row r of the 8 and dimensions 32 b + 8 c .. + 7
+      const int row = (rg * NT + nt) * 8 + r, j = row / g.group;
+      const bool valid = j < si.qn;
+      uint4 w[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        w[b] = valid ? __ldg(reinterpret_cast<const uint4*>(g.q + (int64_t)(si.q0 + j) * g.q_stride +
+                                                            (int64_t)(ch * g.group + row - j * g.group) * D + 32 * b + 8 * c))
+                     : make_uint4(0, 0, 0, 0);
+      float amax = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int sg = rescale_exponent(amax);
+      const float up = exp2i(sg);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(u[i] << 16) * up;
+          v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * up;
+        }
+        if (FMT == MOE_FMT_MXFP4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[nt][b][i] = pack_f16(v[2 * i], v[2 * i + 1]);
+        } else {
+          // pairs (i, i + 4); those that meet n 2^-20 carry 2^-4. The sum of what the fragments hold corrects the + 8.
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w4 = i & 1 ? 0.0625f : 1.f;
+            qf[nt][b][i] = pack_f16(v[i] * w4, v[i + 4] * w4);
+            const __half2 hh = *reinterpret_cast<const __half2*>(&qf[nt][b][i]);
+            sum += (__low2float(hh) + __high2float(hh)) * (i & 1 ? 16.f : 1.f);
+          }
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+          const float start = -8.f / kVal * sum;
+          ci[nt][b][0] = __shfl_sync(0xFFFFFFFFu, start, 8 * c);
+          ci[nt][b][1] = __shfl_sync(0xFFFFFFFFu, start, 8 * c + 4);
+        }
+      }
+      // accumulator columns: rows 2 c and 2 c + 1 of the 8
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int s_row = __shfl_sync(0xFFFFFFFFu, sg, 8 * c + 4 * e);
+        fx[nt][e] = g.scale_log2 * exp2i_neg(s_row) * kVal;
+        const int row_e = (rg * NT + nt) * 8 + 2 * c + e, je = row_e / g.group;
+        lim[nt][e] = je < si.qn ? si.len - si.qn + je + 1 : 0;
+        m[nt][e] = -FLT_MAX;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][b][x][e] = 0.f;
+    }
+  };
+
+  // Value scales of tokens 2 c, 2 c + 1 (u0) and 2 c + 8, 2 c + 9 (u1) times 2^-E as binary16 pairs. Exponents above E or
+  // below E - 7 show in `off` & kOff. Tokens whose bit of `drop` is set count as 2^E, whatever bytes they have.
+  constexpr uint32_t kOff = FMT == MOE_FMT_MXFP4 ? 0xF8F8F8F8u : 0xFC00FC00u;
+  auto scale_pairs = [&](const uint8_t* sb, uint32_t (&u0)[NB], uint32_t (&u1)[NB], uint32_t& off, uint32_t drop) {
+    const uint8_t* p = sb + S::VS + 2 * c * (NB * S::SB);
+    if (FMT == MOE_FMT_MXFP4) {
+      uint32_t wa[NB / 2], wb[NB / 2];   // NB = 4: a token each; NB = 2: two tokens
+      load_words<NB / 2>(wa, p);
+      load_words<NB / 2>(wb, p + 8 * NB);
+      if (drop) {
+        const uint32_t at_e = 0x0F0F0F0Fu - vc[0];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+          const uint32_t ka = NB == 4 ? 0u - ((drop >> i) & 1u) : ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
+          const uint32_t kb = NB == 4 ? 0u - ((drop >> (2 + i)) & 1u) : ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
+          wa[i] = (wa[i] & ~ka) | (at_e & ka);
+          wb[i] = (wb[i] & ~kb) | (at_e & kb);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i) {
+        wa[i] += vc[0];                  // bytes e - E + 15: 8 .. 15 in the window (8 bits: nothing aliases)
+        wb[i] += vc[0];
+        off |= (wa[i] ^ 0x08080808u) | (wb[i] ^ 0x08080808u);
+        wa[i] <<= 2;                     // the high byte of binary16's 2^(e - E)
+        wb[i] <<= 2;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        // bytes (the sign fill of a byte below 128: 0; token 2 c's; 0; token 2 c + 1's)
+        const int t = NB == 4 ? 4 + b : 2 + b;
+        const uint32_t sel = (8u | b) | (uint32_t)b << 4 | (8u | t) << 8 | (uint32_t)t << 12;
+        u0[b] = prmt(wa[0], wa[NB / 2 - 1], sel);
+        u1[b] = prmt(wb[0], wb[NB / 2 - 1], sel);
+      }
+    } else {
+      // bf16 and binary16 differ in the exponent's width and bias: (bits - ((E + 112) << 7)) << 3
+      uint32_t wa[NB], wb[NB];
+      load_words<NB>(wa, p);
+      load_words<NB>(wb, p + 16 * NB);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
+        u0[b] = prmt(wa[b / 2], wa[NB / 2 + b / 2], sel);
+        u1[b] = prmt(wb[b / 2], wb[NB / 2 + b / 2], sel);
+        if (drop) {
+          const uint32_t at_e = 0x07800780u - vc[b % NVC];
+          const uint32_t ka = ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
+          const uint32_t kb = ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
+          u0[b] = (u0[b] & ~ka) | (at_e & ka);
+          u1[b] = (u1[b] & ~kb) | (at_e & kb);
+        }
+        u0[b] += vc[b % NVC];            // exponents e - E + 15
+        u1[b] += vc[b % NVC];
+        off |= (u0[b] ^ 0x04000400u) | (u1[b] ^ 0x04000400u);
+        u0[b] <<= 3;
+        u1[b] <<= 3;
+      }
+    }
+  };
+
+  // The rare path: value scales outside E's window. Moves E to the largest, then adds the products of the weights s (times
+  // 2^14) and the scales in passes.
+  auto wide_products = [&](const uint8_t* base, const float (&s)[SUBS][NT][4]) {
+    float most[NB];              // (a weight of 0 has no product, whatever bytes its scale is)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) most[b] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < SUBS; ++i) {
+      float v0[NB], v1[NB];
+      load_scales<FMT, NB>(v0, base + i * S::BYTES + S::VS + r * (NB * S::SB));
+      load_scales<FMT, NB>(v1, base + i * S::BYTES + S::VS + (r + 8) * (NB * S::SB));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((SUBS == 1 || i == 0 ? s[0][nt][e] : s[SUBS - 1][nt][e]) > 0.f)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) most[b] = fmaxf(most[b], e & 2 ? v1[b] : v0[b]);
+    }
+    int depth = 3;               // passes after the first that the accumulators' range allows
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float vm = most[b];
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, i));
+      const int e_old = pr->ev_ref[b];
+      int run = pr->ev_run[b], e_new = e_old;
+      if (vm > 0.f) {
+        // Accumulators stay below 2^(38 + run - E) for a million keys: E at least run - 36 keeps two passes' 2^52 in range
+        const int ev = (int)(__float_as_uint(vm) >> 23) - 127;
+        run = max(run, ev);
+        e_new = max(ev, run - 36);   // (ev is -126 .. 127)
+      }
+      depth = min(depth, run - e_new <= 10 ? 3 : 2);
+      __syncwarp();
+      if (lane == 0) { pr->ev_run[b] = run; pr->ev_ref[b] = e_new; }
+      const float f1 = exp2i((e_old - e_new) >> 1), f2 = exp2i(e_old - e_new - ((e_old - e_new) >> 1));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][b][x][e] = o[nt][b][x][e] * f1 * f2;
+    }
+    __syncwarp();
+    set_ref();
+    for (int pass = 0;; ++pass) {
+      const float up = exp2i(kPassExp * pass), top = pass ? kNormal * exp2i(kPassExp) : FLT_MAX;
+      bool left = false;
+#pragma unroll 1
+      for (int i = 0; i < SUBS; ++i) {
+        const uint8_t* sb = base + i * S::BYTES;
+        uint32_t vw0[NB], vw1[NB];
+        float v0[NB], v1[NB];
+        load_words<NB>(vw0, sb + S::VC + (r * 4 + c) * (4 * NB));
+        load_words<NB>(vw1, sb + S::VC + (32 + r * 4 + c) * (4 * NB));
+        load_scales<FMT, NB>(v0, sb + S::VS + r * (NB * S::SB));
+        load_scales<FMT, NB>(v1, sb + S::VS + (r + 8) * (NB * S::SB));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float fr = exp2i(-pr->ev_ref[b]);
+          uint32_t f[2][4];
+          decode_v<FMT>(vw0[b], vw1[b], f);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = SUBS == 1 || i == 0 ? s[0][nt][e] : s[SUBS - 1][nt][e];
+              const float x = p == 0.f ? 0.f : p * ((e & 2 ? v1[b] : v0[b]) * fr) * up;
+              left |= x > 0.f && x < kNormal;
+              w[e] = x < kNormal || x >= top ? 0.f : x;      // (NaN stays)
+            }
+            const uint32_t p0 = transpose8(pack_f16(w[0], w[1])), p1 = transpose8(pack_f16(w[2], w[3]));
+            mma(o[nt][b][0], f[0], p0, p1);
+            mma(o[nt][b][1], f[1], p0, p1);
+          }
+        }
+      }
+      const bool again = pass < depth && __any_sync(0xFFFFFFFFu, left);
+      if (!again && pass == 0) return;
+      const float f = exp2i(again ? kPassExp : -kPassExp * pass);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][b][x][e] *= f;
+      if (!again) return;
+    }
+  };
+
+  // SUBS sub-blocks of 16 keys, from k0 on
+  auto process = [&](const uint8_t* base, int k0) {
+    float s[SUBS][NT][4];
+    uint32_t u0[SUBS][NB], u1[SUBS][NB], off = 0;
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      const uint8_t* sb = base + i * S::BYTES;
+      uint32_t kw0[NB], kw1[NB];
+      float ks0[NB], ks1[NB];
+      load_words<NB>(kw0, sb + S::KC + r * (D / 2) + c * (4 * NB));
+      load_words<NB>(kw1, sb + S::KC + (r + 8) * (D / 2) + c * (4 * NB));
+      load_scales<FMT, NB>(ks0, sb + S::KS + r * (NB * S::SB));
+      load_scales<FMT, NB>(ks1, sb + S::KS + (r + 8) * (NB * S::SB));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t f[2][4];
+        decode_k<FMT>(kw0[b], kw1[b], f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          if (FMT == MOE_FMT_INT4G32) { d[0] = d[2] = ci[nt][b][0]; d[1] = d[3] = ci[nt][b][1]; }
+          mma(d, f[0], qf[nt][b][0], qf[nt][b][1]);
+          mma(d, f[1], qf[nt][b][2], qf[nt][b][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ks = e & 2 ? ks1[b] : ks0[b];
+            s[i][nt][e] = b == 0 ? ks * d[e] : fmaf(ks, d[e], s[i][nt][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][nt][e] *= fx[nt][e & 1];
+      if (k0 + 16 * (i + 1) > min_lim || k0 + 16 * i < seg_len - wnd) {   // some row does not see some key
+        const int ka = k0 + 16 * i + r;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = e & 2 ? ka + 8 : ka, top = lim[nt][e & 1];
+            if (key >= top || key < top - wnd) s[i][nt][e] = -INFINITY;
+          }
+        // bytes past the end or before the window may be anything: their scales are replaced (their weights are 0)
+        const int kt = k0 + 16 * i + 2 * c, min_lo = min_lim - wnd;
+        uint32_t drop = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int key = kt + (t & 1) + (t & 2 ? 8 : 0);
+          drop |= (key >= seg_len || key < min_lo ? 1u : 0u) << t;
+        }
+        scale_pairs(sb, u0[i], u1[i], off, drop);
+      } else {
+        scale_pairs(sb, u0[i], u1[i], off, 0u);
+      }
+    }
+    float tmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        tmax = max3(max3(s[i][nt][0] - m[nt][0], s[i][nt][1] - m[nt][1], s[i][nt][2] - m[nt][0]), s[i][nt][3] - m[nt][1], tmax);
+    if (__any_sync(0xFFFFFFFFu, tmax > kPExp + kLazy)) {   // raise the maxima
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < SUBS; ++i) mx = max3(mx, s[i][nt][e], s[i][nt][e + 2]);
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, i));
+          mx = fmaxf(m[nt][e], mx - kPExp);
+          const float al = ex2(m[nt][e] - mx);
+          m[nt][e] = mx;
+          l[nt][e] *= al;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              o[nt][b][x][e] *= al;
+              o[nt][b][x][e + 2] *= al;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][nt][e] = ex2(s[i][nt][e] - m[nt][e & 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[nt][e] += s[i][nt][e] + s[i][nt][e + 2];
+      }
+    if (__any_sync(0xFFFFFFFFu, off & kOff)) {
+      wide_products(base, s);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      uint32_t vw0[NB], vw1[NB], t0[NT], t1[NT];
+      load_words<NB>(vw0, base + i * S::BYTES + S::VC + (r * 4 + c) * (4 * NB));
+      load_words<NB>(vw1, base + i * S::BYTES + S::VC + (32 + r * 4 + c) * (4 * NB));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        t0[nt] = transpose8(pack_f16(s[i][nt][0], s[i][nt][1]));
+        t1[nt] = transpose8(pack_f16(s[i][nt][2], s[i][nt][3]));
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t f[2][4];
+        decode_v<FMT>(vw0[b], vw1[b], f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t p0 = hmul2_bits(t0[nt], u0[i][b]), p1 = hmul2_bits(t1[nt], u1[i][b]);
+          mma(o[nt][b][0], f[0], p0, p1);
+          mma(o[nt][b][1], f[1], p0, p1);
+        }
+      }
+    }
+  };
+
+  // o (times 2^14, as l) in true scale relative to the maximum: dimensions 32 b + 4 r .. + 3 of row 2 c + e
+  auto value4 = [&](int nt, int e, int b) {
+    const float s = kVal * exp2i(pr->ev_ref[b]), s2 = FMT == MOE_FMT_INT4G32 ? s * 0.0625f : s;
+    return make_float4(o[nt][b][0][e] * s, o[nt][b][0][e + 2] * s2, o[nt][b][1][e] * s, o[nt][b][1][e + 2] * s2);
+  };
+  auto end_segment = [&](long long f0, long long f1, bool whole, bool last) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], i);
+    if (whole) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = (rg * NT + nt) * 8 + 2 * c + e, j = row / g.group;
+          if (j >= info[cb].qn) continue;
+          const int64_t at = (int64_t)(info[cb].q0 + j) * g.q_heads + ch * g.group + row - j * g.group;
+          const bool some = l[nt][e] > 0.f || l[nt][e] != l[nt][e];
+          const float inv = some ? 1.f / l[nt][e] : 0.f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const float4 v = value4(nt, e, b);
+            const __nv_bfloat162 p = some ? __floats2bfloat162_rn(v.x * inv, v.y * inv) : __floats2bfloat162_rn(0.f, 0.f);
+            const __nv_bfloat162 q = some ? __floats2bfloat162_rn(v.z * inv, v.w * inv) : __floats2bfloat162_rn(0.f, 0.f);
+            *reinterpret_cast<uint2*>(g.out + at * D + 32 * b + 4 * r) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+          }
+          if (g.lse && r == 0) g.lse[at] = some ? (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f : -INFINITY;
+        }
+      return;
+    }
+    // a part of the pair: in this warp's ring if the warp is done, else in the workspace
+    float* p = last ? reinterpret_cast<float*>(ring) : g.warp_parts + ((size_t)blockIdx.x * NW + warp) * PART;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = nt * 8 + 2 * c + e;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) *reinterpret_cast<float4*>(p + row * D + 32 * b + 4 * r) = value4(nt, e, b);
+        if (r == 0) {
+          p[ROWS * D + row] = m[nt][e];
+          p[ROWS * D + ROWS + row] = l[nt][e];
+        }
+      }
+    if (rg == 0 && lane == 0) s_entry[2 * stream + (last ? 1 : 0)] = Entry{f0, f1, cb * Hkv + ch, cb};
+  };
+
+  int stage = 0, phase = 0, seg_first = 0;
+  bool fresh = true;
+  for (int i = 0; i < todo; ++i) {
+    if (fresh) {
+      begin_segment();
+      seg_first = i;
+      fresh = false;
+    }
+    const bool ok = mbar_wait(bar + stage, phase, kDefaultWaitNs);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      // give up: record it, wait (again with a limit) for the copies that are under way, leave no part
+      if (lane == 0) record_error(a.status, MOE_ERR_DEVICE_TIMEOUT);
+      for (int k = i; k < issued; ++k) {
+        mbar_wait(bar + stage, phase, kDefaultWaitNs);
+        if (++stage == stages) { stage = 0; phase ^= 1; }
+      }
+      break;
+    }
+    const uint8_t* unit = ring + stage * UNIT;
+    process(unit, key0);
+    if (SUBS == 1 && key0 + 16 < seg_len) process(unit + S::BYTES, key0 + 16);
+    key0 += 16 * kUnitSubs;
+    __syncwarp();
+    issue();
+    if (++stage == stages) { stage = 0; phase ^= 1; }
+    const bool done = ++cu == cunits, last = i + 1 == todo;
+    if (done || last) {
+      end_segment(f_begin + seg_first, f_begin + i + 1, done && i + 1 - seg_first == cunits, last);
+      if (done && !last) {
+        next_pair(cb, ch, cu, cunits);
+        fresh = true;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- join the CTA's parts: entries in the order of the units, runs of one pair
+  if (warp == 0) {
+    Entry en;
+    en.seg = -1;
+    if (lane < 2 * KS) en = s_entry[lane];
+    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, en.seg >= 0);
+    const uint32_t before = valid & ((1u << lane) - 1u);
+    const int prev = __shfl_sync(0xFFFFFFFFu, en.seg, before ? 31 - __clz(before) : 0);
+    const bool lead = en.seg >= 0 && (!before || prev != en.seg);
+    const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead);
+    if (lane == 0) s_runs = __popc(leads);
+    if (lead) {
+      const uint32_t later = lane == 31 ? 0u : leads & ~((2u << lane) - 1u);
+      const uint32_t mine = valid & ~((1u << lane) - 1u) & (later ? ((1u << (__ffs(later) - 1)) - 1u) : 0xFFFFFFFFu);
+      const int last = 31 - __clz(mine);
+      Run ru;
+      ru.f0 = en.f0;
+      ru.f1 = s_entry[last].f1;
+      ru.first = lane;
+      ru.last = last;
+      ru.b = en.b;
+      ru.h = en.seg - en.b * Hkv;
+      const int units = seq_units(info[en.b]);
+      const long long p0 = prefix[en.b] + (long long)ru.h * units;
+      ru.whole = ru.f0 == p0 && ru.f1 == p0 + units;
+      ru.slot = ru.f0 == p0 ? 1 : 0;
+      s_run[__popc(leads & ((1u << lane) - 1u))] = ru;
+    }
+  }
+  if (tid < 2) s_last[tid] = -1;
+  __syncthreads();
+  const int rows_all = RG * ROWS, runs = s_runs;
+  const size_t cta_part = (size_t)rows_all * (D + 2);
+  for (int t = warp; t < runs * rows_all; t += NW) {
+    const Run ru = s_run[t / rows_all];
+    const int row = t % rows_all, j = row / g.group;
+    const SeqInfo sj = info[ru.b];
+    if (j >= sj.qn) continue;
+    const int w_rg = row / ROWS, w_row = row % ROWS;
+    auto part = [&](int e) -> const float* {
+      const int w = (e >> 1) * RG + w_rg;
+      return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)w * stages * UNIT)
+                   : g.warp_parts + ((size_t)blockIdx.x * NW + w) * PART;
+    };
+    Row<D> acc;
+    acc.clear();
+    acc.m = -FLT_MAX;
+    for (int e = ru.first; e <= ru.last; ++e)
+      if (s_entry[e].seg >= 0) {
+        const float pm = part(e)[ROWS * D + w_row];
+        acc.m = pm > acc.m || pm != pm ? pm : acc.m;
+      }
+    for (int e = ru.first; e <= ru.last; ++e)
+      if (s_entry[e].seg >= 0) {
+        const float* p = part(e);
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = p[w_row * D + E * lane + i];
+        acc.add(v, p[ROWS * D + w_row], p[ROWS * D + ROWS + w_row]);
+      }
+    if (ru.whole) {
+      acc.write(g, (int64_t)(sj.q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, lane);
+    } else {
+      float* p = g.cta_parts + ((size_t)blockIdx.x * 2 + ru.slot) * cta_part;
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[row * D + E * lane + i] = acc.o[i];
+      if (lane == 0) {
+        p[rows_all * D + row] = acc.m;
+        p[rows_all * D + rows_all + row] = acc.l;
+      }
+    }
+  }
+  __syncthreads();
+  // ---- a pair that spans CTAs: count its units; the CTA that completes the count joins the parts
+  if (tid < runs) {
+    const Run ru = s_run[tid];
+    if (!ru.whole) {
+      uint32_t* cnt = g.counters + ru.b * Hkv + ru.h;
+      const uint32_t n = (uint32_t)(ru.f1 - ru.f0);
+      if (atom_acq_rel_add(cnt, n) + n == (uint32_t)seq_units(info[ru.b])) {
+        *cnt = 0;
+        s_last[ru.slot] = tid;
+      }
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    if (s_last[k] < 0) continue;
+    const Run ru = s_run[s_last[k]];
+    const SeqInfo sj = info[ru.b];
+    const int units = seq_units(sj);
+    const long long p0 = prefix[ru.b] + (long long)ru.h * units;
+    const int c0 = (int)(((p0 + 1) * G - 1) / W), c1 = (int)(((p0 + units) * G - 1) / W);
+    auto part = [&](int i) { return g.cta_parts + ((size_t)i * 2 + ((long long)i * W / G > p0 ? 0 : 1)) * cta_part; };
+    for (int row = warp; row < rows_all; row += NW) {
+      const int j = row / g.group;
+      if (j >= sj.qn) continue;
+      Row<D> acc;
+      acc.clear();
+      float mx = -FLT_MAX;
+      for (int i = c0 + lane; i <= c1; i += 32) {
+        const float pm = __ldcg(part(i) + rows_all * D + row);
+        mx = pm > mx || pm != pm ? pm : mx;
+      }
+#pragma unroll
+      for (int i = 16; i; i >>= 1) {
+        const float y = __shfl_xor_sync(0xFFFFFFFFu, mx, i);
+        mx = y > mx || y != y ? y : mx;
+      }
+      acc.m = mx;
+#pragma unroll 4
+      for (int i = c0; i <= c1; ++i) {
+        const float* p = part(i);
+        float v[E];
+#pragma unroll
+        for (int x = 0; x < E; ++x) v[x] = __ldcg(p + row * D + E * lane + x);
+        acc.add(v, __ldcg(p + rows_all * D + row), __ldcg(p + rows_all * D + rows_all + row));
+      }
+      acc.write(g, (int64_t)(sj.q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, lane);
+    }
+  }
+}
+
+// Rows a warp holds and warps per CTA. 8 rows: 16 warps of 128 registers. More: 16 rows in 8 warps of up to 255
+// registers, as many warps on the same units as it takes.
+struct Shape { int nt, warps, row_groups; };
+static Shape shape_for(int rows) {
+  if (rows <= 8) return {1, 12, 1};
+  int rg = 1;
+  while (rg * 16 < rows) rg *= 2;
+  return {2, 8, rg};
+}
+
+static size_t meta_bytes(int n_seqs, int warps, int stages) {
+  return (size_t)warps * stages * 8 + (size_t)(n_seqs + 2) * 8 + (size_t)n_seqs * sizeof(SeqInfo) +
+         warps * sizeof(Prod);
+}
+
+template <int FMT, int D, int NT, int NW, int SUBS>
+static moe_status_t launch(const Args& a, AttnArgs g, int ctas, cudaStream_t stream) {
+  constexpr int unit = kUnitSubs * Sub<FMT, D>::BYTES;
+  // 4 KB are left for the kernel's fixed tables
+  int stages = 6;
+  while (stages > 1 && (size_t)NW * stages * unit + meta_bytes(a.n_seqs, NW, stages) > kSmemMax - 4096) --stages;
+  g.stages = stages;
+  const size_t smem = (size_t)NW * stages * unit + meta_bytes(a.n_seqs, NW, stages);
+  static int configured[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(attn_kernel<FMT, D, NT, NW, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 4096) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    configured[dev] = 1;
+  }
+  attn_kernel<FMT, D, NT, NW, SUBS><<<ctas, NW * 32, smem, stream>>>(a, g);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace kv
@@ -73,10 +1017,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(Args a, const uint16_t* 
 
 using namespace moe;
 
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 extern "C" size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t q_heads) {
   if (kv::check_cache(cache) != MOE_OK || kv::check_sizes(batch) != MOE_OK) return 0;
   if (q_heads < 1 || q_heads > 4096 || q_heads % cache->kv_heads) return 0;
-  return sizeof(WsHeader);
+  const int64_t rows = (int64_t)batch->max_q * (q_heads / cache->kv_heads);
+  if (batch->max_q > 8 || rows > kv::kMaxRows) return sizeof(WsHeader);   // append and read only
+  const kv::Shape s = kv::shape_for((int)rows);
+  const size_t row_bytes = (size_t)(cache->head_dim + 2) * 4;
+  return sizeof(WsHeader) + up256((size_t)batch->n_seqs * cache->kv_heads * 4) +
+         up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
 }
 
 extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
@@ -94,15 +1045,27 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
       q_stride < (int64_t)q_heads * cache->head_dim || window < 0)
     return MOE_ERR_SHAPE;
   if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;   // NaN or infinite
+  // units of 32 keys in all: a warp counts its share in 32 bits
+  if ((int64_t)batch->n_seqs * cache->kv_heads * ((int64_t)batch->table_stride * cache->page_tokens / 32 + 1) >= (int64_t)1 << 37)
+    return MOE_ERR_SHAPE;
   const size_t need = moe_kv_workspace_bytes(cache, batch, q_heads);
   if (need == 0 || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if ((st = moe_check_device()) != MOE_OK) return st;
   a.status = &((WsHeader*)ws)->status;
-  const dim3 grid(batch->n_tokens, q_heads);
-#define KV_CALL(F, DD)                                                                                                   \
-  kv::attn_kernel<F, DD><<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(a, (const uint16_t*)q, q_stride, q_heads, scale, \
-                                                                          window, (uint16_t*)out, lse)
+  const int group = q_heads / cache->kv_heads, rows = batch->max_q * group;
+  const kv::Shape s = kv::shape_for(rows);
+  uint8_t* w = (uint8_t*)ws + sizeof(WsHeader);
+  kv::AttnArgs g{(const uint16_t*)q, q_stride, q_heads, group, window, s.row_groups, 0, scale * 1.4426950408889634f,
+                 (uint16_t*)out, lse, (uint32_t*)w, nullptr, nullptr};
+  w += up256((size_t)batch->n_seqs * cache->kv_heads * 4);
+  g.warp_parts = (float*)w;
+  w += up256(kv::kMaxCtas * s.warps * 8 * s.nt * (size_t)(cache->head_dim + 2) * 4);
+  g.cta_parts = (float*)w;
+  const int ctas = moe_internal::num_sms() < kv::kMaxCtas ? moe_internal::num_sms() : kv::kMaxCtas;
+  if (ctas < 1) return MOE_ERR_CUDA;
+#define KV_CALL(F, DD)                                                                   \
+  return s.nt == 1 ? kv::launch<F, DD, 1, 12, 2>(a, g, ctas, (cudaStream_t)stream)        \
+                   : kv::launch<F, DD, 2, 8, 1>(a, g, ctas, (cudaStream_t)stream)
   KV_DISPATCH(KV_CALL);
 #undef KV_CALL
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
