@@ -8,9 +8,9 @@
 // dimensions) and half as many in the integer pipe. Everything below serves to convert a code with as few instructions
 // as possible, once per 8 query rows.
 //
-// Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, and the units are dealt out evenly: every
-// warp of the grid streams one contiguous run of them (the prefix sums over the sequences are formed by each CTA from
-// the device's lengths, so a captured graph follows them). A warp copies its units with bulk copies (one per 16-token
+// Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, a pair's start counting as one unit more
+// (what its queries and its output cost), and dealt out evenly: every warp of the grid streams one contiguous run (the
+// prefix sums over the sequences are formed by each CTA from the device's lengths, so a captured graph follows them). A warp copies its units with bulk copies (one per 16-token
 // sub-block, which the layout keeps contiguous) into its own ring and is its own consumer, so there is no barrier
 // between warps until the end. A pair that lies in several warps is joined from partial results, first inside the
 // CTA, then, if it spans CTAs, by the CTA that finishes last (a counter per pair, left at zero); always in the order of
@@ -26,12 +26,13 @@
 //   O^T += V^T P^T: the V layout puts an even and the following odd token's codes of one dimension side by side, which
 //     is what an A fragment's register holds. movmatrix turns the weights' accumulator layout into a B fragment. V's
 //     scales vary along the contraction, so they go into the weights: p_s vscale_s, rounded to binary16 once.
-//   Range: the weights are carried as 2^14 p, at most 2^15 (m is raised when a score passes m + 1), and the value
-//     scales as v 2^-E in binary16, exact within 2^-7 .. 1, with E per block of 32 dimensions the exponent of the largest
-//     scale; the fp32 accumulators hold 2^(14 - E) times the output. Products keep all 11 bits down to 2^-28 of the
-//     largest possible one. Where scales leave the window, E moves (accumulators rescaled, exactly) and the keys take
-//     passes: each adds the products of the next 26 powers of two at a scale of its own, so that no ratio of scales
-//     costs precision.
+//   Range: the weights are carried as 2^12 p, at most 2^14 (m is raised only when a score passes m + 2), and the value
+//     scales as v 2^-E in binary16, exact within 2^-14 .. 2^2, with an E per block of 32 dimensions; the fp32
+//     accumulators hold 2^(12 - E) times the output. Products keep all 11 bits down to 2^-14. Where scales leave the window, E moves
+//     (accumulators rescaled, exactly) and the keys take passes: each adds the products of the next 26 powers of two at a
+//     scale of its own, so that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has
+//     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a dimension whose few heavy keys all have code 0 is
+//     made of such weights.
 #include <cfloat>
 
 #include "kv.cuh"
@@ -42,15 +43,19 @@ namespace kv {
 constexpr int kUnitSubs = 2;        // sub-blocks per unit
 constexpr int kBatch = 16;          // units whose addresses a warp's lanes hold at a time
 constexpr int kSmemMax = 232448;
-constexpr int kPExp = 14;               // weights are carried times 2^14
-constexpr float kLazy = 1.f;            // a score may pass the running maximum by this (base 2)
+constexpr int kPExp = 12;               // weights are carried times 2^12
+constexpr float kLazy = 2.f;            // a score may pass the running maximum by this (base 2)
+constexpr int kEv0 = 2;                 // E at first: scales 2^-12 .. 2^4
 constexpr float kNormal = 6.103515625e-05f;   // 2^-14: binary16 products from here on keep all bits
 constexpr int kPassExp = 26;            // powers of two that a pass covers
+constexpr float kHeavy = 0.25f, kLight = 0.000244140625f;   // 2^12 times 2^-14 and 2^-24
 
 struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   int32_t q_heads, group, window, row_groups, stages;
+  uint32_t group_inv;               // floor(row / group) = row * group_inv >> 16 for rows below 128
+  int32_t rings;                    // bytes of the warps' rings; the tables follow
   float scale_log2;                 // scale * log2(e)
   uint16_t* out;
   float* lse;
@@ -58,6 +63,8 @@ struct AttnArgs {
   float* warp_parts;                // [CTAs][warps] partials of runs that end inside a warp's range
   float* cta_parts;                 // [CTAs][2]
 };
+
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }   // (keeps rare code out of the loop's lines)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -183,70 +190,60 @@ __device__ __forceinline__ int seq_units(const SeqInfo& s) {
   return s.qn > 0 && s.len > 0 ? ((s.len + 15) / 16 - s.sub0 + kUnitSubs - 1) / kUnitSubs : 0;
 }
 
+// A pair's place in the list of work: kPairCost, then its units.
+constexpr int kPairCost = 1;
+__device__ __forceinline__ int seq_cost(const SeqInfo& s) {
+  const int u = seq_units(s);
+  return u ? u + kPairCost : 0;
+}
+// x * W / n without 64-bit division where it is not needed
+__device__ __forceinline__ long long share(long long x, long long W, long long n) {
+  const unsigned long long p = (unsigned long long)x * W;
+  return p >> 32 ? (long long)(p / (unsigned long long)n) : (long long)((uint32_t)p / (uint32_t)n);
+}
+
 struct Prod {        // a warp's producer: the next batch is n units (subs sub-blocks from `sub` on) at unit u of a pair; left
   int b, h, u, units, left, n, subs, sub;   // counts the units from it on
   int ev_run[4];     // and of its consumer, per block: the largest value scale's exponent so far,
   int ev_ref[4];     // and the E in use
 };
 
-struct Entry {       // a partial result of one warp: flat units [f0, f1) of pair `seg`
-  long long f0, f1;
-  int seg, b;        // seg < 0: none
-};
-struct Run {         // consecutive entries of one pair
-  long long f0, f1;
-  int first, last, b, h, slot, whole;
-};
+struct Entry { int u0, u1, b, h; };   // a partial result of one warp: units [u0, u1) of pair (b, h); b < 0: none
+struct Run { int u0, u1, b, h, first, n, slot, whole; };      // n consecutive entries of one pair, from list place `first`
+struct Place { const float* p; int step, at; };   // an entry's values, floats from one row group's to the next's, its place
 
-// One query row's joined result: weighted sum of the parts, written out or stored as a part again.
+// A row's joined values of four dimensions, written out
 template <int D>
-struct Row {
-  static constexpr int E = D / 32;   // values a lane holds: dimensions E lane ..
-  float o[E], m, l;
-  __device__ void clear() {
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    l = 0.f;
-  }
-  __device__ void add(const float* po, float pm, float pl) {
-    const float w = ex2(pm - m);
-    l += w * pl;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += w * po[e];
-  }
-  __device__ void write(const AttnArgs& g, int64_t row, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const __nv_bfloat162 v = l > 0.f || l != l ? __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
-      w[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(g.out + row * D + E * lane);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
-    if (g.lse && lane == 0) g.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
-  }
-};
+__device__ __forceinline__ void write_row4(const AttnArgs& g, int64_t row, int d, float4 o, float m, float l) {
+  const bool some = l > 0.f || l != l;
+  const float inv = some ? 1.f / l : 0.f;
+  const __nv_bfloat162 p = some ? __floats2bfloat162_rn(o.x * inv, o.y * inv) : __floats2bfloat162_rn(0.f, 0.f);
+  const __nv_bfloat162 q = some ? __floats2bfloat162_rn(o.z * inv, o.w * inv) : __floats2bfloat162_rn(0.f, 0.f);
+  *reinterpret_cast<uint2*>(g.out + row * D + d) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+  if (g.lse && d == 0) g.lse[row] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
 
 template <int FMT, int D, int NT, int NW, int SUBS>
 __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   using S = Sub<FMT, D>;
-  constexpr int NB = S::NB, UNIT = kUnitSubs * S::BYTES, ROWS = 8 * NT, E = D / 32;
+  constexpr int NB = S::NB, UNIT = kUnitSubs * S::BYTES, ROWS = 8 * NT, THREADS = NW * 32;
   constexpr int PART = ROWS * (D + 2);                   // floats of a warp's partial: o [ROWS][D], m [ROWS], l [ROWS]
   constexpr int NVC = FMT == MOE_FMT_MXFP4 ? 1 : NB;
   constexpr float kVal = FMT == MOE_FMT_INT4G32 ? 16777216.f : 1.f;   // 2^24 of the INT4 fragments
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Entry s_entry[2 * NW];
   __shared__ Run s_run[2 * NW];
+  __shared__ Place s_place[2 * NW];
   __shared__ int s_runs, s_last[2];
+  __shared__ float s_wt[2 * NW * ROWS], s_m[2 * NW * ROWS], s_l[2 * NW * ROWS];   // [entry or run][row]
   __shared__ long long s_warp[NW], s_total;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   const int stages = g.stages, RG = g.row_groups, KS = NW / RG, Hkv = a.kv_heads;
   const int stream = warp / RG, rg = warp % RG;
   uint8_t* ring = smem + (size_t)warp * stages * UNIT;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)NW * stages * UNIT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + g.rings);
   uint64_t* bar = bars + warp * stages;
   long long* prefix = reinterpret_cast<long long*>(bars + NW * stages);           // [n_seqs + 1]
   SeqInfo* info = reinterpret_cast<SeqInfo*>(prefix + a.n_seqs + 1 + ((a.n_seqs + 1) & 1));
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 
   // ---- the sequences: lengths, first visible sub-block, prefix sums of their units over all KV heads
   if (lane < stages) mbar_init(bar + lane, 1);
-  if (tid < 2 * NW) s_entry[tid].seg = -1;
+  if (tid < 2 * NW) s_entry[tid].b = -1;
   if (tid == 0) { prefix[0] = 0; s_total = 0; }
   for (int base = 0; base < a.n_seqs; base += NW * 32) {
     const int b = base + tid;
@@ -264,7 +261,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       SeqInfo si{sq.q0, sq.qn, sq.len, 0};
       if (g.window > 0 && sq.len - sq.qn - g.window + 1 > 0) si.sub0 = (sq.len - sq.qn - g.window + 1) / 16;
       info[b] = si;
-      x = (long long)seq_units(si) * Hkv;
+      x = (long long)seq_cost(si) * Hkv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -293,16 +290,20 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       for (int64_t i = tid; i < n; i += NW * 32) g.lse[r0 + i] = -INFINITY;
   }
 
-  // ---- this warp's run of units: CTAs beyond G would hold less than a unit per stream
-  const long long G = min((long long)gridDim.x, (W + KS - 1) / KS);
+  // ---- this warp's run [f_begin, f_end) of the list
+  if (W == 0) return;
+  // G: about two units a stream at least; where that leaves SMs over, a multiple of the pairs, so that a pair of an even
+  // batch ends where a CTA does (a pair within one CTA needs no join across CTAs, 3 us)
+  const long long pairs = (long long)a.n_seqs * Hkv, even = (W + 2 * KS * pairs - 1) / (2 * KS * pairs) * pairs;
+  const int G = (int)min(even, (long long)gridDim.x);
+  const int N = G * KS;
   if (blockIdx.x >= G) return;
-  const long long N = G * KS, sidx = (long long)blockIdx.x * KS + stream;
-  const long long f_begin = sidx * W / N, f_end = (sidx + 1) * W / N;
+  const int sidx = blockIdx.x * KS + stream;
+  const long long f_begin = share(sidx, W, N), f_end = share(sidx + 1, W, N);
 
-  // Position in the list of pairs: unit u of `units` of KV head h of sequence b.
-  int cb = 0, ch = 0, cu = 0, cunits = 0;
-  const int todo = (int)(f_end - f_begin);
-  if (todo > 0) {
+  // The unit u of `units` of KV head h of sequence b that the run starts with, and how many units it holds.
+  int cb = 0, ch = 0, cu = 0, cunits = 0, todo = 0;
+  if (f_begin < f_end) {
     int lo = 0, hi = a.n_seqs;                 // the last b with prefix[b] <= f_begin
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -311,9 +312,29 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
     cb = lo;
     cunits = seq_units(info[lo]);
+    const int cost = cunits + kPairCost;
     const long long rem = f_begin - prefix[lo];
-    ch = (int)(rem / cunits);
-    cu = (int)(rem - (long long)ch * cunits);
+    ch = (int)share(rem, 1, cost);
+    int at = (int)(rem - (long long)ch * cost);            // 0 .. cost - 1: the pair's start, or its unit at - kPairCost
+    cu = max(0, at - kPairCost);
+    // units in [f_begin, f_end): all but the pair starts; counted pair by pair, in one step within a sequence
+    long long left = f_end - f_begin;
+    for (int b = lo, h = ch, units = cunits; left > 0;) {
+      const int here = (int)min(left, (long long)(units + kPairCost - at));
+      todo += max(0, at + here - max(at, kPairCost));
+      left -= here;
+      at = 0;
+      if (++h < Hkv) {
+        const int n = (int)min(share(left, 1, units + kPairCost), (long long)(Hkv - h));
+        todo += n * units;
+        left -= (long long)n * (units + kPairCost);
+        h += n;
+      }
+      if (h == Hkv && left > 0) {
+        h = 0;
+        do units = seq_units(info[++b]); while (units == 0);
+      }
+    }
   }
   // to the next pair (there is one: units remain)
   auto next_pair = [&](int& b, int& h, int& u, int& units) {
@@ -367,7 +388,6 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   if (lane == 0) *pr = Prod{cb, ch, cu, cunits, todo, 0, 0, 0, {0, 0, 0, 0}, {0, 0, 0, 0}};
   __syncwarp();
   fetch();
-  take();
   int bi = 0, issued = 0, istage = 0;       // unit within the batch; units issued in all; stage of the next issue
   auto issue = [&]() {                      // every lane of the warp has read what the stage held
     if (issued >= todo) return;
@@ -382,28 +402,42 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       take();
     }
   };
-  for (int i = 0; i < stages; ++i) issue();
 
   // ---- consumer
   uint32_t qf[NT][NB][4];
-  float ci[NT][NB][2], fx[NT][2], m[NT][2], l[NT][2], o[NT][NB][2][4];   // m: the maximum - 14
+  float ci[NT][NB][2], fx[NT][2], m[NT][2], l[NT][2], o[NT][NB][2][4];   // m: the maximum - 12
   uint32_t vc[NVC];                          // E as the conversion of value scales takes it
+  bool settled = false;                      // each row has had 12 keys of some weight (see above);
+  int heavy = 0;                             // their counts until then, a byte a row
   int lim[NT][2];                            // a row sees keys below this
   int seg_len = 0, min_lim = 0, key0 = 0;    // the pair's keys, what all rows see, the next unit's first key
   const int wnd = g.window > 0 ? g.window : 0x3FFFFFFF;
 
   auto set_ref = [&]() {
-    // minus (E + 127 - 15) per block, in its byte (MXFP4) or, shifted to bf16's exponent, in both halves (INT4); signed
-    // terms, so that an E near the smallest exponent works too
+    // minus the exponent of the window's lower end, E + 127 - 14, per block: in its byte (MXFP4) or at bf16's exponent's
+    // place in both halves (INT4). Signed terms, so that an E near the smallest exponent works too.
     if (FMT == MOE_FMT_MXFP4) {
       int low = 0;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) low += (pr->ev_ref[b] + 112) * (1 << (8 * b));
+      for (int b = 0; b < NB; ++b) low += (pr->ev_ref[b] + 113) * (1 << (8 * b));
       if (NB == 2) low += low * 65536;
       vc[0] = 0u - (uint32_t)low;
     } else {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) vc[b % NVC] = 0u - (uint32_t)((pr->ev_ref[b] + 112) * 0x00800080);
+      for (int b = 0; b < NB; ++b) vc[b % NVC] = 0u - (uint32_t)((pr->ev_ref[b] + 113) * 0x00800080);
+    }
+  };
+  // B fragments: this lane holds row r of the 8 and dimensions 32 b + 8 c .. + 7
+  uint4 qw[NT][NB];
+  auto load_q = [&]() {
+    const int q0 = info[cb].q0, qn = info[cb].qn;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = (rg * NT + nt) * 8 + r, j = (int)((uint32_t)row * g.group_inv >> 16);
+      const uint16_t* p = g.q + (int64_t)(q0 + j) * g.q_stride + (int64_t)(ch * g.group + row - j * g.group) * D + 8 * c;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        qw[nt][b] = j < qn ? __ldg(reinterpret_cast<const uint4*>(p + 32 * b)) : make_uint4(0, 0, 0, 0);
     }
   };
   auto begin_segment = [&]() {
@@ -413,25 +447,18 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     key0 = (si.sub0 + cu * kUnitSubs) * 16;
     if (lane < NB) {
       pr->ev_run[lane] = -126;
-      pr->ev_ref[lane] = 2;      // scales up to 4
+      pr->ev_ref[lane] = kEv0;
     }
     __syncwarp();
     set_ref();
+    settled = false;
+    heavy = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // B fragments: this lane holds row r of the 8 and dimensions 32 b + 8 c .. + 7
-      const int row = (rg * NT + nt) * 8 + r, j = row / g.group;
-      const bool valid = j < si.qn;
-      uint4 w[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        w[b] = valid ? __ldg(reinterpret_cast<const uint4*>(g.q + (int64_t)(si.q0 + j) * g.q_stride +
-                                                            (int64_t)(ch * g.group + row - j * g.group) * D + 32 * b + 8 * c))
-                     : make_uint4(0, 0, 0, 0);
       float amax = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+        const uint32_t u[4] = {qw[nt][b].x, qw[nt][b].y, qw[nt][b].z, qw[nt][b].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       const float up = exp2i(sg);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+        const uint32_t u[4] = {qw[nt][b].x, qw[nt][b].y, qw[nt][b].z, qw[nt][b].w};
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -474,7 +501,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       for (int e = 0; e < 2; ++e) {
         const int s_row = __shfl_sync(0xFFFFFFFFu, sg, 8 * c + 4 * e);
         fx[nt][e] = g.scale_log2 * exp2i_neg(s_row) * kVal;
-        const int row_e = (rg * NT + nt) * 8 + 2 * c + e, je = row_e / g.group;
+        const int row_e = (rg * NT + nt) * 8 + 2 * c + e, je = (int)((uint32_t)row_e * g.group_inv >> 16);
         lim[nt][e] = je < si.qn ? si.len - si.qn + je + 1 : 0;
         m[nt][e] = -FLT_MAX;
         l[nt][e] = 0.f;
@@ -488,9 +515,9 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
   };
 
-  // Value scales of tokens 2 c, 2 c + 1 (u0) and 2 c + 8, 2 c + 9 (u1) times 2^-E as binary16 pairs. Exponents above E or
-  // below E - 7 show in `off` & kOff. Tokens whose bit of `drop` is set count as 2^E, whatever bytes they have.
-  constexpr uint32_t kOff = FMT == MOE_FMT_MXFP4 ? 0xF8F8F8F8u : 0xFC00FC00u;
+  // Value scales of tokens 2 c, 2 c + 1 (u0) and 2 c + 8, 2 c + 9 (u1) times 2^-E as binary16 pairs. Exponents outside
+  // E - 14 .. E + 1 show in `off` & kOff. Tokens whose bit of `drop` is set count as 2^-14, whatever bytes they have.
+  constexpr uint32_t kOff = FMT == MOE_FMT_MXFP4 ? 0xF0F0F0F0u : 0xF800F800u;
   auto scale_pairs = [&](const uint8_t* sb, uint32_t (&u0)[NB], uint32_t (&u1)[NB], uint32_t& off, uint32_t drop) {
     const uint8_t* p = sb + S::VS + 2 * c * (NB * S::SB);
     if (FMT == MOE_FMT_MXFP4) {
@@ -498,22 +525,23 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       load_words<NB / 2>(wa, p);
       load_words<NB / 2>(wb, p + 8 * NB);
       if (drop) {
-        const uint32_t at_e = 0x0F0F0F0Fu - vc[0];
+        const uint32_t low = 0u - vc[0];
 #pragma unroll
         for (int i = 0; i < NB / 2; ++i) {
           const uint32_t ka = NB == 4 ? 0u - ((drop >> i) & 1u) : ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
           const uint32_t kb = NB == 4 ? 0u - ((drop >> (2 + i)) & 1u) : ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
-          wa[i] = (wa[i] & ~ka) | (at_e & ka);
-          wb[i] = (wb[i] & ~kb) | (at_e & kb);
+          wa[i] = (wa[i] & ~ka) | (low & ka);
+          wb[i] = (wb[i] & ~kb) | (low & kb);
         }
       }
+      const uint32_t vc4 = vc[0] * 4u + 0x04040404u;
 #pragma unroll
       for (int i = 0; i < NB / 2; ++i) {
-        wa[i] += vc[0];                  // bytes e - E + 15: 8 .. 15 in the window (8 bits: nothing aliases)
-        wb[i] += vc[0];
-        off |= (wa[i] ^ 0x08080808u) | (wb[i] ^ 0x08080808u);
-        wa[i] <<= 2;                     // the high byte of binary16's 2^(e - E)
-        wb[i] <<= 2;
+        // bytes e - E + 14: 0 .. 15 in the window (8 bits: nothing aliases; a borrow comes from a byte that shows itself).
+        // 4 (that + 1) is the high byte of binary16's 2^(e - E).
+        off |= (wa[i] + vc[0]) | (wb[i] + vc[0]);
+        wa[i] = wa[i] * 4u + vc4;
+        wb[i] = wb[i] * 4u + vc4;
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -524,7 +552,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
         u1[b] = prmt(wb[0], wb[NB / 2 - 1], sel);
       }
     } else {
-      // bf16 and binary16 differ in the exponent's width and bias: (bits - ((E + 112) << 7)) << 3
+      // bf16 and binary16 differ in the exponent's width and bias: (bits - ((E + 113) << 7) + (1 << 7)) << 3
       uint32_t wa[NB], wb[NB];
       load_words<NB>(wa, p);
       load_words<NB>(wb, p + 16 * NB);
@@ -534,23 +562,21 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
         u0[b] = prmt(wa[b / 2], wa[NB / 2 + b / 2], sel);
         u1[b] = prmt(wb[b / 2], wb[NB / 2 + b / 2], sel);
         if (drop) {
-          const uint32_t at_e = 0x07800780u - vc[b % NVC];
+          const uint32_t low = 0u - vc[b % NVC];
           const uint32_t ka = ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
           const uint32_t kb = ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
-          u0[b] = (u0[b] & ~ka) | (at_e & ka);
-          u1[b] = (u1[b] & ~kb) | (at_e & kb);
+          u0[b] = (u0[b] & ~ka) | (low & ka);
+          u1[b] = (u1[b] & ~kb) | (low & kb);
         }
-        u0[b] += vc[b % NVC];            // exponents e - E + 15
-        u1[b] += vc[b % NVC];
-        off |= (u0[b] ^ 0x04000400u) | (u1[b] ^ 0x04000400u);
-        u0[b] <<= 3;
-        u1[b] <<= 3;
+        off |= (u0[b] + vc[b % NVC]) | (u1[b] + vc[b % NVC]);
+        u0[b] = u0[b] * 8u + (vc[b % NVC] * 8u + 0x04000400u);
+        u1[b] = u1[b] * 8u + (vc[b % NVC] * 8u + 0x04000400u);
       }
     }
   };
 
   // The rare path: value scales outside E's window. Moves E to the largest, then adds the products of the weights s (times
-  // 2^14) and the scales in passes.
+  // 2^12) and the scales in passes.
   auto wide_products = [&](const uint8_t* base, const float (&s)[SUBS][NT][4]) {
     float most[NB];              // (a weight of 0 has no product, whatever bytes its scale is)
 #pragma unroll
@@ -581,7 +607,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
         // Accumulators stay below 2^(38 + run - E) for a million keys: E at least run - 36 keeps two passes' 2^52 in range
         const int ev = (int)(__float_as_uint(vm) >> 23) - 127;
         run = max(run, ev);
-        e_new = max(ev, run - 36);   // (ev is -126 .. 127)
+        e_new = max(ev <= e_old + 1 && ev >= e_old - 10 ? e_old : ev, run - 36);   // (ev is -126 .. 127)
       }
       depth = min(depth, run - e_new <= 10 ? 3 : 2);
       __syncwarp();
@@ -644,6 +670,11 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
   };
 
+  // the first copies, with the first queries' loads on the way
+  if (todo > 0) load_q();
+  take();
+  for (int i = 0; i < stages; ++i) issue();
+
   // SUBS sub-blocks of 16 keys, from k0 on
   auto process = [&](const uint8_t* base, int k0) {
     float s[SUBS][NT][4];
@@ -678,7 +709,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[i][nt][e] *= fx[nt][e & 1];
-      if (k0 + 16 * (i + 1) > min_lim || k0 + 16 * i < seg_len - wnd) {   // some row does not see some key
+      if (rarely(k0 + 16 * (i + 1) > min_lim || k0 + 16 * i < seg_len - wnd)) {   // some row does not see some key
         const int ka = k0 + 16 * i + r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -706,7 +737,9 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         tmax = max3(max3(s[i][nt][0] - m[nt][0], s[i][nt][1] - m[nt][1], s[i][nt][2] - m[nt][0]), s[i][nt][3] - m[nt][1], tmax);
-    if (__any_sync(0xFFFFFFFFu, tmax > kPExp + kLazy)) {   // raise the maxima
+    if (rarely(__any_sync(0xFFFFFFFFu, tmax > kPExp + kLazy))) {   // raise the maxima
+      settled = false;
+      heavy = heavy >> 1 & 0x7F7F7F7F;   // (some of the keys that counted no longer do; none after a large step)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -718,6 +751,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
           for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, i));
           mx = fmaxf(m[nt][e], mx - kPExp);
           const float al = ex2(m[nt][e] - mx);
+          if (al < 0.0625f) heavy &= ~(255 << (8 * (2 * nt + e)));
           m[nt][e] = mx;
           l[nt][e] *= al;
 #pragma unroll
@@ -738,7 +772,33 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) l[nt][e] += s[i][nt][e] + s[i][nt][e + 2];
       }
-    if (__any_sync(0xFFFFFFFFu, off & kOff)) {
+    bool wide = off & kOff;
+    if (rarely(!settled)) {
+      // keys of weight 2^-14 and more per row, four counts in an int, over the lanes that share the rows
+      int n = 0;
+      bool light = false;
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            n += (s[i][nt][e] >= kHeavy ? 1 : 0) << (8 * (2 * nt + (e & 1)));
+            light |= s[i][nt][e] > 0.f && s[i][nt][e] < kLight;
+          }
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, i);
+      bool all = true;
+#pragma unroll
+      for (int k = 0; k < 2 * NT; ++k) {
+        const int sum = min(128, (heavy >> (8 * k) & 255) + (n >> (8 * k) & 255));
+        heavy = (heavy & ~(255 << (8 * k))) | sum << (8 * k);
+        all = all && (sum >= 12 || lim[k / 2][k % 2] == 0);
+      }
+      settled = __all_sync(0xFFFFFFFFu, all);
+      wide |= light && !settled;
+    }
+    if (rarely(__any_sync(0xFFFFFFFFu, wide))) {
       wide_products(base, s);
       return;
     }
@@ -766,37 +826,29 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
   };
 
-  // o (times 2^14, as l) in true scale relative to the maximum: dimensions 32 b + 4 r .. + 3 of row 2 c + e
+  // o (times 2^12, as l) in true scale relative to the maximum: dimensions 32 b + 4 r .. + 3 of row 2 c + e
   auto value4 = [&](int nt, int e, int b) {
     const float s = kVal * exp2i(pr->ev_ref[b]), s2 = FMT == MOE_FMT_INT4G32 ? s * 0.0625f : s;
     return make_float4(o[nt][b][0][e] * s, o[nt][b][0][e + 2] * s2, o[nt][b][1][e] * s, o[nt][b][1][e + 2] * s2);
   };
-  auto end_segment = [&](long long f0, long long f1, bool whole, bool last) {
+  auto end_segment = [&](int u0, int u1, bool last) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], i);
-    if (whole) {
+    if (u0 == 0 && u1 == cunits) {
+      const int q0 = info[cb].q0, qn = info[cb].qn;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = (rg * NT + nt) * 8 + 2 * c + e, j = row / g.group;
-          if (j >= info[cb].qn) continue;
-          const int64_t at = (int64_t)(info[cb].q0 + j) * g.q_heads + ch * g.group + row - j * g.group;
-          const bool some = l[nt][e] > 0.f || l[nt][e] != l[nt][e];
-          const float inv = some ? 1.f / l[nt][e] : 0.f;
+          const int row = (rg * NT + nt) * 8 + 2 * c + e, j = (int)((uint32_t)row * g.group_inv >> 16);
+          if (j >= qn) continue;
+          const int64_t at = (int64_t)(q0 + j) * g.q_heads + ch * g.group + row - j * g.group;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const float4 v = value4(nt, e, b);
-            const __nv_bfloat162 p = some ? __floats2bfloat162_rn(v.x * inv, v.y * inv) : __floats2bfloat162_rn(0.f, 0.f);
-            const __nv_bfloat162 q = some ? __floats2bfloat162_rn(v.z * inv, v.w * inv) : __floats2bfloat162_rn(0.f, 0.f);
-            *reinterpret_cast<uint2*>(g.out + at * D + 32 * b + 4 * r) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-          }
-          if (g.lse && r == 0) g.lse[at] = some ? (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f : -INFINITY;
+          for (int b = 0; b < NB; ++b) write_row4<D>(g, at, 32 * b + 4 * r, value4(nt, e, b), m[nt][e], l[nt][e]);
         }
       return;
     }
@@ -810,19 +862,21 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) *reinterpret_cast<float4*>(p + row * D + 32 * b + 4 * r) = value4(nt, e, b);
         if (r == 0) {
-          p[ROWS * D + row] = m[nt][e];
-          p[ROWS * D + ROWS + row] = l[nt][e];
+          const int at = (2 * stream + (last ? 1 : 0)) * (RG * ROWS) + rg * ROWS + row;
+          s_m[at] = m[nt][e];
+          s_l[at] = l[nt][e];
         }
       }
-    if (rg == 0 && lane == 0) s_entry[2 * stream + (last ? 1 : 0)] = Entry{f0, f1, cb * Hkv + ch, cb};
+    if (rg == 0 && lane == 0) s_entry[2 * stream + (last ? 1 : 0)] = Entry{u0, u1, cb, ch};
   };
 
-  int stage = 0, phase = 0, seg_first = 0;
+  int stage = 0, phase = 0, seg_u0 = 0;
   bool fresh = true;
   for (int i = 0; i < todo; ++i) {
     if (fresh) {
+      if (i > 0) load_q();
       begin_segment();
-      seg_first = i;
+      seg_u0 = cu;
       fresh = false;
     }
     const bool ok = mbar_wait(bar + stage, phase, kDefaultWaitNs);
@@ -836,15 +890,16 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       break;
     }
     const uint8_t* unit = ring + stage * UNIT;
-    process(unit, key0);
-    if (SUBS == 1 && key0 + 16 < seg_len) process(unit + S::BYTES, key0 + 16);
+#pragma unroll 1
+    for (int k = 0; k < kUnitSubs; k += SUBS)
+      if (key0 + 16 * k < seg_len) process(unit + k * S::BYTES, key0 + 16 * k);
     key0 += 16 * kUnitSubs;
     __syncwarp();
     issue();
     if (++stage == stages) { stage = 0; phase ^= 1; }
     const bool done = ++cu == cunits, last = i + 1 == todo;
     if (done || last) {
-      end_segment(f_begin + seg_first, f_begin + i + 1, done && i + 1 - seg_first == cunits, last);
+      end_segment(seg_u0, cu, last);
       if (done && !last) {
         next_pair(cb, ch, cu, cunits);
         fresh = true;
@@ -854,74 +909,77 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   __syncthreads();
 
   // ---- join the CTA's parts: entries in the order of the units, runs of one pair
+  const int rows_all = RG * ROWS, row_bits = 31 - __clz(rows_all);   // (a power of two)
+  auto token_of = [&](int row) { return (int)((uint32_t)row * g.group_inv >> 16); };
   if (warp == 0) {
-    Entry en;
-    en.seg = -1;
+    Entry en{0, 0, -1, 0};
     if (lane < 2 * KS) en = s_entry[lane];
-    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, en.seg >= 0);
-    const uint32_t before = valid & ((1u << lane) - 1u);
-    const int prev = __shfl_sync(0xFFFFFFFFu, en.seg, before ? 31 - __clz(before) : 0);
-    const bool lead = en.seg >= 0 && (!before || prev != en.seg);
-    const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead);
-    if (lane == 0) s_runs = __popc(leads);
-    if (lead) {
-      const uint32_t later = lane == 31 ? 0u : leads & ~((2u << lane) - 1u);
-      const uint32_t mine = valid & ~((1u << lane) - 1u) & (later ? ((1u << (__ffs(later) - 1)) - 1u) : 0xFFFFFFFFu);
-      const int last = 31 - __clz(mine);
-      Run ru;
-      ru.f0 = en.f0;
-      ru.f1 = s_entry[last].f1;
-      ru.first = lane;
-      ru.last = last;
-      ru.b = en.b;
-      ru.h = en.seg - en.b * Hkv;
-      const int units = seq_units(info[en.b]);
-      const long long p0 = prefix[en.b] + (long long)ru.h * units;
-      ru.whole = ru.f0 == p0 && ru.f1 == p0 + units;
-      ru.slot = ru.f0 == p0 ? 1 : 0;
-      s_run[__popc(leads & ((1u << lane) - 1u))] = ru;
+    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, en.b >= 0), below = (1u << lane) - 1u;
+    const int before = valid & below ? 31 - __clz(valid & below) : 0;
+    const int pb = __shfl_sync(0xFFFFFFFFu, en.b, before), ph = __shfl_sync(0xFFFFFFFFu, en.h, before);
+    const bool lead = en.b >= 0 && (!(valid & below) || pb != en.b || ph != en.h);
+    const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead), later = leads & ~below & ~(1u << lane);
+    const uint32_t mine = valid & ~below & (later ? (1u << (__ffs(later) - 1)) - 1u : 0xFFFFFFFFu);
+    const int u1 = __shfl_sync(0xFFFFFFFFu, en.u1, mine ? 31 - __clz(mine) : 0), place = __popc(valid & below);
+    if (lane == 0) {
+      s_runs = __popc(leads);
+      s_last[0] = s_last[1] = -1;
     }
+    if (en.b >= 0) {
+      const int w = (lane >> 1) * RG;
+      s_place[place] = lane & 1 ? Place{reinterpret_cast<const float*>(smem + (size_t)w * stages * UNIT), stages * UNIT / 4, lane}
+                                : Place{g.warp_parts + ((size_t)blockIdx.x * NW + w) * PART, PART, lane};
+    }
+    if (lead)
+      s_run[__popc(leads & below)] =
+          Run{en.u0, u1, en.b, en.h, place, __popc(mine), en.u0 == 0 ? 1 : 0, en.u0 == 0 && u1 == seq_units(info[en.b]) ? 1 : 0};
   }
-  if (tid < 2) s_last[tid] = -1;
   __syncthreads();
-  const int rows_all = RG * ROWS, runs = s_runs;
+  const int runs = s_runs;
+  // each entry's weight 2^(m_e - m) per row, and each run's m and l (over its first entry's)
+  for (int t = tid; t < runs << row_bits; t += THREADS) {
+    const int row = t & (rows_all - 1), first = s_run[t >> row_bits].first, n = s_run[t >> row_bits].n;
+    float mx = -FLT_MAX, sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float x = s_m[s_place[first + i].at * rows_all + row];
+      mx = x > mx || x != x ? x : mx;
+    }
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int at = s_place[first + i].at * rows_all + row;
+      const float w = ex2(s_m[at] - mx);
+      sum += w * s_l[at];
+      s_wt[(first + i) * rows_all + row] = w;
+    }
+    const int at = s_place[first].at * rows_all + row;
+    s_m[at] = mx;
+    s_l[at] = sum;
+  }
+  __syncthreads();
   const size_t cta_part = (size_t)rows_all * (D + 2);
-  for (int t = warp; t < runs * rows_all; t += NW) {
-    const Run ru = s_run[t / rows_all];
-    const int row = t % rows_all, j = row / g.group;
-    const SeqInfo sj = info[ru.b];
-    if (j >= sj.qn) continue;
-    const int w_rg = row / ROWS, w_row = row % ROWS;
-    auto part = [&](int e) -> const float* {
-      const int w = (e >> 1) * RG + w_rg;
-      return e & 1 ? reinterpret_cast<const float*>(smem + (size_t)w * stages * UNIT)
-                   : g.warp_parts + ((size_t)blockIdx.x * NW + w) * PART;
-    };
-    Row<D> acc;
-    acc.clear();
-    acc.m = -FLT_MAX;
-    for (int e = ru.first; e <= ru.last; ++e)
-      if (s_entry[e].seg >= 0) {
-        const float pm = part(e)[ROWS * D + w_row];
-        acc.m = pm > acc.m || pm != pm ? pm : acc.m;
-      }
-    for (int e = ru.first; e <= ru.last; ++e)
-      if (s_entry[e].seg >= 0) {
-        const float* p = part(e);
-        float v[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = p[w_row * D + E * lane + i];
-        acc.add(v, p[ROWS * D + w_row], p[ROWS * D + ROWS + w_row]);
-      }
+  for (int t = tid; t < (runs << row_bits) * (D / 4); t += THREADS) {
+    const int d = t % (D / 4) * 4, row = t / (D / 4) & (rows_all - 1);
+    const Run ru = s_run[t / (D / 4) >> row_bits];
+    const int j = token_of(row), w_rg = row / ROWS, at = (row % ROWS) * D + d;
+    if (j >= info[ru.b].qn) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < ru.n; ++i) {
+      const Place pl = s_place[ru.first + i];
+      const float4 v = *reinterpret_cast<const float4*>(pl.p + w_rg * pl.step + at);
+      const float wt = s_wt[(ru.first + i) * rows_all + row];
+      acc.x = fmaf(wt, v.x, acc.x); acc.y = fmaf(wt, v.y, acc.y); acc.z = fmaf(wt, v.z, acc.z); acc.w = fmaf(wt, v.w, acc.w);
+    }
+    const int ml = s_place[ru.first].at * rows_all + row;
     if (ru.whole) {
-      acc.write(g, (int64_t)(sj.q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, lane);
+      write_row4<D>(g, (int64_t)(info[ru.b].q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, d, acc, s_m[ml], s_l[ml]);
     } else {
       float* p = g.cta_parts + ((size_t)blockIdx.x * 2 + ru.slot) * cta_part;
-#pragma unroll
-      for (int i = 0; i < E; ++i) p[row * D + E * lane + i] = acc.o[i];
-      if (lane == 0) {
-        p[rows_all * D + row] = acc.m;
-        p[rows_all * D + rows_all + row] = acc.l;
+      *reinterpret_cast<float4*>(p + row * D + d) = acc;
+      if (d == 0) {
+        p[rows_all * D + row] = s_m[ml];
+        p[rows_all * D + rows_all + row] = s_l[ml];
       }
     }
   }
@@ -931,7 +989,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     const Run ru = s_run[tid];
     if (!ru.whole) {
       uint32_t* cnt = g.counters + ru.b * Hkv + ru.h;
-      const uint32_t n = (uint32_t)(ru.f1 - ru.f0);
+      const uint32_t n = (uint32_t)(ru.u1 - ru.u0);
       if (atom_acq_rel_add(cnt, n) + n == (uint32_t)seq_units(info[ru.b])) {
         *cnt = 0;
         s_last[ru.slot] = tid;
@@ -944,34 +1002,44 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     const Run ru = s_run[s_last[k]];
     const SeqInfo sj = info[ru.b];
     const int units = seq_units(sj);
-    const long long p0 = prefix[ru.b] + (long long)ru.h * units;
-    const int c0 = (int)(((p0 + 1) * G - 1) / W), c1 = (int)(((p0 + units) * G - 1) / W);
-    auto part = [&](int i) { return g.cta_parts + ((size_t)i * 2 + ((long long)i * W / G > p0 ? 0 : 1)) * cta_part; };
-    for (int row = warp; row < rows_all; row += NW) {
-      const int j = row / g.group;
+    // the CTAs that hold the pair's first and last unit; CTA i's run begins at i W / G
+    const long long p0 = prefix[ru.b] + (long long)ru.h * (units + kPairCost) + kPairCost;
+    const int c0 = (int)(((p0 + 1) * G - 1) / W), n = (int)(((p0 + units) * G - 1) / W) - c0 + 1;
+    // parts in batches: a batch's loads are all in flight, then the sums move to its maximum
+    for (int t = tid; t < rows_all * (D / 4); t += THREADS) {
+      const int d = t % (D / 4) * 4, row = t / (D / 4), j = token_of(row);
       if (j >= sj.qn) continue;
-      Row<D> acc;
-      acc.clear();
-      float mx = -FLT_MAX;
-      for (int i = c0 + lane; i <= c1; i += 32) {
-        const float pm = __ldcg(part(i) + rows_all * D + row);
-        mx = pm > mx || pm != pm ? pm : mx;
-      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mx = -FLT_MAX, sum = 0.f;
+      constexpr int BATCH = 4;
+      for (int i0 = 0; i0 < n; i0 += BATCH) {
+        float4 v[BATCH];
+        float pm[BATCH], pl[BATCH];
 #pragma unroll
-      for (int i = 16; i; i >>= 1) {
-        const float y = __shfl_xor_sync(0xFFFFFFFFu, mx, i);
-        mx = y > mx || y != y ? y : mx;
-      }
-      acc.m = mx;
-#pragma unroll 4
-      for (int i = c0; i <= c1; ++i) {
-        const float* p = part(i);
-        float v[E];
+        for (int i = 0; i < BATCH; ++i) {
+          // (the pair's first CTA holds its part as one that begins there, the others as one that goes on)
+          const float* p = g.cta_parts + ((size_t)(c0 + i0 + i) * 2 + (i0 + i == 0 ? 1 : 0)) * cta_part;
+          const bool in = i0 + i < n;
+          v[i] = in ? __ldcg(reinterpret_cast<const float4*>(p + row * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          pm[i] = in ? __ldcg(p + rows_all * D + row) : -FLT_MAX;
+          pl[i] = in ? __ldcg(p + rows_all * D + rows_all + row) : 0.f;
+        }
+        float m_new = mx;
 #pragma unroll
-        for (int x = 0; x < E; ++x) v[x] = __ldcg(p + row * D + E * lane + x);
-        acc.add(v, __ldcg(p + rows_all * D + row), __ldcg(p + rows_all * D + rows_all + row));
+        for (int i = 0; i < BATCH; ++i) m_new = pm[i] > m_new || pm[i] != pm[i] ? pm[i] : m_new;
+        const float al = ex2(mx - m_new);
+        mx = m_new;
+        sum *= al;
+        acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const float wt = ex2(pm[i] - mx);
+          sum = fmaf(wt, pl[i], sum);
+          acc.x = fmaf(wt, v[i].x, acc.x); acc.y = fmaf(wt, v[i].y, acc.y);
+          acc.z = fmaf(wt, v[i].z, acc.z); acc.w = fmaf(wt, v[i].w, acc.w);
+        }
       }
-      acc.write(g, (int64_t)(sj.q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, lane);
+      write_row4<D>(g, (int64_t)(sj.q0 + j) * g.q_heads + ru.h * g.group + row - j * g.group, d, acc, mx, sum);
     }
   }
 }
@@ -993,17 +1061,17 @@ static size_t meta_bytes(int n_seqs, int warps, int stages) {
 
 template <int FMT, int D, int NT, int NW, int SUBS>
 static moe_status_t launch(const Args& a, AttnArgs g, int ctas, cudaStream_t stream) {
-  constexpr int unit = kUnitSubs * Sub<FMT, D>::BYTES;
-  // 4 KB are left for the kernel's fixed tables
+  constexpr size_t unit = kUnitSubs * Sub<FMT, D>::BYTES, most = kSmemMax - 6144;   // (the kernel's fixed tables take the rest)
   int stages = 6;
-  while (stages > 1 && (size_t)NW * stages * unit + meta_bytes(a.n_seqs, NW, stages) > kSmemMax - 4096) --stages;
+  while (stages > 1 && NW * stages * unit + meta_bytes(a.n_seqs, NW, stages) > most) --stages;
   g.stages = stages;
-  const size_t smem = (size_t)NW * stages * unit + meta_bytes(a.n_seqs, NW, stages);
+  g.rings = (int32_t)(NW * stages * unit);
+  const size_t smem = g.rings + meta_bytes(a.n_seqs, NW, stages);
   static int configured[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!configured[dev]) {
-    if (cudaFuncSetAttribute(attn_kernel<FMT, D, NT, NW, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 4096) !=
+    if (cudaFuncSetAttribute(attn_kernel<FMT, D, NT, NW, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
         cudaSuccess)
       return MOE_ERR_CUDA;
     configured[dev] = 1;
@@ -1055,7 +1123,7 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   const int group = q_heads / cache->kv_heads, rows = batch->max_q * group;
   const kv::Shape s = kv::shape_for(rows);
   uint8_t* w = (uint8_t*)ws + sizeof(WsHeader);
-  kv::AttnArgs g{(const uint16_t*)q, q_stride, q_heads, group, window, s.row_groups, 0, scale * 1.4426950408889634f,
+  kv::AttnArgs g{(const uint16_t*)q, q_stride, q_heads, group, window, s.row_groups, 0, 65535u / (uint32_t)group + 1u, 0, scale * 1.4426950408889634f,
                  (uint16_t*)out, lse, (uint32_t*)w, nullptr, nullptr};
   w += up256((size_t)batch->n_seqs * cache->kv_heads * 4);
   g.warp_parts = (float*)w;

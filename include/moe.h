@@ -370,7 +370,7 @@ moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
  *   Numerics: q scaled by a power of two into binary16 (exact within 2^-28 of the row's largest), codes exact, block scales
  *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s times the value scales, brought into
  *   binary16's range by powers of two that follow the scales, are rounded to binary16 (2^-11 relative, for products down to
- *   2^-28 of the largest possible one).
+ *   2^-26 of the largest, smaller ones too while a row has fewer than 12 keys of some weight).
  *   q 16-byte aligned with a stride multiple of 8; max_q <= 8, max_q * q_heads / kv_heads <= 128. Scales of blocks that
  *   moe_kv_append writes are finite and below 2^64; other contents must keep to that.
  *   The result of a row does not depend on when CTAs run (partial results are joined in a fixed order). */
