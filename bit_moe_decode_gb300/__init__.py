@@ -186,21 +186,38 @@ def moe_rms_norm_bf16(y, T: int, H: int, eps: float, x_bf16, stream=None):
 
 
 # ------------------------------------------------------------------------------------------------ KV cache and logits
-def _rows(t, heads: int, D: int):
-    """Pointer and row stride (elements) of a bf16 [tokens, heads, D] tensor whose rows may be slices of wider ones."""
-    if t is None:
-        return None, 0
-    assert t.is_cuda and t.element_size() == 2 and t.dim() == 3 and t.shape[1:] == (heads, D), "expected bf16 [tokens, heads, D]"
-    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == D), "heads and dimensions must be contiguous"
-    return C.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * D)
+# (a decode step makes these calls per layer: their pointers go to ctypes as plain integers, which costs less)
+_BF16_SIZED = (torch.bfloat16, torch.int16)
 
 
-def _typed(t, dtype, *shape):
-    """Pointer of a contiguous tensor of this type and shape (None passes)."""
+def _raw_stream(stream, t) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _rows(t, heads: int, D: int, n: int):
+    """Pointer and row stride (elements) of a bf16 [n, heads, D] tensor whose rows may be slices of wider ones."""
+    assert t.is_cuda and t.dtype in _BF16_SIZED and t.shape == (n, heads, D), "expected bf16 [%d, %d, %d]" % (n, heads, D)
+    s0, s1, s2 = t.stride()
+    assert s2 == 1 and (s1 == D or heads == 1), "heads and dimensions must be contiguous"
+    return t.data_ptr(), s0 if n > 1 else max(s0, heads * D)
+
+
+def _dense(t, dtype, shape):
+    """Pointer of a contiguous CUDA tensor of this type and shape (None passes)."""
     if t is None:
         return None
-    assert t.dtype == dtype and tuple(t.shape) == shape, "expected %s %s, got %s %s" % (dtype, shape, t.dtype, tuple(t.shape))
-    return _ptr(t)
+    assert t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous(), \
+        "expected contiguous %s %s, got %s %s" % (dtype, shape, t.dtype, tuple(t.shape))
+    return t.data_ptr()
+
+
+def _dense_bf16(t, shape):
+    assert t.is_cuda and t.dtype in _BF16_SIZED and t.shape == shape and t.is_contiguous(), "expected contiguous bf16 %s" % (shape,)
+    return t.data_ptr()
+
+
+def _ws(ws):
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def moe_kv_page_bytes(fmt: int, head_dim: int, kv_heads: int, page_tokens: int) -> int:
@@ -208,7 +225,7 @@ def moe_kv_page_bytes(fmt: int, head_dim: int, kv_heads: int, page_tokens: int) 
 
 
 def moe_kv_workspace_bytes(cache: "KvCache", batch: "KvBatch", q_heads: int) -> int:
-    return lib().moe_kv_workspace_bytes(C.byref(cache.c), C.byref(batch.c), q_heads)
+    return lib().moe_kv_workspace_bytes(cache.ref, batch.ref, q_heads)
 
 
 def moe_kv_append(cache: "KvCache", batch: "KvBatch", k, v, q=None, q_out=None, cos=None, sin=None,
@@ -216,36 +233,43 @@ def moe_kv_append(cache: "KvCache", batch: "KvBatch", k, v, q=None, q_out=None, 
     """Rotate q and k by their positions (cos, sin [positions, R / 2] fp32; None: no rotation), write q to q_out and
     encode k and v into their pages. k, v [tokens, kv_heads, D], q [tokens, q_heads, D] bf16, rows with any stride."""
     n, D, Hkv = batch.c.n_tokens, cache.head_dim, cache.kv_heads
-    for t in (k, v, q):
-        assert t is None or t.shape[0] == n, "one row a token of the batch"
-    kp, ks = _rows(k, Hkv, D)
-    vp, vs = _rows(v, Hkv, D)
-    Hq = q.shape[1] if q is not None else 0
-    qp, qs = _rows(q, Hq, D)
-    assert q is None or (q_out is not None and tuple(q_out.shape) == (n, Hq, D) and q_out.element_size() == 2)
-    R, rows = (2 * cos.shape[1], cos.shape[0]) if cos is not None else (0, 0)
-    _check(lib().moe_kv_append(C.byref(cache.c), C.byref(batch.c), kp, ks, vp, vs, qp, qs, Hq, _ptr(q_out),
-                               _typed(cos, torch.float32, rows, R // 2), _typed(sin, torch.float32, rows, R // 2), R, rows,
-                               int(interleaved), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_kv_append")
+    kp, ks = _rows(k, Hkv, D, n)
+    vp, vs = _rows(v, Hkv, D, n)
+    qp, qs, Hq, qo = None, 0, 0, None
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows(q, Hq, D, n)
+        qo = _dense_bf16(q_out, (n, Hq, D))
+    R = rows = 0
+    if cos is not None:
+        rows, R = cos.shape
+    wp, wn = _ws(ws)
+    st = lib().moe_kv_append(cache.ref, batch.ref, kp, ks, vp, vs, qp, qs, Hq, qo, _dense(cos, torch.float32, (rows, R)),
+                             _dense(sin, torch.float32, (rows, R)), 2 * R, rows, interleaved, wp, wn, _raw_stream(stream, k))
+    if st:
+        raise MoeError(st, "moe_kv_append")
 
 
 def moe_kv_read(cache: "KvCache", batch: "KvBatch", k_out, v_out, ws=None, stream=None):
     """The values that the batch's tokens have in the cache, fp32 [tokens, kv_heads, D] (either output may be None)."""
     shape = (batch.c.n_tokens, cache.kv_heads, cache.head_dim)
-    _check(lib().moe_kv_read(C.byref(cache.c), C.byref(batch.c), _typed(k_out, torch.float32, *shape),
-                             _typed(v_out, torch.float32, *shape), _ptr(ws), ws.numel() * ws.element_size(),
-                             _stream(stream)), "moe_kv_read")
+    wp, wn = _ws(ws)
+    st = lib().moe_kv_read(cache.ref, batch.ref, _dense(k_out, torch.float32, shape), _dense(v_out, torch.float32, shape), wp, wn,
+                           _raw_stream(stream, ws))
+    if st:
+        raise MoeError(st, "moe_kv_read")
 
 
 def moe_kv_attention(cache: "KvCache", batch: "KvBatch", q, scale: float, out, lse=None, window: int = 0, ws=None,
                      stream=None):
     """Attention of the batch's rows over their sequences' cache: out [tokens, q_heads, D] bf16, lse [tokens, q_heads]."""
     n, Hq, D = batch.c.n_tokens, q.shape[1], cache.head_dim
-    assert q.shape[0] == n and tuple(out.shape) == (n, Hq, D) and out.element_size() == 2
-    qp, qs = _rows(q, Hq, D)
-    _check(lib().moe_kv_attention(C.byref(cache.c), C.byref(batch.c), qp, qs, Hq, scale, window, _ptr(out),
-                                  _typed(lse, torch.float32, n, Hq), _ptr(ws), ws.numel() * ws.element_size(),
-                                  _stream(stream)), "moe_kv_attention")
+    qp, qs = _rows(q, Hq, D, n)
+    wp, wn = _ws(ws)
+    st = lib().moe_kv_attention(cache.ref, batch.ref, qp, qs, Hq, scale, window, _dense_bf16(out, (n, Hq, D)),
+                                _dense(lse, torch.float32, (n, Hq)), wp, wn, _raw_stream(stream, q))
+    if st:
+        raise MoeError(st, "moe_kv_attention")
 
 
 def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, draft=None, bias=None, allowed=None,
@@ -255,21 +279,25 @@ def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, 
     rows_per_seq - 1]), biases ((start, id, value) per sequence) and the allowed-token bits (int32 [rows, words])."""
     R, V = logits.shape
     n = params.shape[0]
-    assert logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16) and logits.stride(1) == 1
+    f32 = logits.dtype == torch.float32
+    s0, s1 = logits.stride()
+    assert logits.is_cuda and (f32 or logits.dtype == torch.bfloat16) and s1 == 1
     assert R == n * rows_per_seq, "rows = n_seqs * rows_per_seq"
-    start, ids, vals = bias if bias is not None and bias[1].numel() else (None, None, None)
-    if ids is not None:
-        assert ids.dtype == torch.int32 and vals.dtype == torch.float32 and ids.numel() == vals.numel()
+    bs = bi = bv = al = None
+    if bias is not None and bias[1].numel():
+        m = bias[1].numel()
+        bs, bi, bv = _dense(bias[0], torch.int32, (n + 1,)), _dense(bias[1], torch.int32, (m,)), _dense(bias[2], torch.float32, (m,))
+    words = 0
     if allowed is not None:
-        assert allowed.dtype == torch.int32 and allowed.dim() == 2 and allowed.shape[0] == R
-    c = moe_logits_t(MOE_LOGITS_F32 if logits.dtype == torch.float32 else MOE_LOGITS_BF16, n, rows_per_seq, V,
-                     logits.data_ptr(), logits.stride(0) if R > 1 else max(V, logits.stride(0)),
-                     _typed(params, torch.float32, n, 4),
-                     _typed(counts, torch.int32, n, V), _typed(draft, torch.int32, n, rows_per_seq - 1),
-                     _typed(start, torch.int32, n + 1), _ptr(ids), _ptr(vals), _ptr(allowed),
-                     allowed.shape[1] if allowed is not None else 0)
-    _check(lib().moe_logits_probs(C.byref(c), _typed(probs, torch.float32, R, V), _typed(top, torch.int32, R),
-                                  _stream(stream)), "moe_logits_probs")
+        words = allowed.shape[1]
+        al = _dense(allowed, torch.int32, (R, words))
+    c = moe_logits_t(MOE_LOGITS_F32 if f32 else MOE_LOGITS_BF16, n, rows_per_seq, V, logits.data_ptr(), s0 if R > 1 else max(V, s0),
+                     _dense(params, torch.float32, (n, 4)), _dense(counts, torch.int32, (n, V)),
+                     _dense(draft, torch.int32, (n, rows_per_seq - 1)), bs, bi, bv, al, words)
+    st = lib().moe_logits_probs(C.byref(c), _dense(probs, torch.float32, (R, V)), _dense(top, torch.int32, (R,)),
+                                _raw_stream(stream, logits))
+    if st:
+        raise MoeError(st, "moe_logits_probs")
 
 
 def moe_workspace_bytes(layer: "Layer", T_max: int, k: int) -> int:
@@ -418,6 +446,7 @@ class KvCache:
         self.fmt, self.head_dim, self.kv_heads, self.page_tokens, self.pages = fmt, head_dim, kv_heads, page_tokens, pages
         self.c = moe_kv_cache_t(fmt, head_dim, kv_heads, page_tokens, pages.shape[0],
                                 max(pages.stride(0), nbytes) if pages.shape[0] == 1 else pages.stride(0), pages.data_ptr())
+        self.ref = C.byref(self.c)
 
     def workspace(self, batch: "KvBatch", q_heads: int, stream=None) -> torch.Tensor:
         """Zeroed, 256-byte aligned workspace for the cache's calls with batches of this size."""
@@ -433,5 +462,6 @@ class KvBatch:
         n = seq_len.numel()
         assert block_table.dim() == 2
         self.q_start, self.seq_len, self.block_table = q_start, seq_len, block_table
-        self.c = moe_kv_batch_t(n, tokens, max_q, block_table.shape[1], _typed(q_start, torch.int32, n + 1),
-                                _typed(seq_len, torch.int32, n), _typed(block_table, torch.int32, n, block_table.shape[1]))
+        self.c = moe_kv_batch_t(n, tokens, max_q, block_table.shape[1], _dense(q_start, torch.int32, (n + 1,)),
+                                _dense(seq_len, torch.int32, (n,)), _dense(block_table, torch.int32, tuple(block_table.shape)))
+        self.ref = C.byref(self.c)

@@ -72,19 +72,16 @@ inline moe_status_t check(const moe_kv_cache_t* c, const moe_kv_batch_t* b, Args
 
 // One sequence's rows and length; anything out of range makes it empty and is recorded.
 struct Seq { int q0, qn, len; };
-__device__ __forceinline__ Seq load_seq(const Args& a, int b, int max_q) {
-  Seq s{a.q_start[b], 0, a.seq_len[b]};
-  const int q1 = a.q_start[b + 1];
-  if (s.q0 < 0 || q1 < s.q0 || q1 > a.n_tokens) {          // its rows are not in the call's tensors
+__device__ __forceinline__ Seq check_seq(const Args& a, int q0, int q1, int len, int max_q) {
+  if (q0 < 0 || q1 < q0 || q1 > a.n_tokens) {              // its rows are not in the call's tensors
     record_error(a.status, MOE_ERR_INVALID_ARG);
     return Seq{0, 0, 0};
   }
-  s.qn = q1 - s.q0;
-  if (s.qn > max_q || s.len < 0 || s.len > a.table_stride * a.page_tokens) {
+  if (q1 - q0 > max_q || len < 0 || len > a.table_stride * a.page_tokens) {
     record_error(a.status, MOE_ERR_INVALID_ARG);
-    s.len = 0;
+    len = 0;
   }
-  return s;
+  return Seq{q0, q1 - q0, len};
 }
 
 // A page id from the table; an id outside the pool is recorded and reads as page 0 (`ok` tells a writer).
@@ -94,14 +91,7 @@ __device__ __forceinline__ int check_page(const Args& a, int id, bool& ok) {
   return ok ? id : 0;
 }
 
-// the value of one 4-bit code, and of a block's scale
-template <int FMT>
-__device__ __forceinline__ float code_value(uint32_t c) {
-  if (FMT == MOE_FMT_INT4G32) return (float)(((int)(c << 28)) >> 28);
-  const uint32_t m = c & 7u;   // magnitudes 0, 0.5, then (2 + (m & 1)) 2^((m >> 1) - 2)
-  const float v = m < 2 ? 0.5f * (float)m : (float)(2u + (m & 1u)) * exp2i((int)(m >> 1) - 2);
-  return (c & 8u) ? -v : v;
-}
+// a block's scale
 template <int FMT>
 __device__ __forceinline__ float load_scale(const uint8_t* p) {
   if (FMT == MOE_FMT_MXFP4) return __uint_as_float((uint32_t)*p << 23);   // 2^(e - 127); e = 0 is zero

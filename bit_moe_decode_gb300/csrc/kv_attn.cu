@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     const int b = base + tid;
     long long x = 0;
     if (b < a.n_seqs) {
-      const Seq sq = load_seq(a, b, a.max_q);
+      const Seq sq = check_seq(a, a.q_start[b], a.q_start[b + 1], a.seq_len[b], a.max_q);
       SeqInfo si{sq.q0, sq.qn, sq.len, 0};
       if (g.window > 0 && sq.len - sq.qn - g.window + 1 > 0) si.sub0 = (sq.len - sq.qn - g.window + 1) / 16;
       info[b] = si;

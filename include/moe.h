@@ -404,7 +404,8 @@ typedef struct {
 /* For each row, in fp32 with each operation rounded, c the count of token v (with earlier drafts):
  *   x = logit (NaN: -inf); if c > 0: x = x > 0 ? x / repetition : x * repetition, then x = (x - frequency * c) - presence;
  *   x = x + bias; x = -inf where not allowed;
- *   probs [rows, vocab] fp32 (contiguous): softmax(x / temperature); temperature 0: 1 at the first largest x, else 0. Where
+ *   probs [rows, vocab] fp32 (contiguous): softmax(x / temperature); temperature 0 (or so small that 1 / temperature
+ *   overflows): 1 at the first largest x, else 0. Where
  *   the largest x is +inf, the tokens at +inf share the row equally. A row whose x are all -inf gives zeros.
  *   top [rows] int32 (or NULL): the first largest x's token, -1 if all are -inf.
  *   Logits and probs may have any alignment of their type; every other pointer 4-byte aligned. probs may be logits itself
