@@ -33,114 +33,26 @@
 //     scale of its own, so that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has
 //     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a dimension whose few heavy keys all have code 0 is
 //     made of such weights.
-#include <cfloat>
-
-#include "kv.cuh"
+#include "kv_attn.cuh"
 
 namespace moe {
 namespace kv {
 
 constexpr int kUnitSubs = 2;        // sub-blocks per unit
 constexpr int kBatch = 16;          // units whose addresses a warp's lanes hold at a time
-constexpr int kSmemMax = 232448;
-constexpr int kPExp = 12;               // weights are carried times 2^12
-constexpr float kLazy = 2.f;            // a score may pass the running maximum by this (base 2)
 constexpr int kEv0 = 2;                 // E at first: scales 2^-12 .. 2^4
 constexpr float kNormal = 6.103515625e-05f;   // 2^-14: binary16 products from here on keep all bits
 constexpr int kPassExp = 26;            // powers of two that a pass covers
-constexpr float kHeavy = 0.25f, kLight = 0.000244140625f;   // 2^12 times 2^-14 and 2^-24
 
-struct AttnArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  int32_t q_heads, group, window, row_groups, stages;
-  uint32_t group_inv;               // floor(row / group) = row * group_inv >> 16 for rows below 128
-  int32_t rings;                    // bytes of the warps' rings; the tables follow
-  float scale_log2;                 // scale * log2(e)
-  uint16_t* out;
-  float* lse;
-  uint32_t* counters;               // [n_seqs * kv_heads]
-  float* warp_parts;                // [CTAs][warps] partials of runs that end inside a warp's range
-  float* cta_parts;                 // [CTAs][2]
-};
-
-__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }   // (keeps rare code out of the loop's lines)
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN loses, as in fmaxf
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float y;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // 8 x 8 of 16 bits over the warp
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-  return d;
-}
-__device__ __forceinline__ uint32_t hadd2_bits(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {   // (selector bit 3: the byte's sign fill)
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {   // N = 1, 2 or 4 words
-  if (N == 4) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x; w[1 % N] = u.y; w[2 % N] = u.z; w[3 % N] = u.w;
-  } else if (N == 2) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x; w[1 % N] = u.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
-}
-
-// the scales of one token's blocks in fp32
-template <int FMT, int NB>
-__device__ __forceinline__ void load_scales(float (&s)[NB], const uint8_t* p) {
-  if (FMT == MOE_FMT_MXFP4) {   // 2^(e - 127), e = 0 is zero: the byte is the exponent field
-    const uint32_t w = NB == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t v = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
-      s[b] = __uint_as_float(b == 0 ? v & 0x7F800000u : v & 0x7F800000u);
-    }
-  } else {
-    uint32_t w[NB / 2];
-    load_words<NB / 2>(w, p);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) s[b] = __uint_as_float(b & 1 ? w[b / 2] & 0xFFFF0000u : w[b / 2] << 16);
-  }
 }
 
 // Two keys' K words (rows r and r + 8) of one block -> the A fragments of its two k-steps.
@@ -184,8 +96,6 @@ __device__ __forceinline__ void decode_v(uint32_t w0, uint32_t w1, uint32_t (&a)
   }
 }
 
-struct SeqInfo { int q0, qn, len, sub0; };   // sub0: first sub-block that a row sees
-
 __device__ __forceinline__ int seq_units(const SeqInfo& s) {
   return s.qn > 0 && s.len > 0 ? ((s.len + 15) / 16 - s.sub0 + kUnitSubs - 1) / kUnitSubs : 0;
 }
@@ -196,12 +106,6 @@ __device__ __forceinline__ int seq_cost(const SeqInfo& s) {
   const int u = seq_units(s);
   return u ? u + kPairCost : 0;
 }
-// x * W / n without 64-bit division where it is not needed
-__device__ __forceinline__ long long share(long long x, long long W, long long n) {
-  const unsigned long long p = (unsigned long long)x * W;
-  return p >> 32 ? (long long)(p / (unsigned long long)n) : (long long)((uint32_t)p / (uint32_t)n);
-}
-
 struct Prod {        // a warp's producer: the next batch is n units (subs sub-blocks from `sub` on) at unit u of a pair; left
   int b, h, u, units, left, n, subs, sub;   // counts the units from it on
   int ev_run[4];     // and of its consumer, per block: the largest value scale's exponent so far,
@@ -211,18 +115,6 @@ struct Prod {        // a warp's producer: the next batch is n units (subs sub-b
 struct Entry { int u0, u1, b, h; };   // a partial result of one warp: units [u0, u1) of pair (b, h); b < 0: none
 struct Run { int u0, u1, b, h, first, n, slot, whole; };      // n consecutive entries of one pair, from list place `first`
 struct Place { const float* p; int step, at; };   // an entry's values, floats from one row group's to the next's, its place
-
-// A row's joined values of four dimensions, written out
-template <int D>
-__device__ __forceinline__ void write_row4(const AttnArgs& g, int64_t row, int d, float4 o, float m, float l) {
-  const bool some = l > 0.f || l != l;
-  const float inv = some ? 1.f / l : 0.f;
-  const __nv_bfloat162 p = some ? __floats2bfloat162_rn(o.x * inv, o.y * inv) : __floats2bfloat162_rn(0.f, 0.f);
-  const __nv_bfloat162 q = some ? __floats2bfloat162_rn(o.z * inv, o.w * inv) : __floats2bfloat162_rn(0.f, 0.f);
-  *reinterpret_cast<uint2*>(g.out + row * D + d) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-  if (g.lse && d == 0) g.lse[row] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
 
 template <int FMT, int D, int NT, int NW, int SUBS>
 __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
@@ -249,6 +141,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   SeqInfo* info = reinterpret_cast<SeqInfo*>(prefix + a.n_seqs + 1 + ((a.n_seqs + 1) & 1));
   Prod* prods = reinterpret_cast<Prod*>(info + a.n_seqs);
 
+  if (NT > 1 && g.redo && __ldcg(g.redo + a.n_seqs) == 0) return;   // nothing was left over
   // ---- the sequences: lengths, first visible sub-block, prefix sums of their units over all KV heads
   if (lane < stages) mbar_init(bar + lane, 1);
   if (tid < 2 * NW) s_entry[tid].b = -1;
@@ -259,6 +152,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     if (b < a.n_seqs) {
       const Seq sq = check_seq(a, a.q_start[b], a.q_start[b + 1], a.seq_len[b], a.max_q);
       SeqInfo si{sq.q0, sq.qn, sq.len, 0};
+      if (NT > 1 && g.redo && __ldcg(g.redo + b) == 0) si.qn = 0;
       if (g.window > 0 && sq.len - sq.qn - g.window + 1 > 0) si.sub0 = (sq.len - sq.qn - g.window + 1) / 16;
       info[b] = si;
       x = (long long)seq_cost(si) * Hkv;
@@ -279,6 +173,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   fence_mbar_init();
   __syncthreads();
   const long long W = prefix[a.n_seqs];
+  if (NT > 1 && g.redo && tid == 0 && atom_acq_rel_add(g.redo + a.n_seqs + 1, 1) == gridDim.x - 1)
+    for (int b = 0; b < a.n_seqs + 2; ++b) g.redo[b] = 0;   // every CTA has read them
 
   // rows of empty sequences
   for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
@@ -515,66 +411,6 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
   };
 
-  // Value scales of tokens 2 c, 2 c + 1 (u0) and 2 c + 8, 2 c + 9 (u1) times 2^-E as binary16 pairs. Exponents outside
-  // E - 14 .. E + 1 show in `off` & kOff. Tokens whose bit of `drop` is set count as 2^-14, whatever bytes they have.
-  constexpr uint32_t kOff = FMT == MOE_FMT_MXFP4 ? 0xF0F0F0F0u : 0xF800F800u;
-  auto scale_pairs = [&](const uint8_t* sb, uint32_t (&u0)[NB], uint32_t (&u1)[NB], uint32_t& off, uint32_t drop) {
-    const uint8_t* p = sb + S::VS + 2 * c * (NB * S::SB);
-    if (FMT == MOE_FMT_MXFP4) {
-      uint32_t wa[NB / 2], wb[NB / 2];   // NB = 4: a token each; NB = 2: two tokens
-      load_words<NB / 2>(wa, p);
-      load_words<NB / 2>(wb, p + 8 * NB);
-      if (drop) {
-        const uint32_t low = 0u - vc[0];
-#pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {
-          const uint32_t ka = NB == 4 ? 0u - ((drop >> i) & 1u) : ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
-          const uint32_t kb = NB == 4 ? 0u - ((drop >> (2 + i)) & 1u) : ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
-          wa[i] = (wa[i] & ~ka) | (low & ka);
-          wb[i] = (wb[i] & ~kb) | (low & kb);
-        }
-      }
-      const uint32_t vc4 = vc[0] * 4u + 0x04040404u;
-#pragma unroll
-      for (int i = 0; i < NB / 2; ++i) {
-        // bytes e - E + 14: 0 .. 15 in the window (8 bits: nothing aliases; a borrow comes from a byte that shows itself).
-        // 4 (that + 1) is the high byte of binary16's 2^(e - E).
-        off |= (wa[i] + vc[0]) | (wb[i] + vc[0]);
-        wa[i] = wa[i] * 4u + vc4;
-        wb[i] = wb[i] * 4u + vc4;
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        // bytes (the sign fill of a byte below 128: 0; token 2 c's; 0; token 2 c + 1's)
-        const int t = NB == 4 ? 4 + b : 2 + b;
-        const uint32_t sel = (8u | b) | (uint32_t)b << 4 | (8u | t) << 8 | (uint32_t)t << 12;
-        u0[b] = prmt(wa[0], wa[NB / 2 - 1], sel);
-        u1[b] = prmt(wb[0], wb[NB / 2 - 1], sel);
-      }
-    } else {
-      // bf16 and binary16 differ in the exponent's width and bias: (bits - ((E + 113) << 7) + (1 << 7)) << 3
-      uint32_t wa[NB], wb[NB];
-      load_words<NB>(wa, p);
-      load_words<NB>(wb, p + 16 * NB);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
-        u0[b] = prmt(wa[b / 2], wa[NB / 2 + b / 2], sel);
-        u1[b] = prmt(wb[b / 2], wb[NB / 2 + b / 2], sel);
-        if (drop) {
-          const uint32_t low = 0u - vc[b % NVC];
-          const uint32_t ka = ((drop & 1u) * 0xFFFFu) | ((drop >> 1 & 1u) * 0xFFFF0000u);
-          const uint32_t kb = ((drop >> 2 & 1u) * 0xFFFFu) | ((drop >> 3 & 1u) * 0xFFFF0000u);
-          u0[b] = (u0[b] & ~ka) | (low & ka);
-          u1[b] = (u1[b] & ~kb) | (low & kb);
-        }
-        off |= (u0[b] + vc[b % NVC]) | (u1[b] + vc[b % NVC]);
-        u0[b] = u0[b] * 8u + (vc[b % NVC] * 8u + 0x04000400u);
-        u1[b] = u1[b] * 8u + (vc[b % NVC] * 8u + 0x04000400u);
-      }
-    }
-  };
-
   // The rare path: value scales outside E's window. Moves E to the largest, then adds the products of the weights s (times
   // 2^12) and the scales in passes.
   auto wide_products = [&](const uint8_t* base, const float (&s)[SUBS][NT][4]) {
@@ -726,9 +562,9 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
           const int key = kt + (t & 1) + (t & 2 ? 8 : 0);
           drop |= (key >= seg_len || key < min_lo ? 1u : 0u) << t;
         }
-        scale_pairs(sb, u0[i], u1[i], off, drop);
+        scale_pairs<FMT, NB, NVC>(sb + S::VS, c, vc, u0[i], u1[i], off, drop);
       } else {
-        scale_pairs(sb, u0[i], u1[i], off, 0u);
+        scale_pairs<FMT, NB, NVC>(sb + S::VS, c, vc, u0[i], u1[i], off, 0u);
       }
     }
     float tmax = -INFINITY;
@@ -772,7 +608,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) l[nt][e] += s[i][nt][e] + s[i][nt][e + 2];
       }
-    bool wide = off & kOff;
+    bool wide = off & kOff<FMT>;
     if (rarely(!settled)) {
       // keys of weight 2^-14 and more per row, four counts in an int, over the lanes that share the rows
       int n = 0;
@@ -1044,7 +880,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   }
 }
 
-// Rows a warp holds and warps per CTA. 8 rows: 16 warps of 128 registers. More: 16 rows in 8 warps of up to 255
+// Rows a warp holds and warps per CTA. 8 rows: 12 warps of up to 168 registers. More: 16 rows in 8 warps of up to 255
 // registers, as many warps on the same units as it takes.
 struct Shape { int nt, warps, row_groups; };
 static Shape shape_for(int rows) {
@@ -1094,8 +930,8 @@ extern "C" size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_
   if (batch->max_q > 8 || rows > kv::kMaxRows) return sizeof(WsHeader);   // append and read only
   const kv::Shape s = kv::shape_for((int)rows);
   const size_t row_bytes = (size_t)(cache->head_dim + 2) * 4;
-  return sizeof(WsHeader) + up256((size_t)batch->n_seqs * cache->kv_heads * 4) +
-         up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
+  return sizeof(WsHeader) + up256((size_t)batch->n_seqs * cache->kv_heads * 2 * 4) +
+         up256((size_t)(batch->n_seqs + 2) * 4) + up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
 }
 
 extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
@@ -1124,13 +960,24 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   const kv::Shape s = kv::shape_for(rows);
   uint8_t* w = (uint8_t*)ws + sizeof(WsHeader);
   kv::AttnArgs g{(const uint16_t*)q, q_stride, q_heads, group, window, s.row_groups, 0, 65535u / (uint32_t)group + 1u, 0, scale * 1.4426950408889634f,
-                 (uint16_t*)out, lse, (uint32_t*)w, nullptr, nullptr};
-  w += up256((size_t)batch->n_seqs * cache->kv_heads * 4);
+                 (uint16_t*)out, lse, (uint32_t*)w, nullptr, nullptr, nullptr};
+  w += up256((size_t)batch->n_seqs * cache->kv_heads * 2 * 4);
+  g.redo = (uint32_t*)w;
+  w += up256((size_t)(batch->n_seqs + 2) * 4);
   g.warp_parts = (float*)w;
   w += up256(kv::kMaxCtas * s.warps * 8 * s.nt * (size_t)(cache->head_dim + 2) * 4);
   g.cta_parts = (float*)w;
   const int ctas = moe_internal::num_sms() < kv::kMaxCtas ? moe_internal::num_sms() : kv::kMaxCtas;
   if (ctas < 1) return MOE_ERR_CUDA;
+  // Above 16 rows a KV head, and where the table and the window leave room for long sequences, kv_attn_wide.cu goes first; its
+  // cost does not grow with the rows up to 64, but a pair's start costs it 3 tiles of 128 keys, this kernel none.
+  // Measured, this kernel / that: 24 rows over 300 keys (256 sequences) 33 / 60 us; 18 rows over a window of 1024 (33)
+  // 54 / 49 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
+  // 16 rows over 8192 (64) 124 / 178 us.
+  int64_t keys = (int64_t)batch->table_stride * cache->page_tokens;
+  if (window && keys > window + batch->max_q) keys = window + batch->max_q;
+  if (rows <= 16 || keys * s.row_groups < 2048) g.redo = nullptr;
+  if (g.redo && (st = kv::attn_wide(a, g, cache->fmt, cache->head_dim, ctas, (cudaStream_t)stream)) != MOE_OK) return st;
 #define KV_CALL(F, DD)                                                                   \
   return s.nt == 1 ? kv::launch<F, DD, 1, 12, 2>(a, g, ctas, (cudaStream_t)stream)        \
                    : kv::launch<F, DD, 2, 8, 1>(a, g, ctas, (cudaStream_t)stream)
