@@ -13,12 +13,13 @@
 // 16 warps convert and do the softmax, one copies packed tiles into a ring, one issues the products. Per tile a worker
 // warp converts eight tokens' keys of the next tile, does the softmax of this one (lane = key, N / 4 rows), then converts
 // the next tile's values: S of the next tile is formed during the softmax, O during the conversion. Splitting the
-// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this takes 248, most of it polling.
+// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this takes 242, most of it polling; one
+// hand-over to the tensor cores a tile instead of two (keys two tiles ahead) 246.
 // P is stored with its rows contiguous (B transposed): a lane's key is then one or two 16-byte stores.
 //
 // What bounds it: instructions. A tile at N = 64 takes 3,500 cycles for about 510 warp instructions a worker
-// warp (58 % of the issue slots), where its shared memory traffic would take 2,300, its HBM share 800, the tensor cores
-// 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 248 us, against
+// warp (58 % of the issue slots; the integer pipe is half, shared memory two thirds busy); its HBM share would take 800, the tensor
+// cores 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 242 us, against
 // 467 us with kv_attn.cu; the cache is read at 1.4 TB/s.
 //
 // What the window of scales cannot hold (set from a pair's first tile: 12 powers of two down, 3 up), and weights below
@@ -137,6 +138,17 @@ __device__ __forceinline__ int seq_tiles(const SeqInfo& s) {
 
 // A row's keys, counted until there are 12 of weight 2^-16 and more (low half); those of 2^-8 and more in the high half.
 __device__ __forceinline__ bool few_keys(int cnt) { return (cnt & 0xFFFF) < 12; }
+
+// The rest of a wait: true if it ran out.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, int parity, int32_t* status) {
+  const long long t0 = globaltimer_ns();
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n)
+    if (n % 64 == 0 && globaltimer_ns() - t0 > kDefaultWaitNs) {
+      record_error(status, MOE_ERR_DEVICE_TIMEOUT);
+      return true;
+    }
+  return false;
+}
 
 template <int FMT, int D, int N>
 struct Wide {   // shared memory, in bytes from the 1024-byte aligned start
@@ -273,14 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
   // loops end (the results are void).
   bool dead = false;
   auto wait = [&](uint64_t* bar, int parity) {
-    if (dead || mbar_try_wait(bar, parity)) return;
-    const long long t0 = globaltimer_ns();
-    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n)
-      if (n % 64 == 0 && globaltimer_ns() - t0 > kDefaultWaitNs) {
-        dead = true;
-        record_error(a.status, MOE_ERR_DEVICE_TIMEOUT);
-        return;
-      }
+    if (!mbar_try_wait(bar, parity) && !dead) dead = wait_longer(bar, parity, a.status);
   };
 
   if (warp == kWorkers) {
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     if (lane == 0) {
       const uint32_t idesc = idesc_f16(N);
       const uint64_t dk = umma_desc_sw128(smem_u32(smem + L::K)), dq = umma_desc_sw128(smem_u32(smem + L::Q)),
-                     dv = umma_desc_sw128(smem_u32(smem + L::V)), 
+                     dv = umma_desc_sw128(smem_u32(smem + L::V)),
                      dp = umma_desc(smem_u32(smem + L::P), 16 * N, 16 * N, N == 64 ? 2 : 4);
       int b = b0, h = h0, u = u0, units = units0;
       bool first = true, first_prev = true;              // the tile begins (this CTA's part of) a pair
