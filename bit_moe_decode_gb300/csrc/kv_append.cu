@@ -6,10 +6,11 @@
 // INT4 the best of six scales by squared error; the rules are moe_encode_blocks'. The kernel is bound by latency in
 // decode (q_start -> length -> table -> store, a chain of four L2 trips) and by HBM for prompts.
 //
-// D / 4 lanes hold a row, four values each, so that a block is 8 neighbouring lanes: its maximum is three shuffles, a K
-// word is two lanes' codes, a V word is one lane's. A warp takes 128 / D rows of one kind (q, k or v) at a time, and
-// several such groups of its token in turn when there are many tokens: the token's lookups and rotation are then
-// shared, and four groups' loads are in flight.
+// D / E lanes hold a row, E values each. MXFP4, E = 8: a block is 4 neighbouring lanes, its maximum two shuffles, a K word one
+// lane's codes, two V words one lane's. INT4, E = 4: its six candidates' sums are spread over 8 lanes. (MXFP4 has E = 4 too, for
+// halves of the rotated part that are no multiple of 8.) A warp takes 32 E / D rows of one kind (q, k or v) at a time, and several
+// such groups of its token in turn when there are many tokens: the token's lookups and rotation are then shared, and four
+// groups' loads are in flight.
 #include "kv.cuh"
 
 namespace moe {
@@ -49,51 +50,105 @@ __device__ __forceinline__ Seq find_seq(const Args& a, int t, int& b) {
                    0x7FFFFFFF);
 }
 
-__device__ __forceinline__ float4 load4_bf16(const uint16_t* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
+template <int E>
+struct Vals { float v[E]; };      // E = 4 or 8 neighbouring dimensions of a row
+
+__device__ __forceinline__ void unpack2(uint32_t u, float& a, float& b) {
+  a = __uint_as_float(u << 16);
+  b = __uint_as_float(u & 0xFFFF0000u);
+}
+template <int E>
+__device__ __forceinline__ Vals<E> load_bf16(const uint16_t* p) {
+  Vals<E> x;
+  if (E == 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    unpack2(u.x, x.v[0], x.v[1]);
+    unpack2(u.y, x.v[2], x.v[3]);
+    unpack2(u.z, x.v[4 % E], x.v[5 % E]);
+    unpack2(u.w, x.v[6 % E], x.v[7 % E]);
+  } else {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    unpack2(u.x, x.v[0], x.v[1]);
+    unpack2(u.y, x.v[2], x.v[3]);
+  }
+  return x;
+}
+template <int E>
+__device__ __forceinline__ Vals<E> no_values() {
+  Vals<E> x;
+#pragma unroll
+  for (int j = 0; j < E; ++j) x.v[j] = 0.f;
+  return x;
+}
+template <int E>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const Vals<E>& y) {
+  uint32_t u[E / 2];
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(y.v[2 * j], y.v[2 * j + 1]);
+    u[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  if (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2 % (E / 2)], u[3 % (E / 2)]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
 }
 
 // The rotation of a token's rows as a lane applies it: y = x c + partner s, the same for every row. `from`: the lane that
 // holds the partners (half-split pairs), or the lane itself (interleaved pairs lie in one lane).
-struct Turn { float c[4], s[4]; int from; bool in, inter; };
-__device__ __forceinline__ Turn load_turn(int l, int R, bool inter, const float* cs, const float* sn) {
-  Turn t;
-  const int d = 4 * l, lane = threadIdx.x & 31;
+template <int E>
+struct Turn { float c[E], s[E]; int from; bool in, inter; };
+template <int E>
+__device__ __forceinline__ Turn<E> load_turn(int l, int R, bool inter, const float* cs, const float* sn) {
+  Turn<E> t;
+  const int d = E * l, lane = threadIdx.x & 31;
   t.inter = inter;
   t.in = d < R;
   t.from = lane;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) { t.c[j] = 1.f; t.s[j] = 0.f; }
+  for (int j = 0; j < E; ++j) { t.c[j] = 1.f; t.s[j] = 0.f; }
   if (!t.in) return t;
   if (inter) {
-    const float2 c = __ldg(reinterpret_cast<const float2*>(cs + 2 * l)), s = __ldg(reinterpret_cast<const float2*>(sn + 2 * l));
-    t.c[0] = t.c[1] = c.x; t.c[2] = t.c[3] = c.y;
-    t.s[0] = -s.x; t.s[1] = s.x; t.s[2] = -s.y; t.s[3] = s.y;
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float2 c = __ldg(reinterpret_cast<const float2*>(cs + (d + j) / 2)), s = __ldg(reinterpret_cast<const float2*>(sn + (d + j) / 2));
+      t.c[j] = t.c[j + 1] = c.x; t.c[j + 2] = t.c[j + 3] = c.y;
+      t.s[j] = -s.x; t.s[j + 1] = s.x; t.s[j + 2] = -s.y; t.s[j + 3] = s.y;
+    }
   } else {
     const bool first = d < R / 2;
     const int i = first ? d : d - R / 2;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + i)), s = __ldg(reinterpret_cast<const float4*>(sn + i));
-    t.from = first ? lane + R / 8 : lane - R / 8;
-    t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
-    t.s[0] = first ? -s.x : s.x; t.s[1] = first ? -s.y : s.y; t.s[2] = first ? -s.z : s.z; t.s[3] = first ? -s.w : s.w;
+    t.from = first ? lane + R / (2 * E) : lane - R / (2 * E);
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + i + j)), s = __ldg(reinterpret_cast<const float4*>(sn + i + j));
+      t.c[j] = c.x; t.c[j + 1] = c.y; t.c[j + 2] = c.z; t.c[j + 3] = c.w;
+      t.s[j] = first ? -s.x : s.x; t.s[j + 1] = first ? -s.y : s.y;
+      t.s[j + 2] = first ? -s.z : s.z; t.s[j + 3] = first ? -s.w : s.w;
+    }
   }
   return t;
 }
-// y of dimensions 4 l .. 4 l + 3 of a row: each product and the sum are rounded (no contraction), as the call promises
+// y of dimensions E l .. E l + E - 1 of a row: each product and the sum are rounded (no contraction), as the call promises
 // (x_a c - x_b s is x_a c + x_b (-s): a sign does not round)
-__device__ __forceinline__ float4 rotate(float4 x, const Turn& t) {
-  float4 p = make_float4(x.y, x.x, x.w, x.z);
-  if (!t.inter)
-    p = make_float4(__shfl_sync(0xFFFFFFFFu, x.x, t.from), __shfl_sync(0xFFFFFFFFu, x.y, t.from),
-                    __shfl_sync(0xFFFFFFFFu, x.z, t.from), __shfl_sync(0xFFFFFFFFu, x.w, t.from));
-  if (!t.in) return x;
-  return make_float4(__fadd_rn(__fmul_rn(x.x, t.c[0]), __fmul_rn(p.x, t.s[0])), __fadd_rn(__fmul_rn(x.y, t.c[1]), __fmul_rn(p.y, t.s[1])),
-                     __fadd_rn(__fmul_rn(x.z, t.c[2]), __fmul_rn(p.z, t.s[2])), __fadd_rn(__fmul_rn(x.w, t.c[3]), __fmul_rn(p.w, t.s[3])));
+template <int E>
+__device__ __forceinline__ Vals<E> rotate(const Vals<E>& x, const Turn<E>& t) {
+  Vals<E> p, y;
+#pragma unroll
+  for (int j = 0; j < E; ++j) p.v[j] = t.inter ? x.v[j ^ 1] : x.v[j];
+  if (!t.inter) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) p.v[j] = __shfl_sync(0xFFFFFFFFu, p.v[j], t.from);
+  }
+#pragma unroll
+  for (int j = 0; j < E; ++j) y.v[j] = t.in ? __fadd_rn(__fmul_rn(x.v[j], t.c[j]), __fmul_rn(p.v[j], t.s[j])) : x.v[j];
+  return y;
 }
 
 __device__ __forceinline__ float sane(float v) { return v != v ? 0.f : fminf(fmaxf(v, -kClamp), kClamp); }
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 
 // clamp(rint(w / s), -8, 7) of the rounded quotient, |w / s| < 8.2, without dividing where the product with the reciprocal
 // (off by less than 3e-6) is not that near to a tie
@@ -104,30 +159,45 @@ __device__ __forceinline__ float quotient(float w, float s, float inv) {
   return fminf(fmaxf(r, -8.f), 7.f);
 }
 
-// Block of 32 values in 8 neighbouring lanes -> this lane's four codes (code j in bits 4 j ..) and the block's scale bits.
-template <int FMT>
-__device__ __forceinline__ uint32_t encode(float4 y, uint32_t& scale) {
-  float w[4] = {sane(y.x), sane(y.y), sane(y.z), sane(y.w)};
-  float amax = fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3])));
+// Block of 32 values in 32 / E neighbouring lanes -> this lane's codes (code j in bits 4 j ..) and the block's scale bits.
+template <int FMT, int E>
+__device__ __forceinline__ uint32_t encode(const Vals<E>& y, uint32_t& scale) {
+  float w[E], amax = fabsf(y.v[0]);
 #pragma unroll
-  for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  for (int j = 0; j < E; ++j) w[j] = y.v[j];
+#pragma unroll
+  for (int j = 1; j < E; ++j) amax = max_or_nan(amax, fabsf(w[j]));
+  if (!(amax <= kClamp)) {            // (NaN too)
+    amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      w[j] = sane(w[j]);
+      amax = fmaxf(amax, fabsf(w[j]));
+    }
+  }
+#pragma unroll
+  for (int o = 16 / E; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   uint32_t codes = 0;
   if (FMT == MOE_FMT_MXFP4) {
     // e = clamp(k + 127, 1, 254), k the smallest integer with amax <= 6 * 2^k: from the exponent, one more if the
     // mantissa exceeds 1.5
     const uint32_t ab = __float_as_uint(amax);
     int e = (int)(ab >> 23) - 2 + ((ab & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    e = e < 1 ? 1 : e;   // e <= 190 for |w| <= 2^64
-    const int h = (127 - e) >> 1;
-    const float s1 = exp2i(h), s2 = exp2i(127 - e - h);   // w 2^(127 - e) by two exact powers of two
+    e = e < 1 ? 1 : e;                // e <= 190 for |w| <= 2^64: 2^(127 - e) is a normal number, the products exact
+    const float s = exp2i(127 - e);
     // nearest magnitude, ties to the even code, signs kept: the hardware's rounding to E2M1 (the second operand goes low)
-    asm("{\n\t.reg .b8 a, b, z;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "mov.b32 %0, {a, b, a, b};\n\t}"
-        : "=r"(codes)
-        : "f"(w[0] * s1 * s2), "f"(w[1] * s1 * s2), "f"(w[2] * s1 * s2), "f"(w[3] * s1 * s2));
-    codes &= 0xFFFFu;
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      uint32_t c;
+      asm("{\n\t.reg .b8 a, b, z;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+          "mov.b32 %0, {a, b, a, b};\n\t}"
+          : "=r"(c)
+          : "f"(w[j] * s), "f"(w[j + 1] * s), "f"(w[j + 2] * s), "f"(w[j + 3] * s));
+      codes |= j ? c << 16 : c & 0xFFFFu;
+    }
     scale = (uint32_t)e;
   } else {
+    static_assert(FMT == MOE_FMT_MXFP4 || E == 4, "the INT4 sums are laid out over 8 lanes");
     // Six candidate scales: each lane forms its four squared errors for all (two padding candidates never win), then
     // three exchanges add the 8 lanes' in the promised order (i with i + 16, + 8, + 4) while halving the candidates a
     // lane holds, so that lane l of the block ends with candidate l: 28 shuffles instead of 72.
@@ -196,35 +266,37 @@ __device__ __forceinline__ void store_scale(uint8_t* p, uint32_t s) {
   else *reinterpret_cast<uint16_t*>(p) = (uint16_t)s;
 }
 
-__device__ __forceinline__ uint32_t spread_nibbles(uint32_t c) {   // 16 bits of four codes -> one code per byte
+__device__ __forceinline__ uint32_t spread_nibbles(uint32_t c) {   // the low 16 bits' four codes -> one code per byte
   return (c & 0xFu) | ((c & 0xF0u) << 4) | ((c & 0xF00u) << 8) | ((c & 0xF000u) << 12);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int E>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(Args a, AppendArgs g) {
   using S = Sub<FMT, D>;
-  constexpr int LPR = D / 4, RPW = 32 / LPR;   // lanes per row, rows per warp
+  constexpr int LPR = D / E, RPW = 32 / LPR, LPB = 32 / E;   // lanes per row, rows per warp, lanes per block
+  constexpr int W = E / 4;                                   // V words of a lane
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int t = (int)(w / g.chunks), chunk = (int)(w % g.chunks);
   if (t >= a.n_tokens) return;
-  const int l = lane % LPR, sub = lane / LPR, blk = l >> 3, r = l & 7;   // this lane's place in its row
+  const int l = lane % LPR, sub = lane / LPR, blk = l / LPB, r = l % LPB;   // this lane's place in its row
   // row groups: first q's, then k's, then v's
   const int gq = (g.q_heads + RPW - 1) / RPW, gk = (a.kv_heads + RPW - 1) / RPW;
   const int g0 = chunk * g.per_warp;
   int g1 = min(gq + 2 * gk, g0 + g.per_warp);
-  const uint16_t* qp = g.q + (int64_t)t * g.q_stride + 4 * l;
-  const uint16_t* kp = g.k + (int64_t)t * g.k_stride + 4 * l;
-  const uint16_t* vp = g.v + (int64_t)t * g.v_stride + 4 * l;
+  const uint16_t* qp = g.q + (int64_t)t * g.q_stride + E * l;
+  const uint16_t* kp = g.k + (int64_t)t * g.k_stride + E * l;
+  const uint16_t* vp = g.v + (int64_t)t * g.v_stride + E * l;
+  uint16_t* qo = g.q_out + (int64_t)t * g.q_heads * D + E * l;
   constexpr int U = 4;   // row groups whose loads are in flight
-  float4 xs[U];
+  Vals<E> xs[U];
   auto load_rows = [&](int gb) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int gi = gb + u;
       const int h = (gi < gq ? gi : gi < gq + gk ? gi - gq : gi - gq - gk) * RPW + sub;
       const uint16_t* p = gi < gq ? qp : gi < gq + gk ? kp : vp;
-      xs[u] = gi < g1 && h < (gi < gq ? g.q_heads : a.kv_heads) ? load4_bf16(p + h * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      xs[u] = gi < g1 && h < (gi < gq ? g.q_heads : a.kv_heads) ? load_bf16<E>(p + h * D) : no_values<E>();
     }
   };
   load_rows(g0);         // (on the way during the lookups)
@@ -247,15 +319,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(Args a, AppendAr
     const int id = check_page(a, __ldg(a.block_table + (int64_t)b * a.table_stride + pg), there);
     base += (int64_t)id * a.page_stride + (int64_t)((pos - pg * a.page_tokens) >> 4) * S::BYTES;
   }
-  const int64_t head_stride = (int64_t)(a.page_tokens / 16) * S::BYTES;
+  const uint32_t head_stride = (uint32_t)(a.page_tokens / 16) * S::BYTES;   // (a page has less than 2^31 bytes)
   // MXFP4 V bytes hold an even and an odd token. If both are new in this call, the even token's warp writes both;
   // otherwise the neighbour's half is read and kept.
   const bool odd = slot & 1;
   const bool mate_new = FMT == MOE_FMT_MXFP4 && pos >= 0 && (odd ? j > 0 && pos > 0 : j + 1 < sq.qn);
-  const Turn turn = load_turn(l, g.rope_dim, g.interleaved, cs, sn);
+  const Turn<E> turn = load_turn<E>(l, g.rope_dim, g.interleaved, cs, sn);
   if (there && odd && mate_new) g1 = min(g1, gq + gk);   // the even token's warp writes v
-  const int k_word = slot * (D / 2) + ((r >> 1) * S::NB + blk) * 4, scale_at = (slot * S::NB + blk) * S::SB;
-  const int v_word = S::VC + ((((slot >> 3) * 8 + r) * 4 + ((slot >> 1) & 3)) * S::NB + blk) * 4;
+  const int k_word = slot * (D / 2) + ((r * E / 8) * S::NB + blk) * 4, scale_at = (slot * S::NB + blk) * S::SB;
+  const int v_word = S::VC + ((((slot >> 3) * 8 + r * W) * 4 + ((slot >> 1) & 3)) * S::NB + blk) * 4;
+  constexpr int V_STEP = 4 * S::NB;                        // words from one of a lane's V words to the next
   for (int gb = g0; gb < g1; gb += U) {
     if (gb > g0) load_rows(gb);
 #pragma unroll
@@ -264,48 +337,55 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(Args a, AppendAr
       if (gi >= g1) break;
       if (gi < gq) {
         const int h = gi * RPW + sub;
-        const float4 y = g.rope_dim ? rotate(xs[u], turn) : xs[u];
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
-        if (h < g.q_heads)
-          *reinterpret_cast<uint2*>(g.q_out + ((int64_t)t * g.q_heads + h) * D + 4 * l) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        const Vals<E> y = g.rope_dim ? rotate(xs[u], turn) : xs[u];
+        if (h < g.q_heads) store_bf16<E>(qo + h * D, y);
         continue;
       }
       if (!there) break;
       uint32_t scale;
       if (gi < gq + gk) {
         const int h = (gi - gq) * RPW + sub;
-        const float4 y = g.rope_dim ? rotate(xs[u], turn) : xs[u];
-        const uint32_t codes = encode<FMT>(y, scale);
-        // a lane pair's 32-bit word (dimensions 32 blk + 8 c .. + 7, c = r / 2)
-        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, codes, 1);
+        const Vals<E> y = g.rope_dim ? rotate(xs[u], turn) : xs[u];
+        const uint32_t codes = encode<FMT, E>(y, scale);
+        // a 32-bit word is dimensions 32 blk + 8 c .. + 7: one lane's, or a lane pair's
+        const uint32_t other = E == 4 ? __shfl_xor_sync(0xFFFFFFFFu, codes, 1) : 0u;
         if (h < a.kv_heads) {
-          uint8_t* sb = base + (int64_t)h * head_stride;
-          if (!(r & 1)) *reinterpret_cast<uint32_t*>(sb + k_word) = codes | (other << 16);
+          uint8_t* sb = base + (uint32_t)h * head_stride;
+          if (E == 8) *reinterpret_cast<uint32_t*>(sb + k_word) = codes;
+          else if (!(r & 1)) *reinterpret_cast<uint32_t*>(sb + k_word) = codes | (other << 16);
           if (r == 0) store_scale<FMT>(sb + S::KS + scale_at, scale);
         }
         continue;
       }
       const int h = (gi - gq - gk) * RPW + sub;
       const bool have = h < a.kv_heads;
-      uint8_t* sb = base + (int64_t)(have ? h : 0) * head_stride;
+      uint8_t* sb = base + (uint32_t)(have ? h : 0) * head_stride;
       uint32_t* word = reinterpret_cast<uint32_t*>(sb + v_word);
       if (FMT == MOE_FMT_INT4G32) {
-        const uint32_t codes = encode<FMT>(xs[u], scale);
+        const uint32_t codes = encode<FMT, E>(xs[u], scale);
         if (have) reinterpret_cast<uint16_t*>(word)[odd] = (uint16_t)codes;
       } else if (mate_new) {   // (this is the even token)
-        const float4 z = have ? load4_bf16(vp + g.v_stride + h * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint32_t codes = encode<FMT>(xs[u], scale);
+        const Vals<E> z = have ? load_bf16<E>(vp + g.v_stride + h * D) : no_values<E>();
+        const uint32_t codes = encode<FMT, E>(xs[u], scale);
         uint32_t scale2;
-        const uint32_t codes2 = encode<FMT>(z, scale2);
+        const uint32_t codes2 = encode<FMT, E>(z, scale2);
         if (have) {
-          *word = spread_nibbles(codes) | (spread_nibbles(codes2) << 4);
+#pragma unroll
+          for (int i = 0; i < W; ++i) word[i * V_STEP] = spread_nibbles(codes >> (16 * i)) | (spread_nibbles(codes2 >> (16 * i)) << 4);
           if (r == 0) store_scale<FMT>(sb + S::VS + scale_at + S::NB * S::SB, scale2);
         }
       } else {
-        const uint32_t old = *word;   // the neighbour's half, on the way while this row is encoded
-        const uint32_t codes = encode<FMT>(xs[u], scale);
-        if (have) *word = odd ? (old & 0x0F0F0F0Fu) | (spread_nibbles(codes) << 4) : (old & 0xF0F0F0F0u) | spread_nibbles(codes);
+        uint32_t old[W];       // the neighbour's half, on the way while this row is encoded
+#pragma unroll
+        for (int i = 0; i < W; ++i) old[i] = word[i * V_STEP];
+        const uint32_t codes = encode<FMT, E>(xs[u], scale);
+        if (have) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const uint32_t c = spread_nibbles(codes >> (16 * i));
+            word[i * V_STEP] = odd ? (old[i] & 0x0F0F0F0Fu) | (c << 4) : (old[i] & 0xF0F0F0F0u) | c;
+          }
+        }
       }
       if (have && r == 0) store_scale<FMT>(sb + S::VS + scale_at, scale);
     }
@@ -422,11 +502,15 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const moe_kv_
   a.status = &((WsHeader*)ws)->status;
   kv::AppendArgs g{(const uint16_t*)k, (const uint16_t*)v, (const uint16_t*)q, k_stride, v_stride, q_stride,
                    (uint16_t*)q_out, cos, sin, q ? q_heads : 0, rope_dim, rope_rows, interleaved ? 1 : 0, 0, 0};
-  const int rpw = 128 / D;   // rows of a group
+  const bool eight = cache->fmt == MOE_FMT_MXFP4 && (interleaved || rope_dim % 16 == 0);   // (half a rotation is whole lanes)
+  const int rpw = 32 * (eight ? 8 : 4) / D;   // rows of a group
   kv::split(batch->n_tokens, (g.q_heads + rpw - 1) / rpw + 2 * ((cache->kv_heads + rpw - 1) / rpw), &g.per_warp, &g.chunks);
   const int64_t warps = (int64_t)batch->n_tokens * g.chunks, ctas = (warps + 3) / 4;
   if (ctas > 0x7FFFFFFF) return MOE_ERR_SHAPE;
-#define KV_CALL(F, DD) kv::append_kernel<F, DD><<<(unsigned)ctas, kv::kAppendThreads, 0, (cudaStream_t)stream>>>(a, g)
+  const cudaStream_t s = (cudaStream_t)stream;
+#define KV_CALL(F, DD)                                                                                              \
+  if (eight) kv::append_kernel<F, DD, F == MOE_FMT_MXFP4 ? 8 : 4><<<(unsigned)ctas, kv::kAppendThreads, 0, s>>>(a, g); \
+  else kv::append_kernel<F, DD, 4><<<(unsigned)ctas, kv::kAppendThreads, 0, s>>>(a, g)
   KV_DISPATCH(KV_CALL);
 #undef KV_CALL
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
