@@ -9,8 +9,9 @@
 // D / E lanes hold a row, E values each. MXFP4, E = 8: a block is 4 neighbouring lanes, its maximum two shuffles, a K word one
 // lane's codes, two V words one lane's. INT4, E = 4: its six candidates' sums are spread over 8 lanes. (MXFP4 has E = 4 too, for
 // halves of the rotated part that are no multiple of 8.) A warp takes 32 E / D rows of one kind (q, k or v) at a time, and several
-// such groups of its token in turn when there are many tokens: the token's lookups and rotation are then shared, and four
+// such groups of its token in turn when there are many tokens: the token's lookups and rotation are then shared, and two
 // groups' loads are in flight.
+// (4 prompts of up to 5459 tokens, 16 + 2 x 16 heads of 64, MXFP4: append 69 us, read 34 us; 48 sequences of 8 tokens: 14 us.)
 #include "kv.cuh"
 
 namespace moe {
@@ -271,7 +272,7 @@ __device__ __forceinline__ uint32_t spread_nibbles(uint32_t c) {   // the low 16
 }
 
 template <int FMT, int D, int E>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(Args a, AppendArgs g) {
+__global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(Args a, AppendArgs g) {
   using S = Sub<FMT, D>;
   constexpr int LPR = D / E, RPW = 32 / LPR, LPB = 32 / E;   // lanes per row, rows per warp, lanes per block
   constexpr int W = E / 4;                                   // V words of a lane
@@ -288,7 +289,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(Args a, AppendAr
   const uint16_t* kp = g.k + (int64_t)t * g.k_stride + E * l;
   const uint16_t* vp = g.v + (int64_t)t * g.v_stride + E * l;
   uint16_t* qo = g.q_out + (int64_t)t * g.q_heads * D + E * l;
-  constexpr int U = 4;   // row groups whose loads are in flight
+  // Row groups whose loads are in flight; with 64 registers 32 warps fit an SM. Prompt of 18344 tokens, with the read back:
+  // 2 in 32 warps 104 us, 1 in 32 108, 4 in 24 118, 4 in 16 warps of 115 registers 116, 2 in 40 warps (spilling) 120.
+  constexpr int U = 2;
   Vals<E> xs[U];
   auto load_rows = [&](int gb) {
 #pragma unroll
