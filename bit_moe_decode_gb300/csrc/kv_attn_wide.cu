@@ -23,8 +23,8 @@
 // 467 us with kv_attn.cu; the cache is read at 1.4 TB/s.
 //
 // What the window of scales cannot hold (set from a pair's first tile: 12 powers of two down, 3 up), and weights below
-// 2^-21 in rows that have not yet seen 12 keys of 2^-16, are left to kv_attn.cu, whose passes keep them: the sequence is marked, and the
-// launch that follows does the marked ones again.
+// 2^-21 (binary16 has no full precision for them) in rows that have not yet seen 12 keys of 2^-20 are left to kv_attn.cu,
+// whose passes keep them: the sequence is marked, and the launch that follows does the marked ones again.
 #include "kv_attn.cuh"
 
 namespace moe {
@@ -36,7 +36,7 @@ constexpr int kThreads = (kWorkers + 2) * 32;
 // Weights are carried times 2^8, and a score may pass the running maximum by 7 (base 2) before it is raised: to raise it
 // stops all 64 rows for about 2,000 cycles, a tile's whole time, and binary16 holds 2^15.
 constexpr int kAnchor = 8;
-constexpr float kSlack = 7.f, kHeavyW = 0.00390625f, kLightW = 0.0001220703125f;   // 2^8 times 2^-16; 2^-13
+constexpr float kSlack = 7.f, kHeavyW = 0.000244140625f, kLightW = 0.0001220703125f;   // 2^8 times 2^-20 and 2^-21
 constexpr int kTileBatch = 4;       // tiles whose addresses the producer's lanes hold at a time
 
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -136,7 +136,7 @@ __device__ __forceinline__ int seq_tiles(const SeqInfo& s) {
   return s.qn > 0 && s.len > 0 ? ((s.len + 15) / 16 - s.sub0 + kTileSubs - 1) / kTileSubs : 0;
 }
 
-// A row's keys, counted until there are 12 of weight 2^-16 and more (low half); those of 2^-8 and more in the high half.
+// A row's keys, counted until there are 12 of weight 2^-20 and more (low half); those of 2^-12 and more in the high half.
 __device__ __forceinline__ bool few_keys(int cnt) { return (cnt & 0xFFFF) < 12; }
 
 // The rest of a wait: true if it ran out.
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
           const float m_new = fmaxf(m, top - kAnchor), al = ex2(m - m_new);
           s_neg[n] = -m_new;
           s_al[n] = al;
-          // after a raise by up to 2^8 the keys of more than 2^-8 still have more than 2^-16
+          // after a raise by up to 2^8 the keys of more than 2^-12 still have more than 2^-20
           const int cnt = al == 1.f ? s_cnt[n] : al < 0.00390625f ? 0 : s_cnt[n] >> 16;
           s_cnt[n] = cnt;
           few = s_lim[n] > 0 && few_keys(cnt);
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
         add2(l[x], t[x]);
       }
       if (rarely(!settled)) {
-        // until a row has 12 keys of weight 2^-16 and more, its weights below 2^-21 go to the other kernel
+        // until a row has 12 keys of weight 2^-20 and more, its weights below 2^-21 go to the other kernel
         int n = 0;
 #pragma unroll
         for (int x = 0; x < C; ++x) {
