@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   if (tid < runs) {
     const Run ru = s_run[tid];
     if (!ru.whole) {
-      uint32_t* cnt = g.counters + ru.b * Hkv + ru.h;
+      uint32_t* cnt = g.counters + first_cta(prefix[ru.b] + (long long)ru.h * (seq_units(info[ru.b]) + kPairCost) + kPairCost, W, G);
       const uint32_t n = (uint32_t)(ru.u1 - ru.u0);
       if (atom_acq_rel_add(cnt, n) + n == (uint32_t)seq_units(info[ru.b])) {
         *cnt = 0;
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     const int units = seq_units(sj);
     // the CTAs that hold the pair's first and last unit; CTA i's run begins at i W / G
     const long long p0 = prefix[ru.b] + (long long)ru.h * (units + kPairCost) + kPairCost;
-    const int c0 = (int)(((p0 + 1) * G - 1) / W), n = (int)(((p0 + units) * G - 1) / W) - c0 + 1;
+    const int c0 = first_cta(p0, W, G), n = (int)(((p0 + units) * G - 1) / W) - c0 + 1;
     // parts in batches: a batch's loads are all in flight, then the sums move to its maximum
     for (int t = tid; t < rows_all * (D / 4); t += THREADS) {
       const int d = t % (D / 4) * 4, row = t / (D / 4), j = token_of(row);
@@ -923,6 +923,10 @@ using namespace moe;
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// What a call leaves at zero (counters, marks) lies at the same place for every batch, so that batches of different sizes can
+// share a workspace.
+static const size_t kZeroBytes = up256((kv::kMaxCtas + kv::kMaxSeqs + 2) * 4);
+
 extern "C" size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t q_heads) {
   if (kv::check_cache(cache) != MOE_OK || kv::check_sizes(batch) != MOE_OK) return 0;
   if (q_heads < 1 || q_heads > 4096 || q_heads % cache->kv_heads) return 0;
@@ -930,8 +934,7 @@ extern "C" size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_
   if (batch->max_q > 8 || rows > kv::kMaxRows) return sizeof(WsHeader);   // append and read only
   const kv::Shape s = kv::shape_for((int)rows);
   const size_t row_bytes = (size_t)(cache->head_dim + 2) * 4;
-  return sizeof(WsHeader) + up256((size_t)batch->n_seqs * cache->kv_heads * 2 * 4) +
-         up256((size_t)(batch->n_seqs + 2) * 4) + up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
+  return sizeof(WsHeader) + kZeroBytes + up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
 }
 
 extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, const void* q,
@@ -961,9 +964,8 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   uint8_t* w = (uint8_t*)ws + sizeof(WsHeader);
   kv::AttnArgs g{(const uint16_t*)q, q_stride, q_heads, group, window, s.row_groups, 0, 65535u / (uint32_t)group + 1u, 0, scale * 1.4426950408889634f,
                  (uint16_t*)out, lse, (uint32_t*)w, nullptr, nullptr, nullptr};
-  w += up256((size_t)batch->n_seqs * cache->kv_heads * 2 * 4);
-  g.redo = (uint32_t*)w;
-  w += up256((size_t)(batch->n_seqs + 2) * 4);
+  g.redo = g.counters + kv::kMaxCtas;
+  w += kZeroBytes;
   g.warp_parts = (float*)w;
   w += up256(kv::kMaxCtas * s.warps * 8 * s.nt * (size_t)(cache->head_dim + 2) * 4);
   g.cta_parts = (float*)w;

@@ -21,7 +21,7 @@ struct AttnArgs {
   float scale_log2;                 // scale * log2(e)
   uint16_t* out;
   float* lse;
-  uint32_t* counters;               // [n_seqs * kv_heads]
+  uint32_t* counters;               // [CTAs], by the CTA in which a pair begins that others go on with (one pair at most)
   float* warp_parts;                // [CTAs][warps] partials of runs that end inside a warp's range
   float* cta_parts;                 // [CTAs][2]
   uint32_t* redo;                   // [n_seqs] sequences that kv_attn_wide.cu leaves to kv_attn.cu, whether any, CTAs that know
@@ -102,6 +102,9 @@ __device__ __forceinline__ long long share(long long x, long long W, long long n
   const unsigned long long p = (unsigned long long)x * W;
   return p >> 32 ? (long long)(p / (unsigned long long)n) : (long long)((uint32_t)p / (uint32_t)n);
 }
+
+// The CTA whose share has place x of the list
+__device__ __forceinline__ int first_cta(long long x, long long W, int G) { return (int)(((x + 1) * G - 1) / W); }
 
 // A row's joined values of four dimensions, written out
 template <int D>

@@ -750,7 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     if (tid < 2 && s_used[tid] >= 0) {
       const int pb = s_used[tid] / Hv;
       const uint32_t n = (uint32_t)s_tiles[tid];
-      uint32_t* cnt = g.counters + s_used[tid];
+      const long long p0 = prefix[pb] + (long long)(s_used[tid] % Hv) * (seq_tiles(info[pb]) + kPairTiles) + kPairTiles;
+      uint32_t* cnt = g.counters + first_cta(p0, W, G);
       if (atom_acq_rel_add(cnt, n) + n == (uint32_t)seq_tiles(info[pb])) {
         *cnt = 0;
         s_last[tid] = 1;
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
       const int pb = s_used[k] / Hv, ph = s_used[k] % Hv, tiles = seq_tiles(info[pb]);
       const SeqInfo sj = info[pb];
       const long long p0 = prefix[pb] + (long long)ph * (tiles + kPairTiles) + kPairTiles;
-      const int c0 = (int)(((p0 + 1) * G - 1) / W), n = (int)(((p0 + tiles) * G - 1) / W) - c0 + 1;
+      const int c0 = first_cta(p0, W, G), n = (int)(((p0 + tiles) * G - 1) / W) - c0 + 1;
       for (int t = tid; t < N * (D / 4); t += kWorkers * 32) {
         const int d = t % (D / 4) * 4, nr = t / (D / 4), row = (ph % RG) * N + nr, j = (int)((uint32_t)row * g.group_inv >> 16);
         if (j >= sj.qn) continue;

@@ -332,7 +332,7 @@ size_t moe_kv_page_bytes(moe_format_t fmt, int32_t head_dim, int32_t kv_heads, i
 
 /* Workspace of moe_kv_append / _read / _attention for batches of up to batch->n_seqs sequences of up to batch->max_q rows
  * and q_heads query heads (0 for unsupported sizes). Zero it once with moe_workspace_init(); the calls leave it ready for
- * the next one. Calls that overlap on the GPU must not share a workspace. Its first word is the device status word
+ * the next one, of any batch that it is large enough for. Calls that overlap on the GPU must not share a workspace. Its first word is the device status word
  * (moe_get_device_status): MOE_ERR_INVALID_ARG for device data out of range (rows that are not in the call's tensors,
  * more rows than max_q, a length beyond the table, a page id outside [0, n_pages), a position beyond the rotation
  * tables). Nothing out of range is accessed then: such a sequence counts as empty (attention: zeros, lse -inf, as far as
@@ -368,9 +368,10 @@ moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
  *   out [n_tokens, q_heads, D] bf16 = sum_s softmax(x)_s v_s, lse [n_tokens, q_heads] fp32 = log sum_s exp(x_s) (natural;
  *   NULL: not wanted). A row that sees no key gives zeros and -inf.
  *   Numerics: q scaled by a power of two into binary16 (exact within 2^-28 of the row's largest), codes exact, block scales
- *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s times the value scales, brought into
- *   binary16's range by powers of two that follow the scales, are rounded to binary16 (2^-11 relative, for products down to
- *   2^-26 of the largest, smaller ones too while a row has fewer than 12 keys of some weight).
+ *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s (up to 16 query rows a KV head: times the
+ *   value scales), brought into binary16's range by powers of two, are rounded to binary16 (2^-11 relative; for products
+ *   down to 2^-26 of the largest, or weights down to 2^-22, smaller ones too while a row has fewer than 12 keys of some weight).
+ *   Launches: one, or two where the rows are more than 16 and the table leaves room for long sequences.
  *   q 16-byte aligned with a stride multiple of 8; max_q <= 8, max_q * q_heads / kv_heads <= 128. Scales of blocks that
  *   moe_kv_append writes are finite and below 2^64; other contents must keep to that.
  *   The result of a row does not depend on when CTAs run (partial results are joined in a fixed order). */
