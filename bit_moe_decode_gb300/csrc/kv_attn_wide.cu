@@ -664,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
           const uint32_t top = __ballot_sync(0xFFFFFFFFu, t[x / 2][x & 1] >= 256.f * kHeavyW);
           if (lane == x) n = __popc(heavy) | __popc(top) << 16;
         }
-        if (n && few_keys(s_cnt[col0 + lane % C])) atomicAdd(s_cnt + col0 + lane % C, n);
+        const bool counts = few_keys(s_cnt[col0 + lane % C]);
+        named_bar(1 + group, 128);                       // (whether a warp's keys count does not depend on who is first)
+        if (n && counts) atomicAdd(s_cnt + col0 + lane % C, n);
         named_bar(1 + group, 128);
         bool light = false, few = false;
 #pragma unroll
