@@ -60,6 +60,8 @@ __device__ __forceinline__ void add2(float (&d)[2], const float (&a)[2]) {
       : "+f"(d[0]), "+f"(d[1])
       : "f"(a[0]), "f"(a[1]));
 }
+// a shared memory address as a pointer (arithmetic on 32-bit addresses costs half of that on pointers)
+__device__ __forceinline__ uint8_t* at_shared(uint32_t addr) { return static_cast<uint8_t*>(__cvta_shared_to_generic(addr)); }
 template <int C>
 __device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[C]) {
   if (C == 8) {
@@ -383,19 +385,20 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     // K rows: a lane writes 8 dimensions of one key per block; lanes 4 to 7 of eight have the row four on, so that eight lanes
     // fill all banks
     const int rk = (r & 1) * 4 + (r >> 1), tk = 8 * half + rk;
-    const uint32_t k_at = (uint32_t)(8 * warp + rk) * 128 + (uint32_t)((c ^ rk) << 4);
+    const uint32_t smem_at = smem_u32(smem), sub_at = smem_at + L::RING + (warp >> 1) * S::BYTES;
+    const uint32_t k_at = smem_at + L::K + (uint32_t)(8 * warp + rk) * 128 + (uint32_t)((c ^ rk) << 4);
     // V rows: dimension 32 b + 4 r + j, j = (i + r / 2) % 4 at step i (again: all banks), tokens 2 c, 2 c + 1 of the eight
     const int rot = r >> 1;
     uint32_t v_at[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = 4 * r + ((i + rot) & 3);
-      v_at[i] = (uint32_t)(warp >> 3) * 16384 + d * 128 + (((warp & 7) ^ (d & 7)) << 4) + 4 * c;
+      v_at[i] = smem_at + L::V + (uint32_t)(warp >> 3) * 16384 + d * 128 + (((warp & 7) ^ (d & 7)) << 4) + 4 * c;
     }
     // ---- keys (and, with a new pair's first tile, its windows and its q) of tile i
     auto convert_keys = [&](int i) {
       wait(bar_ring_full + stage, phase);
-      const uint8_t* sb = ring + stage * L::TILE + (warp >> 1) * S::BYTES;
+      const uint8_t* sb = at_shared(sub_at + stage * L::TILE);
       if (cfirst) {
         const SeqInfo si = info[cb];
         key0 = (si.sub0 + cu * kTileSubs) * 16 + 8 * warp;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
         }
         named_bar(15, kWorkers * 32);                    // (s_exp is free again)
       }
-      uint8_t* kop = smem + L::K + (i & 1) * L::K_OP;
+      const uint32_t k_to = k_at + (i & 1) * L::K_OP;
       uint32_t wd[NB], us[NB], o = 0;
       load_words<NB>(wd, sb + S::KC + tk * (D / 2) + c * (4 * NB));
       if (FMT == MOE_FMT_MXFP4) {
@@ -501,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
       off = key0 + rk < len && key0 + rk >= min_lo ? o : 0u;
 #pragma unroll
       for (int y = 0; y < NB; y += 2) {
-        *reinterpret_cast<uint4*>(kop + (y >> 1) * 16384 + k_at) = convert8<FMT>(wd[y], us[y]);
-        *reinterpret_cast<uint4*>(kop + (y >> 1) * 16384 + (k_at ^ 64u)) = convert8<FMT>(wd[y + 1], us[y + 1]);
+        *reinterpret_cast<uint4*>(at_shared(k_to + (y >> 1) * 16384)) = convert8<FMT>(wd[y], us[y]);
+        *reinterpret_cast<uint4*>(at_shared((k_to ^ 64u) + (y >> 1) * 16384)) = convert8<FMT>(wd[y + 1], us[y + 1]);
       }
       fence_async_smem();
       tc_fence_before();                                 // (the scores of tile i - 2 have been read)
@@ -511,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     };
     // ---- values of tile i; then the conversion moves on to the next
     auto convert_values = [&](int i) {
-      const uint8_t* sb = ring + stage * L::TILE + (warp >> 1) * S::BYTES;
-      uint8_t* vop = smem + L::V + (i & 1) * L::V_OP;
+      const uint8_t* sb = at_shared(sub_at + stage * L::TILE);
+      const uint32_t v_to = (i & 1) * L::V_OP;
       uint32_t drop = 0, u[NB], wd[NB];
       if (key0 + 8 > len || key0 < min_lo) {
         const int key = key0 + 2 * c;
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
         for (int k = 0; k < 4; ++k) {
           const uint32_t v = FMT == MOE_FMT_MXFP4 ? e2m1x2_to_f16x2(x, k)
                                                   : hadd2_bits(lop3_and_xor(x >> (4 * ((k + rot) & 3)), 0x000F000Fu, 0x64086408u), 0xE408E408u);
-          *reinterpret_cast<uint32_t*>(vop + y * 4096 + v_at[k]) = hmul2_bits(v, u[y]);
+          *reinterpret_cast<uint32_t*>(at_shared(v_at[k] + v_to + y * 4096)) = hmul2_bits(v, u[y]);
         }
       }
       if (__any_sync(0xFFFFFFFFu, off & kOff<FMT>) && lane == 0) g.redo[cb] = g.redo[a.n_seqs] = 1;
@@ -553,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     int ev = 0, min_lim = 0, max_lo = 0;
     const int wnd = g.window > 0 ? g.window : 0x3FFFFFFF;
     const uint32_t p_swizzle = N == 64 ? key_in & 7 : key_in >> 1 & 3;
-    uint8_t* p_row = smem + L::P + key_in * (2 * N) + (((uint32_t)(col0 / 8) ^ p_swizzle) << 4);
-    uint8_t* p_row2 = smem + L::P + key_in * (2 * N) + (((uint32_t)(col0 / 8 + 1) ^ p_swizzle) << 4);
+    const uint32_t p_row = smem_at + L::P + key_in * (2 * N) + (((uint32_t)(col0 / 8) ^ p_swizzle) << 4);
     int k0 = 0;
     for (int i = 0; i < todo; ++i) {
       if (i + 1 < todo) convert_keys(i + 1);
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
       if (i > 0) wait(&bar_done, (i - 1) & 1);           // P and V's other operand are free
 #pragma unroll
       for (int y = 0; y < C / 8; ++y)
-        *reinterpret_cast<uint4*>(y ? p_row2 : p_row) = make_uint4(pack_f16(t[4 * y][0], t[4 * y][1]), pack_f16(t[4 * y + 1][0], t[4 * y + 1][1]),
+        *reinterpret_cast<uint4*>(at_shared(p_row ^ (16u * y))) = make_uint4(pack_f16(t[4 * y][0], t[4 * y][1]), pack_f16(t[4 * y + 1][0], t[4 * y + 1][1]),
                                                                    pack_f16(t[4 * y + 2][0], t[4 * y + 2][1]), pack_f16(t[4 * y + 3][0], t[4 * y + 3][1]));
       fence_async_smem();
       __syncwarp();
