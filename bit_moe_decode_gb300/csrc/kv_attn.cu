@@ -101,10 +101,14 @@ __device__ __forceinline__ int seq_units(const SeqInfo& s) {
 }
 
 // A pair's place in the list of work: kPairCost, then its units.
-constexpr int kPairCost = 1;
+// (Measured in units of a warp: decode 256 x 600 47.6, 45.6, 44.6, 45.1 us at 1, 2, 3, 4; 16 rows, 64 x 8192, 124, 129, 135 us
+// at 1, 2, 3, where two warps or more share the units.)
+template <int NT>
+constexpr int pair_cost = NT == 1 ? 3 : 1;
+template <int NT>
 __device__ __forceinline__ int seq_cost(const SeqInfo& s) {
   const int u = seq_units(s);
-  return u ? u + kPairCost : 0;
+  return u ? u + pair_cost<NT> : 0;
 }
 struct Prod {        // a warp's producer: the next batch is n units (subs sub-blocks from `sub` on) at unit u of a pair; left
   int b, h, u, units, left, n, subs, sub;   // counts the units from it on
@@ -123,6 +127,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   constexpr int PART = ROWS * (D + 2);                   // floats of a warp's partial: o [ROWS][D], m [ROWS], l [ROWS]
   constexpr int NVC = FMT == MOE_FMT_MXFP4 ? 1 : NB;
   constexpr float kVal = FMT == MOE_FMT_INT4G32 ? 16777216.f : 1.f;   // 2^24 of the INT4 fragments
+  constexpr int kPairCost = pair_cost<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Entry s_entry[2 * NW];
   __shared__ Run s_run[2 * NW];
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       if (NT > 1 && g.redo && __ldcg(g.redo + b) == 0) si.qn = 0;
       if (g.window > 0 && sq.len - sq.qn - g.window + 1 > 0) si.sub0 = (sq.len - sq.qn - g.window + 1) / 16;
       info[b] = si;
-      x = (long long)seq_cost(si) * Hkv;
+      x = (long long)seq_cost<NT>(si) * Hkv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -610,9 +615,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       }
     bool wide = off & kOff<FMT>;
     if (rarely(!settled)) {
-      // keys of weight 2^-14 and more per row, four counts in an int, over the lanes that share the rows
-      int n = 0;
-      bool light = false;
+      // heavy keys per row, four counts in an int, over the lanes that share the rows; and the rows with light ones
+      int n = 0, light = 0;
 #pragma unroll
       for (int i = 0; i < SUBS; ++i)
 #pragma unroll
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             n += (s[i][nt][e] >= kHeavy ? 1 : 0) << (8 * (2 * nt + (e & 1)));
-            light |= s[i][nt][e] > 0.f && s[i][nt][e] < kLight;
+            light |= (s[i][nt][e] > 0.f && s[i][nt][e] < kLight ? 1 : 0) << (2 * nt + (e & 1));
           }
 #pragma unroll
       for (int i = 4; i < 32; i <<= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, i);
@@ -629,10 +633,11 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       for (int k = 0; k < 2 * NT; ++k) {
         const int sum = min(128, (heavy >> (8 * k) & 255) + (n >> (8 * k) & 255));
         heavy = (heavy & ~(255 << (8 * k))) | sum << (8 * k);
-        all = all && (sum >= 12 || lim[k / 2][k % 2] == 0);
+        const bool few = sum < 12 && lim[k / 2][k % 2] != 0;
+        all = all && !few;
+        wide |= few && (light >> k & 1);
       }
       settled = __all_sync(0xFFFFFFFFu, all);
-      wide |= light && !settled;
     }
     if (rarely(__any_sync(0xFFFFFFFFu, wide))) {
       wide_products(base, s);
