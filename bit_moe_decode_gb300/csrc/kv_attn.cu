@@ -6,16 +6,19 @@
 // What bounds it. A key of one KV head is 136 bytes (MXFP4, D = 128) of HBM traffic and 256 codes to convert. At the
 // measured 6.7 TB/s an SM gets 44 bytes per ns, so it has about 24 issue slots per warp-wide MMA (16 keys x 16
 // dimensions) and half as many in the integer pipe. Everything below serves to convert a code with as few instructions
-// as possible, once per 8 query rows.
+// as possible, once per 8 query rows. What it reaches: 64 sequences of up to 8192 keys, 8 rows a KV head (8 KV heads, D = 128,
+// MXFP4) 42.8 us, 3.4 TB/s (47 % of the issue slots, 44 % of the integer pipe); one of 262143 keys 76 us, 4.0 TB/s; one of
+// 517 keys 10.4 us, latency; 256 of up to 600, 1 row a KV head (16, D = 64, INT4) 44.5 us, pairs' starts and ends.
 //
-// Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, a pair's start counting as one unit more
+// Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, a pair's start counting as some units more
 // (what its queries and its output cost), and dealt out evenly: every warp of the grid streams one contiguous run (the
-// prefix sums over the sequences are formed by each CTA from the device's lengths, so a captured graph follows them). A warp copies its units with bulk copies (one per 16-token
-// sub-block, which the layout keeps contiguous) into its own ring and is its own consumer, so there is no barrier
-// between warps until the end. A pair that lies in several warps is joined from partial results, first inside the
-// CTA, then, if it spans CTAs, by the CTA that finishes last (a counter per pair, left at zero); always in the order of
+// prefix sums over the sequences are formed by each CTA from the device's lengths, so a captured graph follows them). A warp
+// copies its units with bulk copies (one per 16-token sub-block, which the layout keeps contiguous) into its own ring and
+// is its own consumer, so there is no barrier between warps until the end. A pair that lies in several warps is joined
+// from partial results, first inside the CTA, then, if it spans CTAs, by the CTA that finishes last (a counter, left at zero); always in the order of
 // the keys, so the bits do not depend on timing. More than 8 NT query rows: RG warps stream the same units, each
-// for its own rows (the copies then hit L2).
+// for its own rows (the copies then hit L2). Above 16 rows over long sequences kv_attn_wide.cu goes first, and this kernel
+// does again what that one marks.
 //
 // Arithmetic, for 16 keys x 8 rows at a time on mma.sync.m16n8k16 with the keys (then the dimensions) as the 16 rows,
 // so that a decode step's few query rows fill the 8 columns:
@@ -28,11 +31,11 @@
 //     scales vary along the contraction, so they go into the weights: p_s vscale_s, rounded to binary16 once.
 //   Range: the weights are carried as 2^12 p, at most 2^14 (m is raised only when a score passes m + 2), and the value
 //     scales as v 2^-E in binary16, exact within 2^-14 .. 2^2, with an E per block of 32 dimensions; the fp32
-//     accumulators hold 2^(12 - E) times the output. Products keep all 11 bits down to 2^-14. Where scales leave the window, E moves
-//     (accumulators rescaled, exactly) and the keys take passes: each adds the products of the next 26 powers of two at a
+//     accumulators hold 2^(12 - E) times the output. Products keep all 11 bits down to 2^-14. Where scales leave the window, E
+//     moves (accumulators rescaled, exactly) and the keys take passes: each adds the products of the next 26 powers of two at a
 //     scale of its own, so that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has
-//     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a dimension whose few heavy keys all have code 0 is
-//     made of such weights.
+//     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a
+//     dimension whose few heavy keys all have code 0 is made of such weights.
 #include "kv_attn.cuh"
 
 namespace moe {
@@ -979,7 +982,7 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   // Above 16 rows a KV head, and where the table and the window leave room for long sequences, kv_attn_wide.cu goes first; its
   // cost does not grow with the rows up to 64, but a pair's start costs it 3 tiles of 128 keys, this kernel none.
   // Measured, this kernel / that: 24 rows over 300 keys (256 sequences) 33 / 60 us; 18 rows over a window of 1024 (33)
-  // 54 / 49 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
+  // 54 / 48 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
   // 16 rows over 8192 (64) 124 / 178 us.
   int64_t keys = (int64_t)batch->table_stride * cache->page_tokens;
   if (window && keys > window + batch->max_q) keys = window + batch->max_q;

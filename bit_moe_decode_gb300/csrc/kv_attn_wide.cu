@@ -13,13 +13,13 @@
 // 16 warps convert and do the softmax, one copies packed tiles into a ring, one issues the products. Per tile a worker
 // warp converts eight tokens' keys of the next tile, does the softmax of this one (lane = key, N / 4 rows), then converts
 // the next tile's values: S of the next tile is formed during the softmax, O during the conversion. Splitting the
-// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this takes 242, most of it polling; one
-// hand-over to the tensor cores a tile instead of two (keys two tiles ahead) 246.
+// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this takes 237, most of it polling; one
+// hand-over to the tensor cores a tile instead of two (keys two tiles ahead) did no better.
 // P is stored with its rows contiguous (B transposed): a lane's key is then one or two 16-byte stores.
 //
 // What bounds it: instructions. A tile at N = 64 takes 3,500 cycles for about 510 warp instructions a worker
 // warp (58 % of the issue slots; the integer pipe is half, shared memory two thirds busy); its HBM share would take 800, the tensor
-// cores 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 242 us, against
+// cores 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 237 us, against
 // 467 us with kv_attn.cu; the cache is read at 1.4 TB/s.
 //
 // What the window of scales cannot hold (set from a pair's first tile: 12 powers of two down, 3 up), and weights below

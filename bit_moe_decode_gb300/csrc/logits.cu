@@ -7,7 +7,9 @@
 //
 // A row is split over a cluster of C CTAs; each holds its slice of x in shared memory between the passes, so that every
 // value is read and written once: x, then exponentials relative to the slice's maximum, then, after one exchange of
-// (maximum, first place, sum) through distributed shared memory, the output. C is the smallest of 1 .. 16 whose slices
+// (maximum, first place, sum) through distributed shared memory, the output. 256 x 131071 with counts: 125 us, 3.2 TB/s, the
+// phases of three CTAs an SM overlapping in part (512 threads in two CTAs 121, in three 128 to 148, and 1.3 us more for one
+// row); 4 x 8 x 32768: 8.8 us; 1 x 32768: 6.4 us, latency. C is the smallest of 1 .. 16 whose slices
 // fit kSlice and that gives the GPU enough CTAs. Only a vocabulary above 16 kSlice is walked in chunks that are formed
 // twice (once for the statistics, once for the output).
 // The few tokens that need more than their own element (earlier drafts, biases) are patched in shared memory, by the
