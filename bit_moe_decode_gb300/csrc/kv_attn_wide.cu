@@ -141,6 +141,20 @@ __device__ __forceinline__ int seq_tiles(const SeqInfo& s) {
 // A row's keys, counted until there are 12 of weight 2^-20 and more (low half); those of 2^-12 and more in the high half.
 __device__ __forceinline__ bool few_keys(int cnt) { return (cnt & 0xFFFF) < 12; }
 
+// Where scales have left the window (which spoils their neighbours in a word): one block's scale times 2^-E in binary16, for
+// `codes` of that block (those a lane has, other bits 0). Blocks of zeros have the smallest scale and need none; other scales
+// outside the window set `off`. minus_low: minus the window's lower end, as scale_pair takes it.
+template <int FMT>
+__device__ __forceinline__ uint32_t one_scale(const uint8_t* scale, uint32_t minus_low, uint32_t codes, uint32_t& off) {
+  int low = FMT == MOE_FMT_MXFP4 ? (int)((0u - minus_low) & 255) : (int)((0u - minus_low) >> 7 & 511);   // -12 .. 242
+  if (low > 242) low -= FMT == MOE_FMT_MXFP4 ? 256 : 512;
+  const int bits = FMT == MOE_FMT_MXFP4 ? (int)*scale << 7 : (int)*reinterpret_cast<const uint16_t*>(scale);
+  const int x = bits - (low << 7);
+  if ((uint32_t)x < 16u << 7) return (uint32_t)(x + 128) << 3;
+  if (codes & (FMT == MOE_FMT_MXFP4 ? 0x77777777u : 0xFFFFFFFFu)) off = kOff<FMT>;   // (a zero's sign does not count)
+  return 0;
+}
+
 // The rest of a wait: true if it ran out.
 __device__ __noinline__ bool wait_longer(uint64_t* bar, int parity, int32_t* status) {
   const long long t0 = globaltimer_ns();
@@ -501,6 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
           us[y] = us[y] * 8u + (kc * 8u + 0x04000400u);
         }
       }
+      if (rarely(o & kOff<FMT>)) {
+        o = 0;
+#pragma unroll
+        for (int y = 0; y < NB; ++y)
+          us[y] = one_scale<FMT>(sb + S::KS + (tk * NB + y) * S::SB, kc, wd[y], o) * 0x00010001u;
+      }
       off = key0 + rk < len && key0 + rk >= min_lo ? o : 0u;
 #pragma unroll
       for (int y = 0; y < NB; y += 2) {
@@ -522,7 +542,21 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
         drop = (key >= len || key < min_lo ? 1u : 0u) | (key + 1 >= len || key + 1 < min_lo ? 2u : 0u);
       }
       load_words<NB>(wd, sb + S::VC + (half * 32 + lane) * (4 * NB));
-      scale_pair<FMT, NB, NVC>(sb + S::VS + (8 * half + 2 * c) * (NB * S::SB), vc, u, off, drop);
+      uint32_t o = 0;
+      scale_pair<FMT, NB, NVC>(sb + S::VS + (8 * half + 2 * c) * (NB * S::SB), vc, u, o, drop);
+      if (rarely(o & kOff<FMT>)) {
+        o = 0;
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+          u[y] = 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (!(drop >> t & 1u))
+              u[y] |= one_scale<FMT>(sb + S::VS + ((8 * half + 2 * c + t) * NB + y) * S::SB, vc[0],
+                                     wd[y] & (FMT == MOE_FMT_MXFP4 ? 0x0F0F0F0Fu << (4 * t) : 0xFFFFu << (16 * t)), o) << (16 * t);
+        }
+      }
+      off |= o;
 #pragma unroll
       for (int y = 0; y < NB; ++y) {
         const uint32_t x = FMT == MOE_FMT_MXFP4 ? __funnelshift_r(wd[y], wd[y], 8 * rot) : wd[y];
