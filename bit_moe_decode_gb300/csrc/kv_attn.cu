@@ -982,7 +982,7 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   // Above 16 rows a KV head, and where the table and the window leave room for long sequences, kv_attn_wide.cu goes first; its
   // cost does not grow with the rows up to 64, but a pair's start costs it 3 tiles of 128 keys, this kernel none.
   // Measured, this kernel / that: 24 rows over 300 keys (256 sequences) 33 / 60 us; 18 rows over a window of 1024 (33)
-  // 54 / 48 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
+  // 54 / 49 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
   // 16 rows over 8192 (64) 124 / 178 us.
   int64_t keys = (int64_t)batch->table_stride * cache->page_tokens;
   if (window && keys > window + batch->max_q) keys = window + batch->max_q;

@@ -13,18 +13,20 @@
 // 16 warps convert and do the softmax, one copies packed tiles into a ring, one issues the products. Per tile a worker
 // warp converts eight tokens' keys of the next tile, does the softmax of this one (lane = key, N / 4 rows), then converts
 // the next tile's values: S of the next tile is formed during the softmax, O during the conversion. Splitting the
-// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this takes 237, most of it polling; one
+// workers' roles instead (8 warps converting, 16 in the softmax) took 287 us where this took 248, most of it polling; one
 // hand-over to the tensor cores a tile instead of two (keys two tiles ahead) did no better.
 // P is stored with its rows contiguous (B transposed): a lane's key is then one or two 16-byte stores.
 //
 // What bounds it: instructions. A tile at N = 64 takes 3,500 cycles for about 510 warp instructions a worker
 // warp (58 % of the issue slots; the integer pipe is half, shared memory two thirds busy); its HBM share would take 800, the tensor
-// cores 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 237 us, against
+// cores 510. Verify step of 16 sequences of up to 32768 keys, 64 rows a KV head (8 KV heads, D = 128, MXFP4): 249 us, against
 // 467 us with kv_attn.cu; the cache is read at 1.4 TB/s.
 //
 // What the window of scales cannot hold (set from a pair's first tile: 12 powers of two down, 3 up), and weights below
 // 2^-21 (binary16 has no full precision for them) in rows that have not yet seen 12 keys of 2^-20 are left to kv_attn.cu,
-// whose passes keep them: the sequence is marked, and the launch that follows does the marked ones again.
+// whose passes keep them: the sequence is marked, and the launch that follows does the marked ones again. Blocks of zeros,
+// whose scale is the smallest there is, are not left over (a tenth of the tokens zero: 276 us instead of 2,544); looking for
+// them costs 5 % where there are none.
 #include "kv_attn.cuh"
 
 namespace moe {
