@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1) ffn_kernel(const FfnArgs
     if (lane == 0) {
       s_U = nfirst;
       s_direct = direct;
-      if (bad) { s_abort = 1; if (blockIdx.x == 0) record_error(&a.hdr->status, MOE_ERR_INVALID_ARG); }
+      // every CTA records it, before its own waits, cut short by s_abort, record a timeout: the first record stands
+      if (bad) { s_abort = 1; record_error(&a.hdr->status, MOE_ERR_INVALID_ARG); }
     }
   }
   __syncthreads();
