@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   Prod* prods = reinterpret_cast<Prod*>(info + a.n_seqs);
 
   if (NT > 1 && g.redo && __ldcg(g.redo + a.n_seqs) == 0) return;   // nothing was left over
-  // ---- the sequences: lengths, first visible sub-block, prefix sums of their units over all KV heads
+  // ---- the sequences: lengths, first visible sub-block, prefix sums of their units over all KV heads, how many have any
+  int live = 0;
   if (lane < stages) mbar_init(bar + lane, 1);
   if (tid < 2 * NW) s_entry[tid].b = -1;
   if (tid == 0) { prefix[0] = 0; s_total = 0; }
@@ -165,13 +166,14 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       info[b] = si;
       x = (long long)seq_cost<NT>(si) * Hkv;
     }
+    const bool some = x > 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
+    live += __syncthreads_count(some);
     long long add = s_total;
     for (int w = 0; w < warp; ++w) add += s_warp[w];
     if (b < a.n_seqs) prefix[b + 1] = x + add;
@@ -197,8 +199,10 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
   // ---- this warp's run [f_begin, f_end) of the list
   if (W == 0) return;
   // G: about two units a stream at least; where that leaves SMs over, a multiple of the pairs, so that a pair of an even
-  // batch ends where a CTA does (a pair within one CTA needs no join across CTAs, 3 us)
-  const long long pairs = (long long)a.n_seqs * Hkv, even = (W + 2 * KS * pairs - 1) / (2 * KS * pairs) * pairs;
+  // batch ends where a CTA does (a pair within one CTA needs no join across CTAs, 3 us). Only pairs that have units count: with
+  // W >= 2 pairs, G is then at most W, so that every CTA has a place of the list. The joins rely on it: each CTA from a pair's
+  // first unit's to its last unit's has written a part.
+  const long long pairs = (long long)live * Hkv, even = (W + 2 * KS * pairs - 1) / (2 * KS * pairs) * pairs;
   const int G = (int)min(even, (long long)gridDim.x);
   const int N = G * KS;
   if (blockIdx.x >= G) return;

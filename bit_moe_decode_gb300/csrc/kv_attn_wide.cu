@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
     prefix[0] = 0;
     s_total = 0;
   }
-  // ---- the sequences, as in kv_attn.cu: a pair (sequence, KV head and row group) costs one tile more than it has
+  // ---- the sequences, as in kv_attn.cu: a pair (sequence, KV head and row group) costs kPairTiles more than it has
+  int live = 0;
   for (int base = 0; base < a.n_seqs; base += kThreads) {
     const int b = base + tid;
     long long x = 0;
@@ -223,13 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
       info[b] = si;
       x = seq_tiles(si) ? (long long)(seq_tiles(si) + kPairTiles) * Hv : 0;
     }
+    const bool some = x > 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
+    live += __syncthreads_count(some);
     long long add = s_total;
     for (int w = 0; w < warp; ++w) add += s_warp[w];
     if (b < a.n_seqs) prefix[b + 1] = x + add;
@@ -248,8 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
       for (int64_t i = tid; i < n; i += kThreads) g.lse[r0 + i] = -INFINITY;
   }
   if (W == 0) return;
-  // G: at least about four tiles a CTA, a multiple of the pairs while SMs are left over
-  const long long pairs = (long long)a.n_seqs * Hv, even = (W + 4 * pairs - 1) / (4 * pairs) * pairs;
+  // G: at least about four tiles a CTA, a multiple of the pairs (those that have tiles) while SMs are left over; at most W, as
+  // W >= 4 pairs, so that no CTA is without a place of the list (see kv_attn.cu)
+  const long long pairs = (long long)live * Hv, even = (W + 4 * pairs - 1) / (4 * pairs) * pairs;
   const int G = (int)min(even, (long long)gridDim.x);
   if (blockIdx.x >= G) return;
   const long long f_begin = share(blockIdx.x, W, G), f_end = share(blockIdx.x + 1, W, G);
