@@ -36,6 +36,8 @@
 //     scale of its own, so that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has
 //     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a
 //     dimension whose few heavy keys all have code 0 is made of such weights.
+#include <algorithm>
+
 #include "kv_attn.cuh"
 
 namespace moe {
@@ -964,6 +966,9 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
       q_stride < (int64_t)q_heads * cache->head_dim || window < 0)
     return MOE_ERR_SHAPE;
   if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;   // NaN or infinite
+  // A sequence has fewer than 2^30 keys, so a window of that many hides none. Smaller ones keep the kernels' 32-bit differences
+  // of positions and windows in range.
+  if (window >= 1 << 30) window = 0;
   // units of 32 keys in all: a warp counts its share in 32 bits
   if ((int64_t)batch->n_seqs * cache->kv_heads * ((int64_t)batch->table_stride * cache->page_tokens / 32 + 1) >= (int64_t)1 << 37)
     return MOE_ERR_SHAPE;
@@ -989,7 +994,7 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   // 54 / 49 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
   // 16 rows over 8192 (64) 124 / 178 us.
   int64_t keys = (int64_t)batch->table_stride * cache->page_tokens;
-  if (window && keys > window + batch->max_q) keys = window + batch->max_q;
+  if (window) keys = std::min(keys, (int64_t)window + batch->max_q);
   if (rows <= 16 || keys * s.row_groups < 2048) g.redo = nullptr;
   if (g.redo && (st = kv::attn_wide(a, g, cache->fmt, cache->head_dim, ctas, (cudaStream_t)stream)) != MOE_OK) return st;
 #define KV_CALL(F, DD)                                                                   \

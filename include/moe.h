@@ -364,7 +364,8 @@ moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
 
 /* Attention of the batch's rows (decode: one a sequence; verify: up to 8) over their sequences' cache, grouped queries:
  * query head n reads KV head n / (q_heads / kv_heads).
- *   x_s = scale * q . k_s over the keys s <= position, and s > position - window if window > 0 (0: no window);
+ *   x_s = scale * q . k_s over the keys s <= position, and s > position - window if window > 0 (0, or 2^30 and more: no
+ *   window);
  *   out [n_tokens, q_heads, D] bf16 = sum_s softmax(x)_s v_s, lse [n_tokens, q_heads] fp32 = log sum_s exp(x_s) (natural;
  *   NULL: not wanted). A row that sees no key gives zeros and -inf.
  *   Numerics: q scaled by a power of two into binary16 (exact within 2^-28 of the row's largest), codes exact, block scales
