@@ -944,9 +944,10 @@ static const size_t kZeroBytes = up256((kv::kMaxCtas + kv::kMaxSeqs + 2) * 4);
 extern "C" size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t q_heads) {
   if (kv::check_cache(cache) != MOE_OK || kv::check_sizes(batch) != MOE_OK) return 0;
   if (q_heads < 1 || q_heads > 4096 || q_heads % cache->kv_heads) return 0;
-  const int64_t rows = (int64_t)batch->max_q * (q_heads / cache->kv_heads);
-  if (batch->max_q > 8 || rows > kv::kMaxRows) return sizeof(WsHeader);   // append and read only
-  const kv::Shape s = kv::shape_for((int)rows);
+  // attention's part is for the most new tokens that it takes, so that a workspace for longer prompts serves decoding too
+  const int group = q_heads / cache->kv_heads;
+  if (group > kv::kMaxRows) return sizeof(WsHeader);   // append and read only
+  const kv::Shape s = kv::shape_for(group * std::min(batch->max_q, std::min(8, kv::kMaxRows / group)));
   const size_t row_bytes = (size_t)(cache->head_dim + 2) * 4;
   return sizeof(WsHeader) + kZeroBytes + up256(kv::kMaxCtas * s.warps * 8 * s.nt * row_bytes) + up256(kv::kMaxCtas * 2 * s.row_groups * 8 * s.nt * row_bytes);
 }

@@ -331,7 +331,7 @@ typedef struct {
 size_t moe_kv_page_bytes(moe_format_t fmt, int32_t head_dim, int32_t kv_heads, int32_t page_tokens);
 
 /* Workspace of moe_kv_append / _read / _attention for batches of up to batch->n_seqs sequences of up to batch->max_q rows
- * and q_heads query heads (0 for unsupported sizes). Zero it once with moe_workspace_init(); the calls leave it ready for
+ * (more than attention takes: as many as it takes) and q_heads query heads (0 for unsupported sizes). Zero it once with moe_workspace_init(); the calls leave it ready for
  * the next one, of any batch that it is large enough for. Calls that overlap on the GPU must not share a workspace. Its first word is the device status word
  * (moe_get_device_status): MOE_ERR_INVALID_ARG for device data out of range (rows that are not in the call's tensors,
  * more rows than max_q, a length beyond the table, a page id outside [0, n_pages), a position beyond the rotation
