@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 3) probs_kernel(Args a, uint32_t C) 
   __syncthreads();                                     // s_m is reused
 
   // Exponentials relative to the slice's maximum, in place: 2^((x - m) log2(e) / T); the difference first, so that its
-  // error is relative to itself. A temperature whose reciprocal overflows acts as 0: the first largest takes all.
-  const float scale = 1.4426950408889634f / temp;
+  // error is relative to itself. A temperature whose reciprocal overflows acts as 0: the first largest takes all. One that is
+  // infinite: the smallest scale there is (0 times the -inf of tokens that are not allowed, or not there, is not a number).
+  const float by_temp = 1.4426950408889634f / temp, scale = by_temp == 0.f ? __int_as_float(1) : by_temp;
   const bool greedy = !(temp > 0.f && scale < INFINITY);
   float sum = 0.f;
   auto exponentials = [&](int lo, int hi) {

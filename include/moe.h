@@ -407,7 +407,7 @@ typedef struct {
  *   x = logit (NaN: -inf); if c > 0: x = x > 0 ? x / repetition : x * repetition, then x = (x - frequency * c) - presence;
  *   x = x + bias; x = -inf where not allowed;
  *   probs [rows, vocab] fp32 (contiguous): softmax(x / temperature); temperature 0 (or so small that 1 / temperature
- *   overflows): 1 at the first largest x, else 0. Where
+ *   overflows): 1 at the first largest x, else 0; infinite: uniform over the tokens whose x is finite. Where
  *   the largest x is +inf, the tokens at +inf share the row equally. A row whose x are all -inf gives zeros.
  *   top [rows] int32 (or NULL): the first largest x's token, -1 if all are -inf.
  *   Logits and probs may have any alignment of their type; every other pointer 4-byte aligned. probs may be logits itself
