@@ -449,7 +449,8 @@ class KvCache:
         self.ref = C.byref(self.c)
 
     def workspace(self, batch: "KvBatch", q_heads: int, stream=None) -> torch.Tensor:
-        """Zeroed, 256-byte aligned workspace for the cache's calls with batches of this size."""
+        """Zeroed, 256-byte aligned workspace for the cache's calls with batches of up to this size. After a device status of
+        MOE_ERR_DEVICE_TIMEOUT call moe_workspace_init on it before the next call."""
         return _new_workspace(moe_kv_workspace_bytes(self, batch, q_heads), self.pages.device, stream)
 
 

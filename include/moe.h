@@ -331,12 +331,15 @@ typedef struct {
 size_t moe_kv_page_bytes(moe_format_t fmt, int32_t head_dim, int32_t kv_heads, int32_t page_tokens);
 
 /* Workspace of moe_kv_append / _read / _attention for batches of up to batch->n_seqs sequences of up to batch->max_q rows
- * (more than attention takes: as many as it takes) and q_heads query heads (0 for unsupported sizes). Zero it once with moe_workspace_init(); the calls leave it ready for
- * the next one, of any batch that it is large enough for. Calls that overlap on the GPU must not share a workspace. Its first word is the device status word
- * (moe_get_device_status): MOE_ERR_INVALID_ARG for device data out of range (rows that are not in the call's tensors,
- * more rows than max_q, a length beyond the table, a page id outside [0, n_pages), a position beyond the rotation
- * tables). Nothing out of range is accessed then: such a sequence counts as empty (attention: zeros, lse -inf, as far as
- * its rows exist), such a page is not written, and reads as page 0. */
+ * (more than attention takes: as many as it takes) and q_heads query heads (0 for unsupported sizes). Zero it once with
+ * moe_workspace_init(); the calls leave it ready for the next one, of any batch that it is large enough for. Calls that
+ * overlap on the GPU must not share a workspace. Its first word is the device status word (moe_get_device_status):
+ *   MOE_ERR_INVALID_ARG for device data out of range (rows that are not in the call's tensors, more rows than max_q, a
+ *   length beyond the table, a page id outside [0, n_pages), a position beyond the rotation tables). Nothing out of range is
+ *   accessed then: such a sequence counts as empty (attention: zeros, lse -inf, as far as its rows exist), such a page is
+ *   not written, and reads as page 0. The workspace stays ready.
+ *   MOE_ERR_DEVICE_TIMEOUT: the call's outputs are void, and counters of work that was left undone may stand in the
+ *   workspace: zero it again with moe_workspace_init() before the next call. */
 size_t moe_kv_workspace_bytes(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t q_heads);
 
 /* Append: rotates q and k, encodes k and v into their places in the cache.
