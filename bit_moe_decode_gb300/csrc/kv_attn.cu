@@ -30,12 +30,14 @@
 //     is what an A fragment's register holds. movmatrix turns the weights' accumulator layout into a B fragment. V's
 //     scales vary along the contraction, so they go into the weights: p_s vscale_s, rounded to binary16 once.
 //   Range: the weights are carried as 2^12 p, at most 2^14 (m is raised only when a score passes m + 2), and the value
-//     scales as v 2^-E in binary16, exact within 2^-14 .. 2^2, with an E per block of 32 dimensions; the fp32
-//     accumulators hold 2^(12 - E) times the output. Products keep all 11 bits down to 2^-14. Where scales leave the window, E
-//     moves (accumulators rescaled, exactly) and the keys take passes: each adds the products of the next 26 powers of two at a
-//     scale of its own, so that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has
-//     seen 12 keys of more than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a
-//     dimension whose few heavy keys all have code 0 is made of such weights.
+//     scales as v 2^-E in binary16, exact within 2^-14 .. 2^2; the fp32 accumulators hold 2^(12 - E) times the output. E is set
+//     by the first unit of a warp's part of a pair (its largest scale lies 2 below), and moves per block of 32 dimensions.
+//     Products keep all 11 bits down to 2^-14, 2^-24 of the largest. Where scales leave the window, E moves (accumulators
+//     rescaled, exactly) and the keys take passes: each adds the products of the next 26 powers of two at a scale of its own, so
+//     that no ratio of scales costs precision. So do keys of weights below 2^-24 until each row has seen 12 keys of more
+//     than 2^-14 (counts are halved when its maximum rises, and forgotten when that is by 2^4): a dimension whose few heavy
+//     keys all have code 0 is made of such weights. E stays within 36 of the largest scale that the accumulators can hold, which
+//     is what keeps them and the passes' 2^52 (2^78 within 10) in fp32's range.
 #include <algorithm>
 
 #include "kv_attn.cuh"
@@ -45,7 +47,7 @@ namespace kv {
 
 constexpr int kUnitSubs = 2;        // sub-blocks per unit
 constexpr int kBatch = 16;          // units whose addresses a warp's lanes hold at a time
-constexpr int kEv0 = 2;                 // E at first: scales 2^-12 .. 2^4
+constexpr int kEvMin = -112;            // the smallest E (a scale byte of 0, which stands for zero, is below its window)
 constexpr float kNormal = 6.103515625e-05f;   // 2^-14: binary16 products from here on keep all bits
 constexpr int kPassExp = 26;            // powers of two that a pass covers
 
@@ -117,8 +119,8 @@ __device__ __forceinline__ int seq_cost(const SeqInfo& s) {
 }
 struct Prod {        // a warp's producer: the next batch is n units (subs sub-blocks from `sub` on) at unit u of a pair; left
   int b, h, u, units, left, n, subs, sub;   // counts the units from it on
-  int ev_run[4];     // and of its consumer, per block: the largest value scale's exponent so far,
-  int ev_ref[4];     // and the E in use
+  int ev_run[4];     // and of its consumer, per block: no value scale with a weight has had a larger exponent so far,
+  int ev_ref[4];     // and the E in use (units in its window have scales of up to 2^(E + 1))
 };
 
 struct Entry { int u0, u1, b, h; };   // a partial result of one warp: units [u0, u1) of pair (b, h); b < 0: none
@@ -355,12 +357,6 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     seg_len = si.len;
     min_lim = si.len - si.qn + 1;
     key0 = (si.sub0 + cu * kUnitSubs) * 16;
-    if (lane < NB) {
-      pr->ev_run[lane] = -126;
-      pr->ev_ref[lane] = kEv0;
-    }
-    __syncwarp();
-    set_ref();
     settled = false;
     heavy = 0;
 #pragma unroll
@@ -425,17 +421,46 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
     }
   };
 
+  // E from the segment's first unit: its largest scale (of tokens that some row sees) lies 2 below E, so 12 powers of two below
+  // that and 3 above it are in the window. (All blocks the same: four maxima cost 0.1 us a call more than one.)
+  auto first_window = [&](const uint8_t* unit) {
+    const int key = key0 + lane, n = key < seg_len && key >= min_lim - wnd ? 255 : 0;
+    const uint8_t* p = unit + (lane >> 4) * S::BYTES + S::VS + (lane & 15) * (NB * S::SB);
+    int e = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) e = max(e, FMT == MOE_FMT_MXFP4 ? (int)p[b] : (int)(reinterpret_cast<const uint16_t*>(p)[b] >> 7));
+    const int ev = max((int)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)(e & n)) - 125, kEvMin);
+    __syncwarp();
+    if (lane < NB) {
+      pr->ev_run[lane] = ev + 1;
+      pr->ev_ref[lane] = ev;
+    }
+    __syncwarp();
+    set_ref();
+  };
+
   // The rare path: value scales outside E's window. Moves E to the largest, then adds the products of the weights s (times
   // 2^12) and the scales in passes.
   auto wide_products = [&](const uint8_t* base, const float (&s)[SUBS][NT][4]) {
+    // Scales of 2^-100 of the largest so far and less count as zero: the passes do not reach them, and blocks of zeros, which
+    // have the smallest scale, move nothing.
+    auto value_scales = [&](const uint8_t* sb, float (&v0)[NB], float (&v1)[NB]) {
+      load_scales<FMT, NB>(v0, sb + S::VS + r * (NB * S::SB));
+      load_scales<FMT, NB>(v1, sb + S::VS + (r + 8) * (NB * S::SB));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int none = (pr->ev_run[b] + 27) << 23;   // (of positive numbers, the bits order as the numbers do)
+        if (__float_as_int(v0[b]) <= none) v0[b] = 0.f;
+        if (__float_as_int(v1[b]) <= none) v1[b] = 0.f;
+      }
+    };
     float most[NB];              // (a weight of 0 has no product, whatever bytes its scale is)
 #pragma unroll
     for (int b = 0; b < NB; ++b) most[b] = 0.f;
 #pragma unroll 1
     for (int i = 0; i < SUBS; ++i) {
       float v0[NB], v1[NB];
-      load_scales<FMT, NB>(v0, base + i * S::BYTES + S::VS + r * (NB * S::SB));
-      load_scales<FMT, NB>(v1, base + i * S::BYTES + S::VS + (r + 8) * (NB * S::SB));
+      value_scales(base + i * S::BYTES, v0, v1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -454,14 +479,15 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       const int e_old = pr->ev_ref[b];
       int run = pr->ev_run[b], e_new = e_old;
       if (vm > 0.f) {
-        // Accumulators stay below 2^(38 + run - E) for a million keys: E at least run - 36 keeps two passes' 2^52 in range
+        // Accumulators stay below 2^(38 + run - E) for a million keys: E at least run - 36 keeps two passes' 2^52 in range (run
+        // covers the units of the main path too: each window's top)
         const int ev = (int)(__float_as_uint(vm) >> 23) - 127;
         run = max(run, ev);
-        e_new = max(ev <= e_old + 1 && ev >= e_old - 10 ? e_old : ev, run - 36);   // (ev is -126 .. 127)
+        e_new = max(ev <= e_old + 1 && ev >= e_old - 10 ? e_old : ev, max(run - 36, kEvMin));   // (ev is -126 .. 127)
       }
       depth = min(depth, run - e_new <= 10 ? 3 : 2);
       __syncwarp();
-      if (lane == 0) { pr->ev_run[b] = run; pr->ev_ref[b] = e_new; }
+      if (lane == 0) { pr->ev_run[b] = max(run, e_new + 1); pr->ev_ref[b] = e_new; }
       const float f1 = exp2i((e_old - e_new) >> 1), f2 = exp2i(e_old - e_new - ((e_old - e_new) >> 1));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -482,8 +508,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
         float v0[NB], v1[NB];
         load_words<NB>(vw0, sb + S::VC + (r * 4 + c) * (4 * NB));
         load_words<NB>(vw1, sb + S::VC + (32 + r * 4 + c) * (4 * NB));
-        load_scales<FMT, NB>(v0, sb + S::VS + r * (NB * S::SB));
-        load_scales<FMT, NB>(v1, sb + S::VS + (r + 8) * (NB * S::SB));
+        value_scales(sb, v0, v1);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const float fr = exp2i(-pr->ev_ref[b]);
@@ -727,7 +752,6 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       if (i > 0) load_q();
       begin_segment();
       seg_u0 = cu;
-      fresh = false;
     }
     const bool ok = mbar_wait(bar + stage, phase, kDefaultWaitNs);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -740,6 +764,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attn_kernel(Args a, AttnArgs g) {
       break;
     }
     const uint8_t* unit = ring + stage * UNIT;
+    if (fresh) first_window(unit);
+    fresh = false;
 #pragma unroll 1
     for (int k = 0; k < kUnitSubs; k += SUBS)
       if (key0 + 16 * k < seg_len) process(unit + k * S::BYTES, key0 + 16 * k);
