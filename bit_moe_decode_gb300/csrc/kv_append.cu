@@ -4,7 +4,7 @@
 // Per row of D values (one token, one head): y = rotate(x) in fp32, then either one rounding to bf16 (q) or the encoder
 // of 32-value blocks (k, v): MXFP4 keeps the smallest power of two that covers the block's largest |y| with 6 steps,
 // INT4 the best of six scales by squared error; the rules are moe_encode_blocks'. The kernel is bound by latency in
-// decode (q_start -> length -> table -> store, a chain of four L2 trips) and by HBM for prompts.
+// decode (q_start and length -> table -> store, a chain of three L2 trips) and by HBM for prompts.
 //
 // D / E lanes hold a row, E values each. MXFP4, E = 8: a block is 4 neighbouring lanes, its maximum two shuffles, a K word one
 // lane's codes, two V words one lane's. INT4, E = 4: its six candidates' sums are spread over 8 lanes. (MXFP4 has E = 4 too, for

@@ -6,9 +6,10 @@
 // What bounds it. A key of one KV head is 136 bytes (MXFP4, D = 128) of HBM traffic and 256 codes to convert. At the
 // measured 6.7 TB/s an SM gets 44 bytes per ns, so it has about 24 issue slots per warp-wide MMA (16 keys x 16
 // dimensions) and half as many in the integer pipe. Everything below serves to convert a code with as few instructions
-// as possible, once per 8 query rows. What it reaches: 64 sequences of up to 8192 keys, 8 rows a KV head (8 KV heads, D = 128,
-// MXFP4) 42.8 us, 3.4 TB/s (47 % of the issue slots, 44 % of the integer pipe); one of 262143 keys 76 us, 4.0 TB/s; one of
-// 517 keys 10.4 us, latency; 256 of up to 600, 1 row a KV head (16, D = 64, INT4) 44.5 us, pairs' starts and ends.
+// as possible, once per 8 query rows. What it reaches: 64 sequences of up to 8192 keys, 8 rows a KV head (4 KV heads, D = 128,
+// MXFP4) 44.6 us, 3.3 TB/s (47 % of the issue slots, 44 % of the integer pipe); one of 262143 keys (8 KV heads, INT4) 77.6 us,
+// 3.9 TB/s; one of 517 keys 10.5 us, latency; 256 of up to 600, 1 row a KV head (16, D = 64, INT4) 44.2 us, pairs' starts and
+// ends.
 //
 // Work. The (sequence, KV head) pairs are laid end to end in units of 32 keys, a pair's start counting as some units more
 // (what its queries and its output cost), and dealt out evenly: every warp of the grid streams one contiguous run (the
@@ -28,7 +29,9 @@
 //     fragments), q is scaled by a power of two into binary16, and each block's scale multiplies its fp32 partial.
 //   O^T += V^T P^T: the V layout puts an even and the following odd token's codes of one dimension side by side, which
 //     is what an A fragment's register holds. movmatrix turns the weights' accumulator layout into a B fragment. V's
-//     scales vary along the contraction, so they go into the weights: p_s vscale_s, rounded to binary16 once.
+//     scales vary along the contraction, so they go into the weights: p_s is rounded to binary16 and multiplied by vscale_s
+//     there, which is exact for MXFP4's powers of two and rounds a second time for INT4's bf16 scales. (One rounding in fp32
+//     would take a conversion per block and pair of keys instead of one per pair.)
 //   Range: the weights are carried as 2^12 p, at most 2^14 (m is raised only when a score passes m + 2), and the value
 //     scales as v 2^-E in binary16, exact within 2^-14 .. 2^2; the fp32 accumulators hold 2^(12 - E) times the output. E is set
 //     by the first unit of a warp's part of a pair (its largest scale lies 2 below), and moves per block of 32 dimensions.
@@ -108,8 +111,8 @@ __device__ __forceinline__ int seq_units(const SeqInfo& s) {
 }
 
 // A pair's place in the list of work: kPairCost, then its units.
-// (Measured in units of a warp: decode 256 x 600 47.6, 45.6, 44.6, 45.1 us at 1, 2, 3, 4; 16 rows, 64 x 8192, 124, 129, 135 us
-// at 1, 2, 3, where two warps or more share the units.)
+// (Measured in units of a warp: decode 256 x 600 47.6, 45.6, 44.6, 45.1 us at 1, 2, 3, 4; 16 rows, 64 x 8192 with 8 KV heads,
+// 124, 129, 135 us at 1, 2, 3, where two warps or more share the units.)
 template <int NT>
 constexpr int pair_cost = NT == 1 ? 3 : 1;
 template <int NT>
@@ -1019,7 +1022,7 @@ extern "C" moe_status_t moe_kv_attention(const moe_kv_cache_t* cache, const moe_
   // cost does not grow with the rows up to 64, but a pair's start costs it 3 tiles of 128 keys, this kernel none.
   // Measured, this kernel / that: 24 rows over 300 keys (256 sequences) 33 / 60 us; 18 rows over a window of 1024 (33)
   // 54 / 49 us, 32 rows over 16384 keys (16) 181 / 141 us; 64 rows over 600 (16) 41 / 32 us, over 100000 (1) 197 / 97 us;
-  // 16 rows over 8192 (64) 124 / 178 us.
+  // 16 rows over 8192 (64, 8 KV heads) 124 / 178 us.
   int64_t keys = (int64_t)batch->table_stride * cache->page_tokens;
   if (window) keys = std::min(keys, (int64_t)window + batch->max_q);
   if (rows <= 16 || keys * s.row_groups < 2048) g.redo = nullptr;

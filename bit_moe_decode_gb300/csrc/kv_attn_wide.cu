@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(Args a, AttnArgs g) {
   } else if (warp < kWorkers) {
     // ================================================================ workers
     // Conversion: warp w has eight tokens of sub-block w / 2 of a tile. Softmax: lane = key (then dimension) 32 (w % 4) +
-    // lane of the tile, rows col0 .. col0 + C - 1. A tile's iteration converts the next tile's keys, then its values, then
-    // does its own softmax, so that each product has a phase of the others' to finish in.
+    // lane of the tile, rows col0 .. col0 + C - 1. A tile's iteration converts the next tile's keys, does its own softmax, then
+    // converts the next tile's values, so that each product has a phase of the others' to finish in.
     const int r = lane >> 2, c = lane & 3, half = warp & 1;
     int cb = b0, ch_ = h0, cu = u0, cunits = units0, stage = 0, phase = 0, cpair = -1, key0 = 0, len = 0, min_lo = 0;
     bool cfirst = true;

@@ -372,9 +372,11 @@ moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
  *   out [n_tokens, q_heads, D] bf16 = sum_s softmax(x)_s v_s, lse [n_tokens, q_heads] fp32 = log sum_s exp(x_s) (natural;
  *   NULL: not wanted). A row that sees no key gives zeros and -inf.
  *   Numerics: q scaled by a power of two into binary16 (exact within 2^-28 of the row's largest), codes exact, block scales
- *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s (up to 16 query rows a KV head: times the
- *   value scales), brought into binary16's range by powers of two, are rounded to binary16 (2^-11 relative; for products
- *   down to 2^-26 of the largest, or weights down to 2^-22, smaller ones too while a row has fewer than 12 keys of some weight).
+ *   and all sums, the running maximum and the softmax's sum in fp32; the weights p_s, brought into binary16's range by powers
+ *   of two, are rounded to binary16 (2^-11 relative). Up to 16 query rows a KV head they are then multiplied by the value scales
+ *   in binary16 (INT4: a second 2^-11). Products p_s scale_s keep this accuracy down to 2^-24 of the largest, weights alone (more
+ *   rows) down to 2^-22; below that a key's error is up to 2^-33 of the largest. While a row has seen fewer than 12 keys of
+ *   some weight, weights below 2^-24 keep it too. Scales of 2^-100 of the largest and less may count as zero.
  *   Launches: one, or two where the rows are more than 16 and the table leaves room for long sequences.
  *   q 16-byte aligned with a stride multiple of 8; max_q <= 8, max_q * q_heads / kv_heads <= 128. Scales of blocks that
  *   moe_kv_append writes are finite and below 2^64; other contents must keep to that.
