@@ -20,6 +20,7 @@ MOE_LAYOUT_DECODE, MOE_LAYOUT_TC = 0, 1
 MOE_LAYOUT_PREFILL = MOE_LAYOUT_TC
 MOE_MAT_GATE_UP, MOE_MAT_DOWN = 0, 1
 MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
+MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_UNSUPPORTED_FORMAT",
           4: "MOE_ERR_UNSUPPORTED_ARCH", 5: "MOE_ERR_WORKSPACE_TOO_SMALL", 6: "MOE_ERR_CUDA",
@@ -35,7 +36,8 @@ EXPORTS = ["moe_status_string", "moe_version", "moe_check_device", "moe_canonica
            "moe_prefill_workspace_bytes",
            "moe_expert_grouped_gemm_prefill", "moe_debug_prefill", "moe_spec_accept", "moe_rms_norm_bf16",
            "moe_kv_page_bytes", "moe_kv_workspace_bytes", "moe_kv_append", "moe_kv_read", "moe_kv_attention",
-           "moe_logits_probs"]
+           "moe_logits_probs", "moe_i8_quantize", "moe_i8_values", "moe_rms_norm_i8", "moe_i8_workspace_bytes",
+           "moe_i8_matmul", "moe_i8_gated"]
 
 
 class MoeError(RuntimeError):
@@ -66,6 +68,16 @@ class moe_logits_t(C.Structure):
                 ("allowed", C.c_void_p), ("allowed_stride", C.c_int64)]
 
 
+class moe_i8_rows_t(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("cols", C.c_int32), ("stride", C.c_int64), ("q", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class moe_norm_t(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("hidden", C.c_int32), ("h_type", C.c_int), ("r_type", C.c_int), ("h", C.c_void_p),
+                ("h_stride", C.c_int64), ("r", C.c_void_p), ("r_stride", C.c_int64), ("gain", C.c_void_p), ("eps", C.c_float),
+                ("h_out", C.c_void_p), ("h_out_stride", C.c_int64), ("x_bf16", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -78,7 +90,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(LIB_PATH)
         P, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         LP = C.POINTER(moe_layer_t)
-        KP, BP = C.POINTER(moe_kv_cache_t), C.POINTER(moe_kv_batch_t)
+        KP, BP, RP = C.POINTER(moe_kv_cache_t), C.POINTER(moe_kv_batch_t), C.POINTER(moe_i8_rows_t)
         sig = {
             "moe_status_string": (C.c_char_p, [C.c_int]),
             "moe_version": (i32, []),
@@ -96,6 +108,12 @@ def lib() -> C.CDLL:
             "moe_kv_read": (C.c_int, [KP, BP, P, P, P, sz, P]),
             "moe_kv_attention": (C.c_int, [KP, BP, P, i64, i32, C.c_float, i32, P, P, P, sz, P]),
             "moe_logits_probs": (C.c_int, [C.POINTER(moe_logits_t), P, P, P]),
+            "moe_i8_quantize": (C.c_int, [C.c_int, P, i64, RP, P]),
+            "moe_i8_values": (C.c_int, [RP, P, P]),
+            "moe_rms_norm_i8": (C.c_int, [C.POINTER(moe_norm_t), RP, P]),
+            "moe_i8_workspace_bytes": (sz, [RP, i32]),
+            "moe_i8_matmul": (C.c_int, [RP, RP, P, i64, P, i64, P, i64, P, sz, P]),
+            "moe_i8_gated": (C.c_int, [RP, RP, RP, P, i64, P, i64, P, sz, P]),
             "moe_workspace_bytes": (sz, [LP, i32, i32]),
             "moe_workspace_init": (C.c_int, [P, sz, P]),
             "moe_get_device_status": (C.c_int, [P, P]),
@@ -300,6 +318,86 @@ def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, 
         raise MoeError(st, "moe_logits_probs")
 
 
+# ------------------------------------------------------------------------------------------------ the dense half in 8 bits
+def _typed_rows(t, shape):
+    """Pointer, type and row stride (elements) of an fp32 or bf16 [n, m] tensor whose rows may be slices of wider ones."""
+    f32 = t.dtype == torch.float32
+    assert t.is_cuda and (f32 or t.dtype in _BF16_SIZED) and t.shape == shape and t.stride(1) == 1, \
+        "expected fp32 or bf16 rows %s, got %s %s" % (shape, t.dtype, tuple(t.shape))
+    return t.data_ptr(), MOE_TYPE_F32 if f32 else MOE_TYPE_BF16, _row_stride(t)
+
+
+def _row_stride(t) -> int:
+    # (the stride of a single row means nothing: any that is wide and aligned enough will do)
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+
+
+def _out_rows(t, dtypes, shape):
+    """Pointer and row stride of an output of one of these types (None: not wanted)."""
+    if t is None:
+        return None, 0
+    assert t.is_cuda and t.dtype in dtypes and t.shape == shape and (t.stride(1) == 1 or shape[1] == 1), \
+        "expected %s rows %s, got %s %s" % (dtypes[0], shape, t.dtype, tuple(t.shape))
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def moe_i8_quantize(src, dst: "I8Rows", stream=None):
+    """Rows of src [rows, cols] (fp32 or bf16) to 8 bits with a scale each."""
+    p, type_, stride = _typed_rows(src, (dst.rows, dst.cols))
+    st = lib().moe_i8_quantize(type_, p, stride, dst.ref, _raw_stream(stream, src))
+    if st:
+        raise MoeError(st, "moe_i8_quantize")
+
+
+def moe_i8_values(src: "I8Rows", out, stream=None):
+    """The values that rows stand for, fp32 [rows, cols]."""
+    st = lib().moe_i8_values(src.ref, _dense(out, torch.float32, (src.rows, src.cols)), _raw_stream(stream, out))
+    if st:
+        raise MoeError(st, "moe_i8_values")
+
+
+def moe_rms_norm_i8(h, xq: "I8Rows" = None, r=None, gain=None, eps: float = 1e-6, h_out=None, x_bf16=None, stream=None):
+    """s = h + r (to h_out), RMS norm of s with a gain: bf16 to x_bf16 and 8 bits to xq (at least one of them). h, r and h_out
+    [tokens, hidden] fp32 or bf16 (h_out has h's type), rows with any stride; gain [hidden] fp32."""
+    T, H = h.shape
+    hp, ht, hs = _typed_rows(h, (T, H))
+    rp, rt, rs = _typed_rows(r, (T, H)) if r is not None else (None, 0, 0)
+    op, ot, os_ = _typed_rows(h_out, (T, H)) if h_out is not None else (None, ht, 0)
+    assert ot == ht, "h_out has h's type"
+    c = moe_norm_t(T, H, ht, rt, hp, hs, rp, rs, _dense(gain, torch.float32, (H,)), eps, op, os_,
+                   None if x_bf16 is None else _dense_bf16(x_bf16, (T, H)))
+    st = lib().moe_rms_norm_i8(C.byref(c), xq.ref if xq is not None else None, _raw_stream(stream, h))
+    if st:
+        raise MoeError(st, "moe_rms_norm_i8")
+
+
+def moe_i8_workspace_bytes(w: "I8Rows", T_max: int) -> int:
+    return lib().moe_i8_workspace_bytes(w.ref, T_max)
+
+
+def moe_i8_matmul(x: "I8Rows", w: "I8Rows", y=None, y_bf16=None, base=None, ws=None, stream=None):
+    """x [T, K] times w [N, K]: y fp32 and / or y_bf16 [T, N], plus base fp32 [T, N] (may be y); rows with any stride."""
+    shape = (x.rows, w.rows)
+    yp, ys = _out_rows(y, (torch.float32,), shape)
+    bp, bs = _out_rows(y_bf16, _BF16_SIZED, shape)
+    ap, as_ = _out_rows(base, (torch.float32,), shape)
+    wp, wn = _ws(ws)
+    st = lib().moe_i8_matmul(x.ref, w.ref, ap, as_, yp, ys, bp, bs, wp, wn, _raw_stream(stream, ws))
+    if st:
+        raise MoeError(st, "moe_i8_matmul")
+
+
+def moe_i8_gated(x: "I8Rows", gate: "I8Rows", up: "I8Rows", y=None, y_bf16=None, ws=None, stream=None):
+    """SiLU(x gate) * (x up): y fp32 and / or y_bf16 [T, I], rows with any stride."""
+    shape = (x.rows, gate.rows)
+    yp, ys = _out_rows(y, (torch.float32,), shape)
+    bp, bs = _out_rows(y_bf16, _BF16_SIZED, shape)
+    wp, wn = _ws(ws)
+    st = lib().moe_i8_gated(x.ref, gate.ref, up.ref, yp, ys, bp, bs, wp, wn, _raw_stream(stream, ws))
+    if st:
+        raise MoeError(st, "moe_i8_gated")
+
+
 def moe_workspace_bytes(layer: "Layer", T_max: int, k: int) -> int:
     return lib().moe_workspace_bytes(C.byref(layer.c), T_max, k)
 
@@ -466,3 +564,35 @@ class KvBatch:
         self.c = moe_kv_batch_t(n, tokens, max_q, block_table.shape[1], _dense(q_start, torch.int32, (n + 1,)),
                                 _dense(seq_len, torch.int32, (n,)), _dense(block_table, torch.int32, tuple(block_table.shape)))
         self.ref = C.byref(self.c)
+
+
+# ------------------------------------------------------------------------------------------------ 8-bit rows
+class I8Rows:
+    """Rows of 8-bit codes with a scale each (tokens, or a weight matrix's output channels) and the moe_i8_rows_t that
+    describes them: existing tensors q int8 [rows, cols] (rows with any stride that is a multiple of 16) and scale fp32 [rows],
+    or new ones of this size."""
+
+    def __init__(self, rows: int = 0, cols: int = 0, q=None, scale=None, device="cuda"):
+        if q is None:
+            q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+            scale = torch.empty(rows, dtype=torch.float32, device=device)
+        assert q.is_cuda and q.dtype == torch.int8 and q.dim() == 2 and q.stride(1) == 1, "q: int8 rows [rows, cols]"
+        self.rows, self.cols = q.shape
+        self.q, self.scale = q, scale
+        self.c = moe_i8_rows_t(self.rows, self.cols, _row_stride(q), q.data_ptr(), _dense(scale, torch.float32, (self.rows,)))
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def of(cls, t, stream=None) -> "I8Rows":
+        """The rows of t [rows, cols] (fp32 or bf16) in 8 bits."""
+        out = cls(t.shape[0], t.shape[1], device=t.device)
+        moe_i8_quantize(t, out, stream)
+        return out
+
+    def first(self, rows: int) -> "I8Rows":
+        """Its first rows (the same memory)."""
+        return I8Rows(q=self.q[:rows], scale=self.scale[:rows])
+
+    def workspace(self, T_max: int, stream=None) -> torch.Tensor:
+        """Zeroed workspace for products of up to T_max tokens with these weights."""
+        return _new_workspace(moe_i8_workspace_bytes(self, T_max), self.q.device, stream)

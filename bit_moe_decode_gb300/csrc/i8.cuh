@@ -1,0 +1,25 @@
+// i8.cuh -- rows of 8-bit codes with a scale each: what the kernels of a layer's dense half share.
+#pragma once
+#include "common.cuh"
+#include "api_internal.h"
+
+namespace moe {
+namespace i8 {
+
+constexpr int kMaxRows = 1 << 22;
+constexpr int kMaxCols = 131056;   // the largest multiple of 16 whose sums of products (up to 2^14 each) stay in 31 bits
+
+// MOE_OK if the descriptor can be used (its sizes first, as the other calls do)
+inline moe_status_t check_rows(const moe_i8_rows_t* r) {
+  if (!r || !r->q || !r->scale || ((uintptr_t)r->q & 15) || ((uintptr_t)r->scale & 3)) return MOE_ERR_INVALID_ARG;
+  if (r->rows < 1 || r->rows > kMaxRows || r->cols < 16 || r->cols > kMaxCols || r->cols % 16) return MOE_ERR_SHAPE;
+  if (r->stride % 16 || r->stride < r->cols) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// SiLU(g) u in fp32: one exponential (2 units in the last place at the most times |g|'s rounding in its argument), one IEEE
+// reciprocal. g = -inf gives NaN as the formula does; exp(-g) = inf gives the formula's zero.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, __frcp_rn(1.0f + expf(-g))), u); }
+
+}  // namespace i8
+}  // namespace moe

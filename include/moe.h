@@ -31,7 +31,7 @@
  *     moe_expert_ffn_decode_static.
  *   - Host-side fault injection for tests: if the environment variable MOE_FAULT names a call
  *     ("pack", "route", "decode", "verify", "route_ffn", "prefill", "encode", "spec", "norm", "kv_append", "kv_read",
- *     "kv_attention", "logits"), that call returns
+ *     "kv_attention", "logits", "i8_quantize", "i8_values", "norm_i8", "i8_matmul", "i8_gated"), that call returns
  *     MOE_ERR_FAULT_INJECTED
  *     without launching anything.
  */
@@ -418,6 +418,84 @@ typedef struct {
  *   Logits and probs may have any alignment of their type; every other pointer 4-byte aligned. probs may be logits itself
  *   if those are fp32 with stride vocab. Errors are found on the host; runs on `stream`, no workspace. */
 moe_status_t moe_logits_probs(const moe_logits_t* logits, float* probs, int32_t* top, void* stream);
+
+/* ---------------------------------------------------------------- a layer's dense half in 8 bits ------------------ */
+
+/* What stands around the attention and the routed experts of a layer: the residual's addition and the norm, the
+ * projections of q, k, v, of attention's output and to the vocabulary, a dense or shared expert's FFN ("Mixed-precision
+ * compression of DeepSeek-V4-Flash", "The recipe": these weights stay in 8 bits). From one token to prompts:
+ *   moe_rms_norm_i8 -> moe_i8_matmul (q, k, v) -> attention -> moe_i8_quantize -> moe_i8_matmul (onto the stream)
+ *   -> moe_rms_norm_i8 -> moe_i8_gated -> moe_i8_quantize -> moe_i8_matmul (onto the stream). */
+
+typedef enum { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1 } moe_type_t;
+
+/* Rows of 8-bit codes with a scale each: tokens, or a weight matrix's output channels. Row i stands for q[i, k] * scale[i].
+ * Device memory, owned by the caller. Codes made here are -127 .. 127; the products also take -128. */
+typedef struct {
+  int32_t rows;         /* >= 1, <= 2^22 */
+  int32_t cols;         /* a multiple of 16, 16 .. 131056 */
+  int64_t stride;       /* bytes from one row to the next: a multiple of 16, >= cols */
+  int8_t* q;            /* 16-byte aligned */
+  float* scale;         /* [rows] */
+} moe_i8_rows_t;
+
+/* Rows of src [dst->rows, dst->cols] (fp32 or bf16, row stride src_stride elements) to 8 bits:
+ *   a = max(max_k |v_k|, 2^-100),  q_k = 127 v_k / a rounded to the nearest integer, ties to even (of the real quotient, so
+ *   that the codes are the same bits everywhere),  scale = a / 127 (one fp32 division).
+ *   A row that holds NaN or an infinity gets scale NaN and codes 0: whatever is computed from it is NaN.
+ *   src 16-byte aligned, its stride in bytes a multiple of 16. */
+moe_status_t moe_i8_quantize(moe_type_t type, const void* src, int64_t src_stride, const moe_i8_rows_t* dst, void* stream);
+
+/* The values that rows stand for: out [rows, cols] fp32 (contiguous, 16-byte aligned), one product each. */
+moe_status_t moe_i8_values(const moe_i8_rows_t* src, float* out, void* stream);
+
+/* The arguments of moe_rms_norm_i8. */
+typedef struct {
+  int32_t tokens, hidden;   /* hidden: a multiple of 16, 16 .. 32768; tokens 1 .. 2^22 */
+  moe_type_t h_type;        /* of h and h_out */
+  moe_type_t r_type;        /* of r */
+  const void* h;            /* [tokens, hidden], row stride h_stride elements: the residual stream */
+  int64_t h_stride;
+  const void* r;            /* [tokens, hidden], row stride r_stride: what is added to it (NULL: nothing) */
+  int64_t r_stride;
+  const float* gain;        /* [hidden] (NULL: ones) */
+  float eps;                /* >= 0 */
+  void* h_out;              /* [tokens, hidden], row stride h_out_stride: the sum (NULL: not wanted; may be h, or r if that has
+                               its type, with the same stride) */
+  int64_t h_out_stride;
+  void* x_bf16;             /* [tokens, hidden] bf16, contiguous: the normalised rows (NULL: not wanted) */
+} moe_norm_t;
+
+/* Residual addition, RMS norm and its result in 8 bits. Per token, in fp32 with each operation rounded:
+ *   s = h + r;  h_out = s (rounded once to its type);  v = s * gain;  rho = 1 / sqrt(mean_k s_k^2 + eps);
+ *   x_bf16 = bf16(v * rho);  xq (NULL: not wanted) = moe_i8_quantize of v with its scale times rho (scale = a * rho / 127).
+ *   The sum of squares in fp32, scaled where it would overflow or vanish. A row with NaN or an infinity in v gets scale
+ *   NaN; a row of zeros with eps 0 is NaN, as in moe_rms_norm_bf16. A token's result does not depend on the other tokens.
+ *   xq is [tokens, hidden]; at least one of x_bf16, xq. All pointers 16-byte aligned (xq->scale 4), strides in bytes
+ *   multiples of 16. */
+moe_status_t moe_rms_norm_i8(const moe_norm_t* norm, const moe_i8_rows_t* xq, void* stream);
+
+/* Workspace of moe_i8_matmul and moe_i8_gated with weights like w and up to T_max tokens (0 for unsupported sizes). Its
+ * first word is the device status word (moe_get_device_status): MOE_ERR_DEVICE_TIMEOUT where a wait ran out (the call's
+ * outputs are void). Zero it once with moe_workspace_init(); the calls write nothing else to it, so calls that overlap on the
+ * GPU may share one. */
+size_t moe_i8_workspace_bytes(const moe_i8_rows_t* w, int32_t T_max);
+
+/* Product of 8-bit integers, x [T, K] tokens, w [N, K] output channels (K = cols of both):
+ *   y[t, n] = (float(sum_k x_q[t, k] w_q[n, k]) * x_scale[t]) * w_scale[n] (+ base[t, n]),
+ *   the integer sum exact, its conversion, each product and the addition rounded to fp32. So a token's result does not depend
+ *   on the other tokens, nor on how many there are.
+ *   base [T, N] fp32, row stride base_stride elements (NULL: none; may be y itself with its stride). y [T, N] fp32, row stride
+ *   y_stride, and / or y_bf16 [T, N] bf16, row stride yb_stride (round-to-nearest-even copy); either may be NULL, not both.
+ *   base, y and y_bf16 may have any alignment of their type and any strides >= N. */
+moe_status_t moe_i8_matmul(const moe_i8_rows_t* x, const moe_i8_rows_t* w, const float* base, int64_t base_stride, float* y,
+                           int64_t y_stride, void* y_bf16, int64_t yb_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* Gated block: h[t, i] = SiLU(g) * u with g and u as moe_i8_matmul's y for the weights gate and up (both [I, K]), SiLU(g) =
+ * g / (1 + exp(-g)): both projections, the activation and the product in one kernel. Outputs as moe_i8_matmul's y and y_bf16. The
+ * activation is formed in fp32 (relative error below 2^-20). */
+moe_status_t moe_i8_gated(const moe_i8_rows_t* x, const moe_i8_rows_t* gate, const moe_i8_rows_t* up, float* y,
+                          int64_t y_stride, void* y_bf16, int64_t yb_stride, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- debug (tests only) ----------------------------- */
 
