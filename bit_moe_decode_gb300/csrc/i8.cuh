@@ -17,6 +17,27 @@ inline moe_status_t check_rows(const moe_i8_rows_t* r) {
   return MOE_OK;
 }
 
+// A product's arguments: x [T, K], one or two weight matrices [N, K] (gated: gate and up), outputs [T, N].
+struct MatArgs {
+  const int8_t *x, *w[2];
+  const float *xs, *ws[2], *base;
+  float* y;
+  uint16_t* yb;
+  int64_t x_stride, w_stride[2], base_stride, y_stride, yb_stride;
+  int T, N, K;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float product(int acc, float xs, float ws) { return __fmul_rn(__fmul_rn((float)acc, xs), ws); }
+__device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v) {
+  if (a.base) v = __fadd_rn(v, a.base[t * a.base_stride + n]);
+  if (a.y) a.y[t * a.y_stride + n] = v;
+  if (a.yb) a.yb[t * a.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// tcgen05 (i8_tc.cu); arguments checked by the caller
+moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream);
+
 // SiLU(g) u in fp32: one exponential (2 units in the last place at the most times |g|'s rounding in its argument), one IEEE
 // reciprocal. g = -inf gives NaN as the formula does; exp(-g) = inf gives the formula's zero.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, __frcp_rn(1.0f + expf(-g))), u); }

@@ -4,22 +4,6 @@
 namespace moe {
 namespace i8 {
 
-struct MatArgs {
-  const int8_t *x, *w[2];
-  const float *xs, *ws[2], *base;
-  float* y;
-  uint16_t* yb;
-  int64_t x_stride, w_stride[2], base_stride, y_stride, yb_stride;
-  int T, N, K;
-};
-
-__device__ __forceinline__ float product(int acc, float xs, float ws) { return __fmul_rn(__fmul_rn((float)acc, xs), ws); }
-__device__ __forceinline__ void put(const MatArgs& a, int t, int n, float v) {
-  if (a.base) v = __fadd_rn(v, a.base[t * a.base_stride + n]);
-  if (a.y) a.y[t * a.y_stride + n] = v;
-  if (a.yb) a.yb[t * a.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 // 64 channels x 64 tokens a CTA, 64 of K at a time; a thread has 4 x 4 of them (channels tid % 16 + 16 i, tokens tid / 16 + 16 j)
 template <bool GATED>
 __global__ void __launch_bounds__(256) tile_kernel(MatArgs a) {
@@ -86,7 +70,8 @@ static moe_status_t multiply(const moe_i8_rows_t* x, const moe_i8_rows_t* w, con
   st = moe_check_device();
   if (st != MOE_OK) return st;
   MatArgs a{x->q, {w->q, w2 ? w2->q : nullptr}, x->scale, {w->scale, w2 ? w2->scale : nullptr}, base, y, (uint16_t*)y_bf16,
-            x->stride, {w->stride, w2 ? w2->stride : 0}, base_stride, y_stride, yb_stride, x->rows, w->rows, x->cols};
+            x->stride, {w->stride, w2 ? w2->stride : 0}, base_stride, y_stride, yb_stride, x->rows, w->rows, x->cols, (int32_t*)ws};
+  if (a.T > 8) return tc_multiply(a, (cudaStream_t)stream);
   const dim3 grid((a.N + 63) / 64, (a.T + 63) / 64);
   if (w2) tile_kernel<true><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
   else tile_kernel<false><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
