@@ -2,43 +2,43 @@
 //
 // GB300's tensor cores multiply 8-bit integers at a small fraction of their 16-bit rate, but binary16 holds every code
 // exactly, and a product of two codes is at most 2^14: kind::f16 with fp32 accumulators adds 1024 of them without rounding
-// (2^24). So codes are converted to binary16 on their way to the tensor cores, and every 1024 of K at the latest the
+// (2^24). So codes are converted to binary16 on their way to the tensor cores, and after every 1024 of K at the latest the
 // accumulators are added to integers in registers: the sums are exact whatever the codes are.
 //
-//   D [128 channels x nt tokens] += W [128 x 64] X^T [64 x nt]: channels are the rows of the product, so that a weight's tile
-//   goes from shared memory through a warpgroup's registers straight into TMEM (operand A; lane = channel) and is not written to
-//   shared memory again. X is converted into a swizzled shared memory operand (B).
+//   D [128 channels x tokens] += W [128 x 128] X^T [128 x tokens]: channels are the rows of the product, so that a weight's
+//   tile goes from shared memory through a warpgroup's registers straight into TMEM (operand A; lane = channel) and is not
+//   written to shared memory again. X is converted into a swizzled shared memory operand (B).
 //
-// A CTA has 256 channels: two blocks of 128 (gated: 128 of gate and the same 128 of up), each with a warpgroup that converts its
-// weights, adds up its accumulators and writes its outputs, and with a warp of its own that issues its products. The blocks'
-// sums are taken out 512 of K apart, so that one block's products run while the other's accumulators are read.
-// One warpgroup converts X for both, one warp copies packed tiles (TMA, 128 of K a stage).
+// Warpgroups: two take the sums out of the accumulators and write the outputs, one or two convert W, one converts X, one copies
+// packed tiles (TMA, 128 of K a stage) and issues products. A CTA has two accumulators whose sums are taken half a segment
+// apart, each with a thread of its own that issues its products, so that one's products run while the other is read; the
+// outputs of a tile are written while the next one's products run.
 //
-// Few channels: a cluster of CTAs shares a tile, each takes a part of K; the integer parts are exchanged through distributed
-// shared memory, each CTA finishing some of the tokens. Many tiles: CTAs go from one to the next, outputs of one tile being
-// written while the tensor cores work on the next.
+// small_kernel: a CTA has 256 channels (two blocks of 128; gated: 128 of gate and the same 128 of up) and up to 64 tokens. Where
+// that makes few tiles, a cluster of CTAs shares one, each with a part of K; the integer parts are exchanged through
+// distributed shared memory, each CTA finishing some of the tokens.
+// pair_kernel: two CTAs (cta_group::2) have 256 channels (128 each; gated: 64 of gate and 64 of up each) and up to 256 tokens (two
+// halves); each converts its own channels and half of the tokens, which halves the conversions and the reads of X.
 #include "i8.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace i8 {
 
-constexpr int kThreads = 512;
-constexpr int kMaxTokens = 128;        // of a tile
-constexpr int kTileK = 128;            // K of a stage of packed codes; two steps of 64
-constexpr int kSlots = 4;              // converted steps in flight
-constexpr int kSegment = 16;           // steps that fp32 adds exactly
+constexpr int kTileK = 128;            // K of a stage
+constexpr int kSegment = 8;            // stages that fp32 adds exactly
 constexpr int kMaxStages = 8;
-constexpr uint32_t kTmemA = 256;       // columns: accumulators of the blocks at 0 and 128, then [block][slot] 32 columns of A
-constexpr int kXchgTokens = 8;         // tokens that the blocks of a gated tile exchange at a time
-constexpr int kXchgBytes = 2 * 2 * kXchgTokens * 128 * 4;
-constexpr int kSmemLimit = 232448 - 1024;    // (1 KB for alignment and the static part)
+constexpr int kSlots = 2;              // converted stages of X in flight
+constexpr int kSmallTokens = 64, kSmallThreads = 768, kSmallA = 3;    // A slots: TMEM columns 128 + (block * 3 + slot) * 64
+constexpr int kPairTokens = 256, kPairThreads = 640, kPairA = 4;      // A slots: TMEM columns 256 + slot * 64
+constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
+constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
 
 struct TcArgs {
   MatArgs m;
-  int nt;              // tokens of a tile: a multiple of 16
+  int nt;              // tokens of a tile: a multiple of 16 (pairs: 32)
   int tiles_n, tiles;  // tiles of 256 channels (gated: 128), times the tiles of nt tokens
-  int split;           // CTAs (a cluster) that share a tile
+  int split;           // CTAs (a cluster) that share a tile of small_kernel
   int stages;
 };
 
@@ -92,6 +92,31 @@ __device__ __forceinline__ void convert4(uint32_t w, uint32_t& lo, uint32_t& hi)
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0xE480E480u));
 }
 
+// Outputs of channel n for the `count` (up to E) tokens from t on. Loads and stores go in groups, so that their latencies overlap.
+template <int E>
+__device__ __forceinline__ void put_tokens(const MatArgs& a, int64_t t, int count, int n, float (&v)[E]) {
+  if (a.base) {
+    const float* p = a.base + t * a.base_stride + n;
+    float d[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) d[e] = e < count ? p[e * a.base_stride] : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = __fadd_rn(v[e], d[e]);
+  }
+  if (a.y) {
+    float* p = a.y + t * a.y_stride + n;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < count) p[e * a.y_stride] = v[e];
+  }
+  if (a.yb) {
+    uint16_t* p = a.yb + t * a.yb_stride + n;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < count) p[e * a.yb_stride] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+  }
+}
+
 // The rest of a wait: true if it ran out. (Inlined: a call would hold registers that the warpgroups' split has not left.)
 __device__ __forceinline__ bool wait_longer(uint64_t* bar, int parity, int32_t* status) {
   const long long t0 = globaltimer_ns();
@@ -103,26 +128,157 @@ __device__ __forceinline__ bool wait_longer(uint64_t* bar, int parity, int32_t* 
   return false;
 }
 
-// Step i of `steps` of a block ends a segment: every kSegment steps, the second block's half as many earlier, and the last
-__device__ __forceinline__ bool ends_segment(int i, int steps, int block) {
-  return i == steps - 1 || (i + 1 + block * (kSegment / 2)) % kSegment == 0;
+// A wait that runs out is recorded; the thread then goes on without waiting, so that every barrier is still met and all loops
+// end (the results are void).
+struct Waits {
+  int32_t* status;
+  bool dead;
+  __device__ __forceinline__ void operator()(uint64_t* bar, int parity) {
+    if (!mbar_try_wait(bar, parity) && !dead) dead = wait_longer(bar, parity, status);
+  }
+};
+
+// Stage i of a tile's `stages` ends a segment of accumulator d: every kSegment stages, the second's half as many earlier, and
+// the last
+__device__ __forceinline__ bool ends_segment(int i, int stages, int d) {
+  return i == stages - 1 || (i + 1 + d * (kSegment / 2)) % kSegment == 0;
 }
 
+// 128 codes of a weight row (row: its place in the tile, for the swizzle) -> 64 TMEM columns of the thread's lane
+__device__ __forceinline__ void convert_w(uint32_t from, int row, uint32_t taddr) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint4 v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = ld_shared(from + (((4 * q + c) ^ (row & 7)) << 4));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t h[16];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        convert4(v[2 * k + c].x, h[8 * c], h[8 * c + 1]);
+        convert4(v[2 * k + c].y, h[8 * c + 2], h[8 * c + 3]);
+        convert4(v[2 * k + c].z, h[8 * c + 4], h[8 * c + 5]);
+        convert4(v[2 * k + c].w, h[8 * c + 6], h[8 * c + 7]);
+      }
+      tc_st16(taddr + 32 * q + 16 * k, h);
+    }
+  }
+  tc_wait_st();
+  tc_fence_before();
+}
+
+// A stage of X, `rows` (up to 128) tokens of 128 codes at `from` -> operands at `to`: parts of `part` rows, each [two halves of
+// K][part rows][64 values], swizzled. t: thread of 128. Eight lanes have four 16-byte pieces of rows r and r ^ 5: their reads and
+// their writes meet no bank twice.
+__device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, int part, int t) {
+  const int c = t & 3, pair = (t >> 3) & 3, r0 = (t >> 5) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r0 & 7;
+  const uint32_t d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t src = from + r0 * 128 + (((half * 4 + c) ^ sw) << 4);
+    uint4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r0 + 32 * e < rows) v[e] = ld_shared(src + e * 4096);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = r0 + 32 * e;
+      if (r < rows) {
+        uint32_t h[8];
+        convert4(v[e].x, h[0], h[1]);
+        convert4(v[e].y, h[2], h[3]);
+        convert4(v[e].z, h[4], h[5]);
+        convert4(v[e].w, h[6], h[7]);
+        // part p begins 256 part bytes after the one before it, its row 0 is row p part
+        const uint32_t dst = to + r * 128 + (half + (r >= part)) * (part * 128);
+        st_shared(dst + d0, h[0], h[1], h[2], h[3]);
+        st_shared(dst + d1, h[4], h[5], h[6], h[7]);
+      }
+    }
+  }
+  fence_async_smem();
+}
+
+// Adds accumulator columns 0 .. n - 1 of the thread's lane, exact integers, to its sums
+template <int COLS>
+__device__ __forceinline__ void take_sums(uint32_t taddr, int n, int (&sum)[COLS]) {
+#pragma unroll
+  for (int c = 0; c < COLS / 16; ++c)
+    if (c * 16 < n) {
+      uint32_t r[16];
+      tc_ld16(taddr + 16 * c, r);
+      tc_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[16 * c + e] += __float2int_rn(__uint_as_float(r[e]));
+    }
+  tc_fence_before();
+}
+// Tokens 16 c .. of the sums, which start again at 0: a rolled loop over c keeps the code of the outputs small (unrolled it was
+// 130 KB, and a tile's end took 15 us longer, of instruction misses)
+template <int COLS>
+__device__ __forceinline__ void give_sums(int c, int (&sum)[COLS], int (&r)[16]) {
+#pragma unroll
+  for (int k = 0; k < COLS / 16; ++k)
+    if (c == k) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        r[e] = sum[16 * k + e];
+        sum[16 * k + e] = 0;
+      }
+    }
+}
+// The outputs of `count` tokens from t0 on, channel n (none if n >= N). Gated: the thread has gate's (side 0) or up's sums, and
+// the thread with the other of the same n is at the same idx (of `width`) on the other side; of 16 tokens side 0 finishes the first
+// eight, side 1 the last, and what the other needs goes through shared memory (two buffers in turn), ordered by barrier `bar` among
+// 2 width threads.
+template <bool GATED, int COLS>
+__device__ __forceinline__ void output_sums(const MatArgs& a, int (&sum)[COLS], int t0, int count, int n, int side, uint32_t xchg,
+                                            int idx, int width, int bar) {
+  const float ws = n < a.N ? a.ws[GATED ? side : 0][n] : 0.f;
+  int r[16];
+#pragma unroll 1
+  for (int c = 0; c * 16 < count; ++c) {
+    give_sums(c, sum, r);
+    const int t1 = t0 + 16 * c;
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = product(r[e], __ldg(a.xs + min(t1 + e, a.T - 1)), ws);
+    if (!GATED) {
+      if (n < a.N) put_tokens<16>(a, t1, a.T - t1, n, v);
+    } else {
+      const uint32_t buf = xchg + ((c & 1) * 16 * width + idx) * 4, mine = buf + side * 32 * width, theirs = buf + (1 - side) * 32 * width;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(theirs + e * 4 * width), "f"(side == 0 ? v[8 + e] : v[e]) : "memory");
+      named_bar(bar, 2 * width);
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(h[e]) : "r"(mine + e * 4 * width) : "memory");
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = side == 0 ? silu_mul(v[e], h[e]) : silu_mul(h[e], v[8 + e]);
+      if (n < a.N) put_tokens<8>(a, t1 + 8 * side, a.T - t1 - 8 * side, n, h);
+    }
+  }
+  if (GATED) named_bar(bar, 2 * width);   // the next tile's first buffer is free
+}
+
+// ------------------------------------------------------------------------------------------------ one CTA, up to 64 tokens
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads, 1) tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x,
-                                                         const __grid_constant__ CUtensorMap map_w0,
-                                                         const __grid_constant__ CUtensorMap map_w1) {
+__global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x,
+                                                                 const __grid_constant__ CUtensorMap map_w0,
+                                                                 const __grid_constant__ CUtensorMap map_w1) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];          // packed tiles
-  __shared__ uint64_t bar_a_full[2][kSlots], bar_a_empty[2][kSlots];        // converted W
+  __shared__ uint64_t bar_a_full[2][kSmallA], bar_a_empty[2][kSmallA];      // converted W
   __shared__ uint64_t bar_x_full[kSlots], bar_x_empty[kSlots];              // converted X
   __shared__ uint64_t bar_d_full[2], bar_d_empty[2];                        // accumulators
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
   const int nt = a.nt, stages = a.stages, T = a.m.T, N = a.m.N;
-  const uint32_t stage_bytes = 32768 + nt * 128, slot_bytes = nt * 128;
+  const uint32_t stage_bytes = 32768 + nt * 128, slot_bytes = nt * 256;
   const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
 
   // ---- this CTA's tiles and its part of K (in stages of 128)
@@ -130,323 +286,433 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(TcArgs a, const __grid_
   const int first = blockIdx.x / a.split, step_tiles = gridDim.x / a.split;
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int k_begin = (int)((long long)rank * nk / a.split), k_end = (int)((long long)(rank + 1) * nk / a.split);
-  const int steps = 2 * (k_end - k_begin);
-  const int my_tiles = first < a.tiles ? (a.tiles - first + step_tiles - 1) / step_tiles : 0;
+  const int per_tile = k_end - k_begin, my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * per_tile;
 
-  if (tid == 0) {
+  // the copies' barriers first: the first stages are on their way while the rest is set up
+  auto copy = [&](int stage, int tile, int k) {
+    const int tn = tile % a.tiles_n, tt = tile / a.tiles_n;
+    uint8_t* to = smem + stage * stage_bytes;
+    mbar_arrive_expect_tx(bar_full + stage, stage_bytes);
+    tma_load_2d(to, &map_w0, k * kTileK, tn * (GATED ? 128 : 256), bar_full + stage);
+    if (GATED) tma_load_2d(to + 16384, &map_w1, k * kTileK, tn * 128, bar_full + stage);
+    else tma_load_2d(to + 16384, &map_w0, k * kTileK, tn * 256 + 128, bar_full + stage);
+    tma_load_2d(to + 32768, &map_x, k * kTileK, tt * nt, bar_full + stage);
+  };
+  const int early = min(stages, per_tile);                 // stages copied before the roles begin (of the first tile)
+  if (warp == 20 && lane == 0) {
     for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 12); }
-    for (int i = 0; i < kSlots; ++i) {
-      for (int b = 0; b < 2; ++b) { mbar_init(&bar_a_full[b][i], 4); mbar_init(&bar_a_empty[b][i], 1); }
-      mbar_init(bar_x_full + i, 4);
-      mbar_init(bar_x_empty + i, 2);
+    fence_mbar_init();
+    for (int i = 0; i < early; ++i) copy(i, first, k_begin + i);
+  }
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      for (int i = 0; i < kSmallA; ++i) { mbar_init(&bar_a_full[b][i], 4); mbar_init(&bar_a_empty[b][i], 1); }
+      mbar_init(bar_d_full + b, 1);
+      mbar_init(bar_d_empty + b, 4);
     }
-    for (int b = 0; b < 2; ++b) { mbar_init(bar_d_full + b, 1); mbar_init(bar_d_empty + b, 4); }
+    for (int i = 0; i < kSlots; ++i) { mbar_init(bar_x_full + i, 4); mbar_init(bar_x_empty + i, 2); }
     fence_mbar_init();
   }
-  if (warp == 12) tc_alloc(&s_tmem, 512);
+  if (warp == 21) tc_alloc(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  Waits wait{a.m.status, false};
 
-  // A wait that runs out is recorded; the thread then goes on without waiting, so that every barrier is still met and all
-  // loops end (the results are void).
-  bool dead = false;
-  auto wait = [&](uint64_t* bar, int parity) {
-    if (!mbar_try_wait(bar, parity) && !dead) dead = wait_longer(bar, parity, a.m.status);
-  };
-
-  if (wg == 3) {
+  if (wg == 5) {
     regs_less<40>();
-    if (warp == 12) {
+    if (warp == 20) {
       // ================================================================ copies
       if (lane == 0) {
-        int stage = 0, phase = 1;                              // (the first pass over the ring finds it empty)
-        for (int j = 0; j < my_tiles; ++j) {
-          const int tile = first + j * step_tiles, tn = tile % a.tiles_n, tt = tile / a.tiles_n;
-          for (int k = k_begin; k < k_end; ++k) {
+        int stage = early % stages, phase = early == stages ? 0 : 1;   // (the first pass over the ring finds it empty)
+        for (int j = 0; j < my_tiles; ++j)
+          for (int k = k_begin + (j ? 0 : early); k < k_end; ++k) {
             wait(bar_empty + stage, phase);
-            uint8_t* to = smem + stage * stage_bytes;
-            mbar_arrive_expect_tx(bar_full + stage, stage_bytes);
-            tma_load_2d(to, &map_w0, k * kTileK, tn * (GATED ? 128 : 256), bar_full + stage);
-            if (GATED) tma_load_2d(to + 16384, &map_w1, k * kTileK, tn * 128, bar_full + stage);
-            else tma_load_2d(to + 16384, &map_w0, k * kTileK, tn * 256 + 128, bar_full + stage);
-            tma_load_2d(to + 32768, &map_x, k * kTileK, tt * nt, bar_full + stage);
+            copy(stage, first + j * step_tiles, k);
             if (++stage == stages) { stage = 0; phase ^= 1; }
           }
-        }
         // (where waits have run out, copies may still be in flight)
-        dead = false;
-        const int total = my_tiles * (k_end - k_begin);
+        wait.dead = false;
         for (int t = max(0, total - stages); t < total; ++t) wait(bar_full + t % stages, (t / stages) & 1);
       }
-    } else if (warp <= 14) {
+    } else if (warp <= 22) {
       // ================================================================ products of block b
-      const int b = warp - 13;
+      const int b = warp - 21;
       if (lane == 0) {
         const uint32_t idesc = idesc_f16(nt);
         const uint64_t dx = umma_desc_sw128(xring);
-        int i = 0, seg = 0;
+        int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
         for (int j = 0; j < my_tiles; ++j) {
           bool fresh = true;
-          for (int s = 0; s < steps; ++s, ++i) {
-            const int slot = i % kSlots, phase = (i / kSlots) & 1;
+          for (int s = 0; s < per_tile; ++s) {
             if (fresh) wait(bar_d_empty + b, (seg & 1) ^ 1);
+            wait(bar_x_full + xslot, xphase);
             wait(&bar_a_full[b][slot], phase);
-            wait(bar_x_full + slot, phase);
             tc_fence_after();
-            const uint32_t ta = tmem + kTmemA + (b * kSlots + slot) * 32;
-            const uint64_t dxs = dx + slot * (slot_bytes / 16);
+            const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
+            const uint64_t dxs = dx + xslot * (slot_bytes / 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ts(tmem + b * 128, ta + 8 * k, dxs + 2 * k, idesc, k > 0 || !fresh);
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ts(tmem + b * 64, ta + 8 * k, dxs + (k >> 2) * (nt * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
             tc_commit(&bar_a_empty[b][slot]);
-            tc_commit(bar_x_empty + slot);
+            tc_commit(bar_x_empty + xslot);
             fresh = false;
-            if (ends_segment(s, steps, b)) {
+            if (ends_segment(s, per_tile, b)) {
               tc_commit(bar_d_full + b);
               ++seg;
               fresh = true;
             }
+            if (++slot == kSmallA) { slot = 0; phase ^= 1; }
+            if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
           }
         }
       }
     }
     __syncwarp();
     if (a.split > 1) { cluster_sync(); cluster_sync(); }
-  } else if (wg == 2) {
+  } else if (wg == 4) {
     // ================================================================ conversion of X
-    regs_less<72>();
-    const int t = tid - 256, items = nt * 4;                    // 16-byte pieces of a step
-    int stage = 0, phase = 0, i = 0;
-    for (int j = 0; j < my_tiles; ++j)
-      for (int s = 0; s < steps; s += 2) {
-        wait(bar_full + stage, phase);
-        const uint32_t from = ring + stage * stage_bytes + 32768;
-#pragma unroll
-        for (int half = 0; half < 2; ++half, ++i) {
-          const int slot = i % kSlots;
-          wait(bar_x_empty + slot, ((i / kSlots) & 1) ^ 1);
-          const uint32_t to = xring + slot * slot_bytes;
-          // eight lanes have the four pieces of rows r and r ^ 5: their reads and their writes meet no bank twice
-          for (int p = t; p < items; p += 128) {
-            const int c = p & 3, pair = (p >> 3) & 3, r = (p >> 5) * 8 + ((p & 4) ? pair ^ 5 : pair);
-            const uint4 v = ld_shared(from + r * 128 + (((half * 4 + c) ^ (r & 7)) << 4));
-            uint32_t h[8];
-            convert4(v.x, h[0], h[1]);
-            convert4(v.y, h[2], h[3]);
-            convert4(v.z, h[4], h[5]);
-            convert4(v.w, h[6], h[7]);
-            const uint32_t row = to + r * 128;
-            st_shared(row + (((2 * c) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-            st_shared(row + (((2 * c + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_x_full + slot);
-        }
-        if (lane == 0) mbar_arrive(bar_empty + stage);
-        if (++stage == stages) { stage = 0; phase ^= 1; }
+    regs_less<56>();
+    int stage = 0, phase = 0, slot = 0, sphase = 1;
+    for (int i = 0; i < total; ++i) {
+      wait(bar_x_empty + slot, sphase);
+      wait(bar_full + stage, phase);
+      convert_x(ring + stage * stage_bytes + 32768, xring + slot * slot_bytes, nt, nt, tid & 127);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_x_full + slot);
+        mbar_arrive_relaxed(bar_empty + stage);
       }
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+      if (++slot == kSlots) { slot = 0; sphase ^= 1; }
+    }
     __syncwarp();
     if (a.split > 1) { cluster_sync(); cluster_sync(); }
-  } else {
-    // ================================================================ block wg: conversion of W, sums, outputs
-    regs_more<200>();
-    const int b = wg, row = tid & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // TMEM lane quarter
-    int sum[kMaxTokens];
-#pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0;
-    int stage = 0, phase = 0, i = 0, seg = 0;
-    uint32_t from = 0;
-
-    // converts step i: the next 64 of K
-    auto convert = [&]() {
-      const int half = i & 1, slot = i % kSlots;
-      if (half == 0) {
-        wait(bar_full + stage, phase);
-        from = ring + stage * stage_bytes + b * 16384 + row * 128;
-      }
-      wait(&bar_a_empty[b][slot], ((i / kSlots) & 1) ^ 1);
+  } else if (wg >= 2) {
+    // ================================================================ conversion of block b's W
+    regs_less<64>();
+    const int b = wg - 2, row = tid & 127;
+    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 128 + b * kSmallA * 64;
+    int stage = 0, phase = 0, slot = 0, sphase = 1;
+    for (int i = 0; i < total; ++i) {
+      wait(&bar_a_empty[b][slot], sphase);
+      wait(bar_full + stage, phase);
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t h[16];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 v = ld_shared(from + (((half * 4 + 2 * k + c) ^ (row & 7)) << 4));
-          convert4(v.x, h[8 * c], h[8 * c + 1]);
-          convert4(v.y, h[8 * c + 2], h[8 * c + 3]);
-          convert4(v.z, h[8 * c + 4], h[8 * c + 5]);
-          convert4(v.w, h[8 * c + 6], h[8 * c + 7]);
-        }
-        tc_st16(tmem + lanes + kTmemA + (b * kSlots + slot) * 32 + 16 * k, h);
-      }
-      tc_wait_st();
-      tc_fence_before();
+      convert_w(ring + stage * stage_bytes + b * 16384 + row * 128, row, ta + slot * 64);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bar_a_full[b][slot]);
-        if (half == 1) mbar_arrive(bar_empty + stage);
+        mbar_arrive_relaxed(bar_empty + stage);
       }
-      if (half == 1 && ++stage == stages) { stage = 0; phase ^= 1; }
-      ++i;
-    };
-    // adds the accumulators of the segment that is done next to the sums
-    auto take = [&]() {
-      wait(bar_d_full + b, seg & 1);
-      ++seg;
-      tc_fence_after();
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+      if (++slot == kSmallA) { slot = 0; sphase ^= 1; }
+    }
+    __syncwarp();
+    if (a.split > 1) { cluster_sync(); cluster_sync(); }
+  } else {
+    // ================================================================ block b's sums and outputs
+    regs_more<128>();
+    const int b = wg, row = tid & 127;
+    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
+    int sum[kSmallTokens];
 #pragma unroll
-      for (int c = 0; c < kMaxTokens / 16; ++c)
-        if (c * 16 < nt) {
-          uint32_t r[16];
-          tc_ld16(tmem + lanes + b * 128 + 16 * c, r);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sum[16 * c + e] += __float2int_rn(__uint_as_float(r[e]));
-        }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_d_empty + b);
-    };
-    auto output = [&](int tile) {
-      const int tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
-      if (!GATED) {
-        const int n = tn * 256 + b * 128 + row;
-        const float ws = n < N ? a.m.ws[0][n] : 0.f;
-#pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t) {
-          if (t < nt && t0 + t < T && n < N) put(a.m, t0 + t, n, product(sum[t], __ldg(a.m.xs + t0 + t), ws));
-          sum[t] = 0;
-        }
-      } else {
-        // block 0 (gate) finishes the lower half of every 16 tokens, block 1 (up) the upper; what the other needs goes through
-        // shared memory, two buffers in turn
-        const int n = tn * 128 + row;
-        const float ws = n < N ? a.m.ws[b][n] : 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxTokens / 16; ++c)
-          if (c * 16 < nt) {
-            const uint32_t buf = xchg + (c & 1) * (kXchgBytes / 2);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int v = b == 0 ? sum[16 * c + 8 + e] : sum[16 * c + e];
-              const int t = t0 + 16 * c + 8 * (1 - b) + e;
-              const float p = product(v, t < T ? __ldg(a.m.xs + t) : 0.f, ws);
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (((1 - b) * 8 + e) * 128 + row) * 4), "f"(p) : "memory");
-            }
-            named_bar(1, 256);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int t = t0 + 16 * c + 8 * b + e;
-              float other;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(buf + ((b * 8 + e) * 128 + row) * 4) : "memory");
-              if (t < T && n < N) {
-                const float p = product(b == 0 ? sum[16 * c + e] : sum[16 * c + 8 + e], __ldg(a.m.xs + t), ws);
-                put(a.m, t, n, b == 0 ? silu_mul(p, other) : silu_mul(other, p));
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sum[16 * c + e] = 0;
-          }
-        named_bar(1, 256);   // the next tile's first buffer is free
+    for (int t = 0; t < kSmallTokens; ++t) sum[t] = 0;
+    int seg = 0;
+    for (int j = 0; j < my_tiles; ++j) {
+      for (int s = 0; s < per_tile; ++s) {
+        if (!ends_segment(s, per_tile, b)) continue;
+        wait(bar_d_full + b, seg & 1);
+        ++seg;
+        tc_fence_after();
+        take_sums(td, nt, sum);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_d_empty + b);
       }
-    };
-
-    // A segment's sums are taken three steps after its last one has been converted, so that the tensor cores have steps to
-    // go on with. d: the next segment's end; one tile's steps after another's.
-    const int total = my_tiles * steps;
-    int ds = 0, dtile = 0;                          // the next step whose sums may be due, within its tile
-    for (int at = 0; at < total + kSlots - 1; ++at) {
-      if (at < total) convert();
-      if (at >= kSlots - 1) {
-        if (ends_segment(ds, steps, b)) take();
-        if (++ds == steps) {
-          if (a.split == 1) output(first + dtile * step_tiles);
-          ds = 0;
-          ++dtile;
-        }
+      if (a.split == 1) {
+        const int tile = first + j * step_tiles, tn = tile % a.tiles_n;
+        output_sums<GATED>(a.m, sum, tile / a.tiles_n * nt, nt, GATED ? tn * 128 + row : tn * 256 + b * 128 + row, b, xchg, row, 128, 1);
       }
     }
-
     if (a.split > 1) {
       // every CTA of the cluster is through with its rings; token t is finished by CTA t / per
       const int per = (nt + a.split - 1) / a.split;
       cluster_sync();
+      int r[16], to = 0, at = 0;                    // token t goes to place t % per of CTA t / per
+#pragma unroll 1
+      for (int c = 0; c * 16 < nt; ++c) {
+        give_sums(c, sum, r);
 #pragma unroll
-      for (int t = 0; t < kMaxTokens; ++t)
-        if (t < nt) st_peer(ring + ((rank * per + t % per) * 256 + (b * 128 + row)) * 4, t / per, (uint32_t)sum[t]);
-      cluster_sync();
-      const int tn = first % a.tiles_n, t0 = first / a.tiles_n * nt;
-      const int* got = reinterpret_cast<const int*>(smem);
-      const int here = min(per, nt - rank * per);
-      if (!GATED) {
-        const int n = tn * 256 + tid;
-        if (n < N && first < a.tiles) {
-          const float ws = a.m.ws[0][n];
-          for (int t = 0; t < here; ++t) {
-            const int tok = t0 + rank * per + t;
-            if (tok >= T) break;
-            int acc = 0;
-            for (int s = 0; s < a.split; ++s) acc += got[(s * per + t) * 256 + tid];
-            put(a.m, tok, n, product(acc, __ldg(a.m.xs + tok), ws));
-          }
+        for (int e = 0; e < 16; ++e) {
+          st_peer(ring + ((rank * per + at) * 256 + (b * 128 + row)) * 4, to, (uint32_t)r[e]);
+          if (++at == per) { at = 0; ++to; }
         }
-      } else {
-        const int n = tn * 128 + row;
-        if (n < N && first < a.tiles) {
-          const float wg_ = a.m.ws[0][n], wu = a.m.ws[1][n];
-          for (int t = b; t < here; t += 2) {
-            const int tok = t0 + rank * per + t;
-            if (tok >= T) break;
-            int g = 0, u = 0;
-            for (int s = 0; s < a.split; ++s) {
-              g += got[(s * per + t) * 256 + row];
-              u += got[(s * per + t) * 256 + 128 + row];
-            }
-            const float xs = __ldg(a.m.xs + tok);
-            put(a.m, tok, n, silu_mul(product(g, xs, wg_), product(u, xs, wu)));
+      }
+      cluster_sync();
+      const int tn = first % a.tiles_n, t0 = first / a.tiles_n * nt + rank * per, count = min(min(per, nt - rank * per), T - t0);
+      const int* got = reinterpret_cast<const int*>(smem);
+      const int n = GATED ? tn * 128 + row : tn * 256 + tid;
+      if (n < N) {
+        const float w0 = a.m.ws[0][n], w1 = GATED ? a.m.ws[1][n] : 0.f;
+        for (int t = GATED ? b : 0; t < count; t += GATED ? 2 : 1) {
+          int g = 0, u = 0;
+          for (int s = 0; s < a.split; ++s) {
+            const int* p = got + (s * per + t) * 256;
+            g += p[GATED ? row : tid];
+            if (GATED) u += p[128 + row];
           }
+          const float xs = __ldg(a.m.xs + t0 + t);
+          float v[1] = {GATED ? silu_mul(product(g, xs, w0), product(u, xs, w1)) : product(g, xs, w0)};
+          put_tokens<1>(a.m, t0 + t, 1, n, v);
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 21) {
     tc_fence_after();
     tc_dealloc(tmem, 512);
   }
 }
 
+// ------------------------------------------------------------------------------------------------ two CTAs, up to 256 tokens
+__device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on this barrier of both CTAs once every product issued so far by this thread is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// Arrive on this barrier of CTA 0.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, 0;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
+                const __grid_constant__ CUtensorMap map_w1) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];      // packed tiles
+  __shared__ uint64_t bar_a_full[kPairA], bar_a_empty[kPairA];          // converted W (full: CTA 0's, for both)
+  __shared__ uint64_t bar_x_full[kSlots], bar_x_empty[kSlots];          // converted X (likewise)
+  __shared__ uint64_t bar_d_full[2], bar_d_empty[2];                    // accumulators of the halves (empty: CTA 0's)
+  __shared__ uint32_t s_tmem;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
+  const int half = a.nt / 2, part = half / 2, stages = a.stages;        // tokens of a half, and of it this CTA converts
+  const uint32_t stage_bytes = 16384 + half * 128, slot_bytes = half * 256;
+  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
+  const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step_tiles = gridDim.x / 2;
+  const int nk = (a.m.K + kTileK - 1) / kTileK;
+  const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
+
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 8); }
+    for (int i = 0; i < kPairA; ++i) { mbar_init(bar_a_full + i, 8); mbar_init(bar_a_empty + i, 2); }
+    for (int i = 0; i < kSlots; ++i) { mbar_init(bar_x_full + i, 8); mbar_init(bar_x_empty + i, 2); }
+    for (int i = 0; i < 2; ++i) { mbar_init(bar_d_full + i, 1); mbar_init(bar_d_empty + i, 8); }
+    fence_mbar_init();
+  }
+  if (warp == 17) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                         // both CTAs' barriers and columns are there
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  Waits wait{a.m.status, false};
+
+  if (wg == 4) {
+    regs_less<40>();
+    if (warp == 16) {
+      // ================================================================ copies
+      if (lane == 0) {
+        int stage = 0, phase = 1;                         // (the first pass over the ring finds it empty)
+        for (int j = 0; j < my_tiles; ++j) {
+          const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + rank * part;
+          for (int k = 0; k < nk; ++k) {
+            wait(bar_empty + stage, phase);
+            uint8_t* to = smem + stage * stage_bytes;
+            mbar_arrive_expect_tx(bar_full + stage, stage_bytes);
+            if (GATED) {
+              tma_load_2d(to, &map_w0, k * kTileK, tn * 128 + rank * 64, bar_full + stage);
+              tma_load_2d(to + 8192, &map_w1, k * kTileK, tn * 128 + rank * 64, bar_full + stage);
+            } else {
+              tma_load_2d(to, &map_w0, k * kTileK, tn * 256 + rank * 128, bar_full + stage);
+            }
+            tma_load_2d(to + 16384, &map_x, k * kTileK, t0, bar_full + stage);
+            tma_load_2d(to + 16384 + part * 128, &map_x, k * kTileK, t0 + half, bar_full + stage);
+            if (++stage == stages) { stage = 0; phase ^= 1; }
+          }
+        }
+        // (where waits have run out, copies may still be in flight)
+        wait.dead = false;
+        for (int t = max(0, total - stages); t < total; ++t) wait(bar_full + t % stages, (t / stages) & 1);
+      }
+    } else if (warp <= 18 && rank == 0) {
+      // ================================================================ products of half d (both CTAs')
+      const int d = warp - 17;
+      if (lane == 0) {
+        bool dead = false;
+        auto wait_both = [&](uint64_t* bar, int parity) {
+          if (!try_wait_cluster(bar, parity) && !dead) {
+            dead = wait_longer(bar, parity, a.m.status);
+            if (!dead) try_wait_cluster(bar, parity);
+          }
+        };
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24);
+        const uint64_t dx = umma_desc_sw128(xring + d * part * 256);
+        int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
+        for (int j = 0; j < my_tiles; ++j) {
+          bool fresh = true;
+          for (int s = 0; s < nk; ++s) {
+            if (fresh) wait_both(bar_d_empty + d, (seg & 1) ^ 1);
+            wait_both(bar_x_full + xslot, xphase);
+            wait_both(bar_a_full + slot, phase);
+            tc_fence_after();
+            const uint32_t ta = tmem + 256 + slot * 64;
+            const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ts_pair(tmem + d * 128, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
+            commit_pair(bar_a_empty + slot);
+            commit_pair(bar_x_empty + xslot);
+            fresh = false;
+            if (ends_segment(s, nk, d)) {
+              commit_pair(bar_d_full + d);
+              ++seg;
+              fresh = true;
+            }
+            if (++slot == kPairA) { slot = 0; phase ^= 1; }
+            if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
+          }
+        }
+      }
+    }
+  } else if (wg == 3) {
+    // ================================================================ conversion of X
+    regs_less<48>();
+    int stage = 0, phase = 0, slot = 0, sphase = 1;
+    for (int i = 0; i < total; ++i) {
+      wait(bar_x_empty + slot, sphase);
+      wait(bar_full + stage, phase);
+      convert_x(ring + stage * stage_bytes + 16384, xring + slot * slot_bytes, half, part, tid & 127);
+      __syncwarp();
+      if (lane == 0) {
+        arrive_first(bar_x_full + slot);
+        mbar_arrive_relaxed(bar_empty + stage);
+      }
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+      if (++slot == kSlots) { slot = 0; sphase ^= 1; }
+    }
+  } else if (wg == 2) {
+    // ================================================================ conversion of W
+    regs_less<56>();
+    const int row = tid & 127;
+    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 256;
+    int stage = 0, phase = 0, slot = 0, sphase = 1;
+    for (int i = 0; i < total; ++i) {
+      wait(bar_a_empty + slot, sphase);
+      wait(bar_full + stage, phase);
+      tc_fence_after();
+      convert_w(ring + stage * stage_bytes + row * 128, row, ta + slot * 64);
+      __syncwarp();
+      if (lane == 0) {
+        arrive_first(bar_a_full + slot);
+        mbar_arrive_relaxed(bar_empty + stage);
+      }
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+      if (++slot == kPairA) { slot = 0; sphase ^= 1; }
+    }
+  } else {
+    // ================================================================ half d's sums and outputs
+    regs_more<168>();
+    const int d = wg, row = tid & 127;
+    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * 128;
+    int sum[kPairTokens / 2];
+#pragma unroll
+    for (int t = 0; t < kPairTokens / 2; ++t) sum[t] = 0;
+    int seg = 0;
+    for (int j = 0; j < my_tiles; ++j) {
+      for (int s = 0; s < nk; ++s) {
+        if (!ends_segment(s, nk, d)) continue;
+        wait(bar_d_full + d, seg & 1);
+        ++seg;
+        tc_fence_after();
+        take_sums(td, half, sum);
+        __syncwarp();
+        if (lane == 0) arrive_first(bar_d_empty + d);
+      }
+      const int tile = first + j * step_tiles, tn = tile % a.tiles_n;
+      const int n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
+      output_sums<GATED>(a.m, sum, tile / a.tiles_n * a.nt + d * half, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                         // no CTA leaves while the other's barriers or columns are in use
+  if (warp == 17) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Which kernel, and how the work is cut, by an estimate in units of a stage's time of products with 128 tokens (0.5 us).
 struct TcPlan {
+  bool pair;
   int nt, tiles_n, tiles, split, stages;
   uint32_t smem;
 };
 
-static TcPlan plan(const MatArgs& a, bool gated, int sms) {
+static TcPlan plan(const MatArgs& a, bool gated, int sms, const int (&clusters)[4]) {
   TcPlan p;
   p.tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-  const int nk = (a.K + kTileK - 1) / kTileK;
-  // tokens of a tile: as few columns as the waves of tiles need in all
-  p.nt = 16;
-  if (a.T <= kMaxTokens) {
-    p.nt = (a.T + 15) / 16 * 16;
-  } else {
+  const int nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
+  p.pair = a.T > kSmallTokens;
+  p.split = 1;
+  if (p.pair) {
+    // tokens of a tile: as few columns as the waves of tiles need in all
     long long best = 0;
-    for (int nt = kMaxTokens; nt >= 64; nt -= 16) {
-      const long long tiles = (long long)p.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms - 1) / sms * nt;
+    for (int nt = kPairTokens; nt >= 96; nt -= 32) {
+      const long long tiles = (long long)p.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms / 2 - 1) / (sms / 2) * (nt + 16);
       if (best == 0 || cost < best) { best = cost; p.nt = nt; }
     }
+    const int stage = 16384 + p.nt * 64, rest = fixed + kSlots * p.nt * 128;
+    p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
+    p.smem = 1024 + rest + p.stages * stage;
+  } else {
+    p.nt = (a.T + 15) / 16 * 16;
+    while (p.split < 8 && p.split * 2 <= nk && p.tiles_n <= clusters[p.split == 1 ? 1 : p.split == 2 ? 2 : 3]) p.split *= 2;
+    const int stage = 32768 + p.nt * 128, rest = fixed + kSlots * p.nt * 256;
+    p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
+    p.smem = 1024 + rest + p.stages * stage;
   }
   p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
-  p.split = 1;
-  while (p.split < 8 && p.tiles * p.split * 2 <= sms && p.split * 2 <= nk) p.split *= 2;
-  const int stage = 32768 + p.nt * 128, fixed = kSlots * p.nt * 128 + (gated ? kXchgBytes : 0);
-  p.stages = (kSmemLimit - 1024 - fixed) / stage;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.smem = 1024 + fixed + p.stages * stage;
   return p;
 }
 
@@ -456,40 +722,69 @@ static bool map_rows(CUtensorMap* m, const int8_t* q, int rows, int cols, int64_
   return moe_internal::tmap_u8(m, q, 2, dims, strides, box);
 }
 
+static cudaLaunchConfig_t config(int grid, int threads, uint32_t smem, int cluster, cudaLaunchAttribute* at, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  if (cluster > 1) {
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = cluster;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  return cfg;
+}
+
+// Per device, once: the kernels' shared memory, and how many clusters of 2, 4, 8 CTAs of small_kernel run at a time.
+struct Device {
+  bool ready;
+  int clusters[4];
+};
+static Device g_device[64];
+
+static bool prepare(Device& d) {
+  if (d.ready) return true;
+  if (cudaFuncSetAttribute(small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+      cudaFuncSetAttribute(small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
+    return false;
+  for (int i = 1; i < 4; ++i) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = config(1 << i, kSmallThreads, kSmemLimit, 1 << i, &at, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&d.clusters[i], small_kernel<false>, &cfg) != cudaSuccess) return false;
+  }
+  d.ready = true;
+  return true;
+}
+
 moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   const bool gated = a.w[1] != nullptr;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  static int configured[64] = {0};
-  if (!configured[dev]) {
-    if (cudaFuncSetAttribute(tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    configured[dev] = 1;
-  }
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(g_device[dev])) { cudaGetLastError(); return MOE_ERR_CUDA; }
   const int sms = moe_internal::num_sms();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  const TcPlan p = plan(a, gated, sms);
+  if (sms <= 1) return MOE_ERR_CUDA;
+  const TcPlan p = plan(a, gated, sms, g_device[dev].clusters);
   CUtensorMap mx, m0, m1;
-  if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.nt) || !map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], 128)) return MOE_ERR_CUDA;
+  const int box_w = p.pair && gated ? 64 : 128;
+  if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.pair ? p.nt / 4 : p.nt) || !map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w))
+    return MOE_ERR_CUDA;
   m1 = m0;
-  if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], 128)) return MOE_ERR_CUDA;
-  TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.split > 1 ? p.tiles * p.split : min(p.tiles, sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = stream;
+  if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
+  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages};
   cudaLaunchAttribute at;
-  if (p.split > 1) {
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.split;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+  cudaError_t e;
+  if (p.pair) {
+    const cudaLaunchConfig_t cfg = config(2 * min(p.tiles, sms / 2), kPairThreads, p.smem, 1, &at, stream);
+    e = gated ? cudaLaunchKernelEx(&cfg, pair_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, pair_kernel<false>, args, mx, m0, m1);
+  } else {
+    const cudaLaunchConfig_t cfg =
+        config(p.split > 1 ? p.tiles * p.split : min(p.tiles, sms), kSmallThreads, p.smem, p.split, &at, stream);
+    e = gated ? cudaLaunchKernelEx(&cfg, small_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, small_kernel<false>, args, mx, m0, m1);
   }
-  const cudaError_t e = gated ? cudaLaunchKernelEx(&cfg, tc_kernel<true>, args, mx, m0, m1)
-                              : cudaLaunchKernelEx(&cfg, tc_kernel<false>, args, mx, m0, m1);
   if (e != cudaSuccess) { cudaGetLastError(); return MOE_ERR_CUDA; }
   return MOE_OK;
 }
