@@ -62,6 +62,13 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// One lane of the warp. (Loops that issue products run in the whole warp, so that descriptors and addresses stay in uniform
+// registers, and only the issue itself in this lane: under `lane == 0` a stage took 550 cycles more.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -168,23 +175,22 @@ __device__ __forceinline__ void convert_w(uint32_t from, int row, uint32_t taddr
   tc_fence_before();
 }
 
-// A stage of X, `rows` (up to 128) tokens of 128 codes at `from` -> operands at `to`: parts of `part` rows, each [two halves of
-// K][part rows][64 values], swizzled. t: thread of 128. Eight lanes have four 16-byte pieces of rows r and r ^ 5: their reads and
-// their writes meet no bank twice.
+// A stage of X, `rows` (a multiple of 16, up to 128) tokens of 128 codes at `from` -> operands at `to`: parts of `part` rows, each
+// [two halves of K][part rows][64 values], swizzled. t: thread of 128. A warp has the 16-byte pieces of 8 rows' half; eight lanes
+// have four pieces of rows r and r ^ 5, so that their reads and their writes meet no bank twice.
 __device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, int part, int t) {
-  const int c = t & 3, pair = (t >> 3) & 3, r0 = (t >> 5) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r0 & 7;
-  const uint32_t d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint32_t src = from + r0 * 128 + (((half * 4 + c) ^ sw) << 4);
+  const int c = t & 3, pair = (t >> 3) & 3, half = (t >> 5) & 1, r0 = (t >> 6) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r0 & 7;
+  const uint32_t src = from + r0 * 128 + (((half * 4 + c) ^ sw) << 4), d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
+#pragma unroll 1
+  for (int g = 0; g < rows; g += 64) {
     uint4 v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (r0 + 32 * e < rows) v[e] = ld_shared(src + e * 4096);
+      if (g + 16 * e < rows) v[e] = ld_shared(src + (g + 16 * e) * 128);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = r0 + 32 * e;
-      if (r < rows) {
+      const int r = g + 16 * e + r0;
+      if (g + 16 * e < rows) {
         uint32_t h[8];
         convert4(v[e].x, h[0], h[1]);
         convert4(v[e].y, h[2], h[3]);
@@ -339,33 +345,31 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     } else if (warp <= 22) {
       // ================================================================ products of block b
       const int b = warp - 21;
-      if (lane == 0) {
-        const uint32_t idesc = idesc_f16(nt);
-        const uint64_t dx = umma_desc_sw128(xring);
-        int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
-        for (int j = 0; j < my_tiles; ++j) {
-          bool fresh = true;
-          for (int s = 0; s < per_tile; ++s) {
-            if (fresh) wait(bar_d_empty + b, (seg & 1) ^ 1);
-            wait(bar_x_full + xslot, xphase);
-            wait(&bar_a_full[b][slot], phase);
-            tc_fence_after();
-            const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
-            const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+      const uint32_t idesc = idesc_f16(nt), td = tmem + b * 64;
+      const uint64_t dx = umma_desc_sw128(xring);
+      int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
+      for (int j = 0; j < my_tiles; ++j) {
+        bool fresh = true;
+        for (int s = 0; s < per_tile; ++s) {
+          if (fresh) wait(bar_d_empty + b, (seg & 1) ^ 1);
+          wait(bar_x_full + xslot, xphase);
+          wait(&bar_a_full[b][slot], phase);
+          tc_fence_after();
+          const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
+          const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+          const bool ends = ends_segment(s, per_tile, b);
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ts(tmem + b * 64, ta + 8 * k, dxs + (k >> 2) * (nt * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
+            for (int k = 0; k < 8; ++k) mma_f16_ts(td, ta + 8 * k, dxs + (k >> 2) * (nt * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
             tc_commit(&bar_a_empty[b][slot]);
             tc_commit(bar_x_empty + xslot);
-            fresh = false;
-            if (ends_segment(s, per_tile, b)) {
-              tc_commit(bar_d_full + b);
-              ++seg;
-              fresh = true;
-            }
-            if (++slot == kSmallA) { slot = 0; phase ^= 1; }
-            if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
+            if (ends) tc_commit(bar_d_full + b);
           }
+          __syncwarp();
+          fresh = ends;
+          seg += ends;
+          if (++slot == kSmallA) { slot = 0; phase ^= 1; }
+          if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
         }
       }
     }
@@ -491,23 +495,14 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// Arrive on this barrier of CTA 0.
+// Arrive on this barrier of CTA 0. The release is for this CTA: what it orders (operands in this CTA's shared memory and TMEM) is
+// read by this CTA's tensor core. (For the cluster it took 1,000 cycles.)
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, 0;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n\t}" ::"r"(
+      "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, 0;\n\tmbarrier.arrive.release.cta.shared::cluster.b64 _, [p];\n\t}" ::"r"(
           smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
@@ -576,40 +571,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp <= 18 && rank == 0) {
       // ================================================================ products of half d (both CTAs')
       const int d = warp - 17;
-      if (lane == 0) {
-        bool dead = false;
-        auto wait_both = [&](uint64_t* bar, int parity) {
-          if (!try_wait_cluster(bar, parity) && !dead) {
-            dead = wait_longer(bar, parity, a.m.status);
-            if (!dead) try_wait_cluster(bar, parity);
-          }
-        };
-        const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24);
-        const uint64_t dx = umma_desc_sw128(xring + d * part * 256);
-        int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
-        for (int j = 0; j < my_tiles; ++j) {
-          bool fresh = true;
-          for (int s = 0; s < nk; ++s) {
-            if (fresh) wait_both(bar_d_empty + d, (seg & 1) ^ 1);
-            wait_both(bar_x_full + xslot, xphase);
-            wait_both(bar_a_full + slot, phase);
-            tc_fence_after();
-            const uint32_t ta = tmem + 256 + slot * 64;
-            const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * 128;
+      const uint64_t dx = umma_desc_sw128(xring + d * part * 256);
+      int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
+      for (int j = 0; j < my_tiles; ++j) {
+        bool fresh = true;
+        for (int s = 0; s < nk; ++s) {
+          if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
+          wait(bar_x_full + xslot, xphase);
+          wait(bar_a_full + slot, phase);
+          tc_fence_after();
+          const uint32_t ta = tmem + 256 + slot * 64;
+          const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+          const bool ends = ends_segment(s, nk, d);
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ts_pair(tmem + d * 128, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
+            for (int k = 0; k < 8; ++k) mma_f16_ts_pair(td, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
             commit_pair(bar_a_empty + slot);
             commit_pair(bar_x_empty + xslot);
-            fresh = false;
-            if (ends_segment(s, nk, d)) {
-              commit_pair(bar_d_full + d);
-              ++seg;
-              fresh = true;
-            }
-            if (++slot == kPairA) { slot = 0; phase ^= 1; }
-            if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
+            if (ends) commit_pair(bar_d_full + d);
           }
+          __syncwarp();
+          fresh = ends;
+          seg += ends;
+          if (++slot == kPairA) { slot = 0; phase ^= 1; }
+          if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
         }
       }
     }
