@@ -30,7 +30,8 @@ constexpr int kSegment = 8;            // stages that fp32 adds exactly
 constexpr int kMaxStages = 8;
 constexpr int kSlots = 2;              // converted stages of X in flight
 constexpr int kSmallTokens = 64, kSmallThreads = 768, kSmallA = 3;    // A slots: TMEM columns 128 + (block * 3 + slot) * 64
-constexpr int kPairTokens = 256, kPairThreads = 640, kPairA = 4;      // A slots: TMEM columns 256 + slot * 64
+constexpr int kPairTokens = 256, kPairThreads = 512, kPairA = 4;      // A slots: TMEM columns 256 + slot * 64
+constexpr int kPairX = 3, kPairLag = 2;
 constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
 constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
 
@@ -143,6 +144,12 @@ struct Waits {
   __device__ __forceinline__ void operator()(uint64_t* bar, int parity) {
     if (!mbar_try_wait(bar, parity) && !dead) dead = wait_longer(bar, parity, status);
   }
+  // two at once: a wait takes 140 cycles even where the barrier is ready
+  __device__ __forceinline__ void operator()(uint64_t* bar, int parity, uint64_t* bar2, int parity2) {
+    const bool ok = mbar_try_wait(bar, parity), ok2 = mbar_try_wait(bar2, parity2);
+    if (!ok && !dead) dead = wait_longer(bar, parity, status);
+    if (!ok2 && !dead) dead = wait_longer(bar2, parity2, status);
+  }
 };
 
 // Stage i of a tile's `stages` ends a segment of accumulator d: every kSegment stages, the second's half as many earlier, and
@@ -175,48 +182,43 @@ __device__ __forceinline__ void convert_w(uint32_t from, int row, uint32_t taddr
   tc_fence_before();
 }
 
-// A stage of X, `rows` (a multiple of 16, up to 128) tokens of 128 codes at `from` -> operands at `to`: parts of `part` rows, each
-// [two halves of K][part rows][64 values], swizzled. t: thread of 128. A warp has the 16-byte pieces of 8 rows' half; eight lanes
-// have four pieces of rows r and r ^ 5, so that their reads and their writes meet no bank twice.
-__device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, int part, int t) {
-  const int c = t & 3, pair = (t >> 3) & 3, half = (t >> 5) & 1, r0 = (t >> 6) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r0 & 7;
-  const uint32_t src = from + r0 * 128 + (((half * 4 + c) ^ sw) << 4), d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
-#pragma unroll 1
-  for (int g = 0; g < rows; g += 64) {
-    uint4 v[4];
+// A stage of X, `rows` (a multiple of 8, up to 64) tokens of 128 codes at `from` -> the operand at `to`: [two halves of K][rows][64
+// values], swizzled. t: thread of 128. A warp has the 16-byte pieces of 8 rows' half; eight lanes have four pieces of rows r and
+// r ^ 5, so that their reads and their writes meet no bank twice.
+__device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, int t) {
+  const int c = t & 3, pair = (t >> 3) & 3, half = (t >> 5) & 1, r = (t >> 6) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r & 7;
+  const uint32_t src = from + r * 128 + (((half * 4 + c) ^ sw) << 4), dst = to + (half * rows + r) * 128;
+  const uint32_t d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
+  uint4 v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (g + 16 * e < rows) v[e] = ld_shared(src + (g + 16 * e) * 128);
+  for (int e = 0; e < 4; ++e)
+    if (r + 16 * e < rows) v[e] = ld_shared(src + e * 2048);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = g + 16 * e + r0;
-      if (g + 16 * e < rows) {
-        uint32_t h[8];
-        convert4(v[e].x, h[0], h[1]);
-        convert4(v[e].y, h[2], h[3]);
-        convert4(v[e].z, h[4], h[5]);
-        convert4(v[e].w, h[6], h[7]);
-        // part p begins 256 part bytes after the one before it, its row 0 is row p part
-        const uint32_t dst = to + r * 128 + (half + (r >= part)) * (part * 128);
-        st_shared(dst + d0, h[0], h[1], h[2], h[3]);
-        st_shared(dst + d1, h[4], h[5], h[6], h[7]);
-      }
+  for (int e = 0; e < 4; ++e)
+    if (r + 16 * e < rows) {
+      uint32_t h[8];
+      convert4(v[e].x, h[0], h[1]);
+      convert4(v[e].y, h[2], h[3]);
+      convert4(v[e].z, h[4], h[5]);
+      convert4(v[e].w, h[6], h[7]);
+      st_shared(dst + e * 2048 + d0, h[0], h[1], h[2], h[3]);
+      st_shared(dst + e * 2048 + d1, h[4], h[5], h[6], h[7]);
     }
-  }
   fence_async_smem();
 }
 
 // Adds accumulator columns 0 .. n - 1 of the thread's lane, exact integers, to its sums
 template <int COLS>
 __device__ __forceinline__ void take_sums(uint32_t taddr, int n, int (&sum)[COLS]) {
+  uint32_t r[2][8];
+  tc_ld8(taddr, r[0]);
 #pragma unroll
-  for (int c = 0; c < COLS / 16; ++c)
-    if (c * 16 < n) {
-      uint32_t r[16];
-      tc_ld16(taddr + 16 * c, r);
+  for (int c = 0; c < COLS / 8; ++c)
+    if (c * 8 < n) {
       tc_wait_ld();
+      if ((c + 1) * 8 < n) tc_ld8(taddr + 8 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum[16 * c + e] += __float2int_rn(__uint_as_float(r[e]));
+      for (int e = 0; e < 8; ++e) sum[8 * c + e] += __float2int_rn(__uint_as_float(r[c & 1][e]));
     }
   tc_fence_before();
 }
@@ -234,22 +236,35 @@ __device__ __forceinline__ void give_sums(int c, int (&sum)[COLS], int (&r)[16])
       }
     }
 }
+// The scales that a tile's outputs need, loaded long before: tokens t0 + lane, + 32, ... of the warp's lanes, and channel n's.
+template <int COLS>
+struct Scales {
+  float x[(COLS + 31) / 32], w;
+  __device__ __forceinline__ void load(const MatArgs& a, const float* ws, int t0, int n) {
+#pragma unroll
+    for (int i = 0; i < (COLS + 31) / 32; ++i) x[i] = __ldg(a.xs + min(t0 + (int)(threadIdx.x & 31) + 32 * i, a.T - 1));
+    w = __ldg(ws + min(n, a.N - 1));
+  }
+};
 // The outputs of `count` tokens from t0 on, channel n (none if n >= N). Gated: the thread has gate's (side 0) or up's sums, and
 // the thread with the other of the same n is at the same idx (of `width`) on the other side; of 16 tokens side 0 finishes the first
 // eight, side 1 the last, and what the other needs goes through shared memory (two buffers in turn), ordered by barrier `bar` among
 // 2 width threads.
 template <bool GATED, int COLS>
-__device__ __forceinline__ void output_sums(const MatArgs& a, int (&sum)[COLS], int t0, int count, int n, int side, uint32_t xchg,
-                                            int idx, int width, int bar) {
-  const float ws = n < a.N ? a.ws[GATED ? side : 0][n] : 0.f;
+__device__ __forceinline__ void output_sums(const MatArgs& a, int (&sum)[COLS], const Scales<COLS>& sc, int t0, int count, int n, int side,
+                                            uint32_t xchg, int idx, int width, int bar) {
   int r[16];
 #pragma unroll 1
   for (int c = 0; c * 16 < count; ++c) {
     give_sums(c, sum, r);
     const int t1 = t0 + 16 * c;
+    float xs = sc.x[0];
+#pragma unroll
+    for (int i = 1; i < (COLS + 31) / 32; ++i)
+      if (c >> 1 == i) xs = sc.x[i];
     float v[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = product(r[e], __ldg(a.xs + min(t1 + e, a.T - 1)), ws);
+    for (int e = 0; e < 16; ++e) v[e] = product(r[e], __shfl_sync(0xFFFFFFFFu, xs, 16 * (c & 1) + e), sc.w);
     if (!GATED) {
       if (n < a.N) put_tokens<16>(a, t1, a.T - t1, n, v);
     } else {
@@ -352,8 +367,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
         bool fresh = true;
         for (int s = 0; s < per_tile; ++s) {
           if (fresh) wait(bar_d_empty + b, (seg & 1) ^ 1);
-          wait(bar_x_full + xslot, xphase);
-          wait(&bar_a_full[b][slot], phase);
+          wait(bar_x_full + xslot, xphase, &bar_a_full[b][slot], phase);
           tc_fence_after();
           const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
           const uint64_t dxs = dx + xslot * (slot_bytes / 16);
@@ -377,12 +391,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else if (wg == 4) {
     // ================================================================ conversion of X
-    regs_less<56>();
+    regs_less<40>();
     int stage = 0, phase = 0, slot = 0, sphase = 1;
     for (int i = 0; i < total; ++i) {
-      wait(bar_x_empty + slot, sphase);
-      wait(bar_full + stage, phase);
-      convert_x(ring + stage * stage_bytes + 32768, xring + slot * slot_bytes, nt, nt, tid & 127);
+      wait(bar_x_empty + slot, sphase, bar_full + stage, phase);
+      convert_x(ring + stage * stage_bytes + 32768, xring + slot * slot_bytes, nt, tid & 127);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar_x_full + slot);
@@ -395,13 +408,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else if (wg >= 2) {
     // ================================================================ conversion of block b's W
-    regs_less<64>();
+    regs_less<48>();
     const int b = wg - 2, row = tid & 127;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 128 + b * kSmallA * 64;
     int stage = 0, phase = 0, slot = 0, sphase = 1;
     for (int i = 0; i < total; ++i) {
-      wait(&bar_a_empty[b][slot], sphase);
-      wait(bar_full + stage, phase);
+      wait(&bar_a_empty[b][slot], sphase, bar_full + stage, phase);
       tc_fence_after();
       convert_w(ring + stage * stage_bytes + b * 16384 + row * 128, row, ta + slot * 64);
       __syncwarp();
@@ -416,14 +428,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else {
     // ================================================================ block b's sums and outputs
-    regs_more<128>();
+    regs_more<152>();
     const int b = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
     int sum[kSmallTokens];
 #pragma unroll
     for (int t = 0; t < kSmallTokens; ++t) sum[t] = 0;
     int seg = 0;
+    Scales<kSmallTokens> scales;
     for (int j = 0; j < my_tiles; ++j) {
+      const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
+      const int n = GATED ? tn * 128 + row : tn * 256 + b * 128 + row;
+      scales.load(a.m, a.m.ws[GATED ? b : 0], t0, n);
       for (int s = 0; s < per_tile; ++s) {
         if (!ends_segment(s, per_tile, b)) continue;
         wait(bar_d_full + b, seg & 1);
@@ -433,10 +449,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_d_empty + b);
       }
-      if (a.split == 1) {
-        const int tile = first + j * step_tiles, tn = tile % a.tiles_n;
-        output_sums<GATED>(a.m, sum, tile / a.tiles_n * nt, nt, GATED ? tn * 128 + row : tn * 256 + b * 128 + row, b, xchg, row, 128, 1);
-      }
+      if (a.split == 1) output_sums<GATED>(a.m, sum, scales, t0, nt, n, b, xchg, row, 128, 1);
     }
     if (a.split > 1) {
       // every CTA of the cluster is through with its rings; token t is finished by CTA t / per
@@ -511,26 +524,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];      // packed tiles
   __shared__ uint64_t bar_a_full[kPairA], bar_a_empty[kPairA];          // converted W (full: CTA 0's, for both)
-  __shared__ uint64_t bar_x_full[kSlots], bar_x_empty[kSlots];          // converted X (likewise)
+  __shared__ uint64_t bar_x_full[2][kPairX], bar_x_empty[2][kPairX];    // converted X of the halves (likewise)
   __shared__ uint64_t bar_d_full[2], bar_d_empty[2];                    // accumulators of the halves (empty: CTA 0's)
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
   const int half = a.nt / 2, part = half / 2, stages = a.stages;        // tokens of a half, and of it this CTA converts
-  const uint32_t stage_bytes = 16384 + half * 128, slot_bytes = half * 256;
-  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
+  const uint32_t stage_bytes = 16384 + half * 128, slot_bytes = part * 256;
+  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + 2 * kPairX * slot_bytes;
   const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step_tiles = gridDim.x / 2;
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
 
   if (tid == 0) {
-    for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 8); }
+    for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 12); }
     for (int i = 0; i < kPairA; ++i) { mbar_init(bar_a_full + i, 8); mbar_init(bar_a_empty + i, 2); }
-    for (int i = 0; i < kSlots; ++i) { mbar_init(bar_x_full + i, 8); mbar_init(bar_x_empty + i, 2); }
-    for (int i = 0; i < 2; ++i) { mbar_init(bar_d_full + i, 1); mbar_init(bar_d_empty + i, 8); }
+    for (int d = 0; d < 2; ++d) {
+      for (int i = 0; i < kPairX; ++i) { mbar_init(&bar_x_full[d][i], 8); mbar_init(&bar_x_empty[d][i], 1); }
+      mbar_init(bar_d_full + d, 1);
+      mbar_init(bar_d_empty + d, 8);
+    }
     fence_mbar_init();
   }
-  if (warp == 17) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
@@ -541,9 +557,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = s_tmem;
   Waits wait{a.m.status, false};
 
-  if (wg == 4) {
+  if (wg == 3) {
     regs_less<40>();
-    if (warp == 16) {
+    if (warp == 12) {
       // ================================================================ copies
       if (lane == 0) {
         int stage = 0, phase = 1;                         // (the first pass over the ring finds it empty)
@@ -568,18 +584,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         wait.dead = false;
         for (int t = max(0, total - stages); t < total; ++t) wait(bar_full + t % stages, (t / stages) & 1);
       }
-    } else if (warp <= 18 && rank == 0) {
+    } else if (warp <= 14 && rank == 0) {
       // ================================================================ products of half d (both CTAs')
-      const int d = warp - 17;
+      const int d = warp - 13;
       const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * 128;
-      const uint64_t dx = umma_desc_sw128(xring + d * part * 256);
+      const uint64_t dx = umma_desc_sw128(xring + d * kPairX * slot_bytes);
       int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
       for (int j = 0; j < my_tiles; ++j) {
         bool fresh = true;
         for (int s = 0; s < nk; ++s) {
           if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
-          wait(bar_x_full + xslot, xphase);
-          wait(bar_a_full + slot, phase);
+          wait(&bar_x_full[d][xslot], xphase, bar_a_full + slot, phase);
           tc_fence_after();
           const uint32_t ta = tmem + 256 + slot * 64;
           const uint64_t dxs = dx + xslot * (slot_bytes / 16);
@@ -588,42 +603,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_f16_ts_pair(td, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
             commit_pair(bar_a_empty + slot);
-            commit_pair(bar_x_empty + xslot);
+            commit_pair(&bar_x_empty[d][xslot]);
             if (ends) commit_pair(bar_d_full + d);
           }
           __syncwarp();
           fresh = ends;
           seg += ends;
           if (++slot == kPairA) { slot = 0; phase ^= 1; }
-          if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
+          if (++xslot == kPairX) { xslot = 0; xphase ^= 1; }
         }
       }
     }
-  } else if (wg == 3) {
-    // ================================================================ conversion of X
-    regs_less<48>();
-    int stage = 0, phase = 0, slot = 0, sphase = 1;
-    for (int i = 0; i < total; ++i) {
-      wait(bar_x_empty + slot, sphase);
-      wait(bar_full + stage, phase);
-      convert_x(ring + stage * stage_bytes + 16384, xring + slot * slot_bytes, half, part, tid & 127);
-      __syncwarp();
-      if (lane == 0) {
-        arrive_first(bar_x_full + slot);
-        mbar_arrive_relaxed(bar_empty + stage);
-      }
-      if (++stage == stages) { stage = 0; phase ^= 1; }
-      if (++slot == kSlots) { slot = 0; sphase ^= 1; }
-    }
   } else if (wg == 2) {
     // ================================================================ conversion of W
-    regs_less<56>();
+    regs_less<40>();
     const int row = tid & 127;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 256;
     int stage = 0, phase = 0, slot = 0, sphase = 1;
     for (int i = 0; i < total; ++i) {
-      wait(bar_a_empty + slot, sphase);
-      wait(bar_full + stage, phase);
+      wait(bar_a_empty + slot, sphase, bar_full + stage, phase);
       tc_fence_after();
       convert_w(ring + stage * stage_bytes + row * 128, row, ta + slot * 64);
       __syncwarp();
@@ -635,17 +633,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (++slot == kPairA) { slot = 0; sphase ^= 1; }
     }
   } else {
-    // ================================================================ half d's sums and outputs
-    regs_more<168>();
+    // ================================================================ half d: conversion of its tokens, sums, outputs
+    // A segment's sums are taken when two more stages have been converted, so that the tensor cores have some to go on with.
+    regs_more<216>();
     const int d = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * 128;
     int sum[kPairTokens / 2];
 #pragma unroll
     for (int t = 0; t < kPairTokens / 2; ++t) sum[t] = 0;
-    int seg = 0;
-    for (int j = 0; j < my_tiles; ++j) {
-      for (int s = 0; s < nk; ++s) {
-        if (!ends_segment(s, nk, d)) continue;
+    Scales<kPairTokens / 2> scales;
+    int stage = 0, phase = 0, slot = 0, sphase = 1, seg = 0, ds = 0, tile = first, t0 = 0, n = 0;
+    for (int at = 0; at < total + kPairLag; ++at) {
+      if (at < total) {
+        wait(&bar_x_empty[d][slot], sphase, bar_full + stage, phase);
+        convert_x(ring + stage * stage_bytes + 16384 + d * part * 128, xring + (d * kPairX + slot) * slot_bytes, part, tid & 127);
+        __syncwarp();
+        if (lane == 0) {
+          arrive_first(&bar_x_full[d][slot]);
+          mbar_arrive_relaxed(bar_empty + stage);
+        }
+        if (++stage == stages) { stage = 0; phase ^= 1; }
+        if (++slot == kPairX) { slot = 0; sphase ^= 1; }
+      }
+      if (at < kPairLag) continue;
+      if (ds == 0) {
+        const int tn = tile % a.tiles_n;
+        t0 = tile / a.tiles_n * a.nt + d * half;
+        n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
+        scales.load(a.m, a.m.ws[GATED ? row >> 6 : 0], t0, n);
+      }
+      if (ends_segment(ds, nk, d)) {
         wait(bar_d_full + d, seg & 1);
         ++seg;
         tc_fence_after();
@@ -653,16 +670,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_first(bar_d_empty + d);
       }
-      const int tile = first + j * step_tiles, tn = tile % a.tiles_n;
-      const int n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
-      output_sums<GATED>(a.m, sum, tile / a.tiles_n * a.nt + d * half, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
+      if (++ds == nk) {
+        output_sums<GATED>(a.m, sum, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
+        ds = 0;
+        tile += step_tiles;
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                         // no CTA leaves while the other's barriers or columns are in use
-  if (warp == 17) {
+  if (warp == 13) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
@@ -688,7 +707,7 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms, const int (&clusters)[
       const long long tiles = (long long)p.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms / 2 - 1) / (sms / 2) * (nt + 16);
       if (best == 0 || cost < best) { best = cost; p.nt = nt; }
     }
-    const int stage = 16384 + p.nt * 64, rest = fixed + kSlots * p.nt * 128;
+    const int stage = 16384 + p.nt * 64, rest = fixed + kPairX * p.nt * 128;
     p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
     p.smem = 1024 + rest + p.stages * stage;
   } else {
