@@ -30,8 +30,7 @@ constexpr int kSegment = 8;            // stages that fp32 adds exactly
 constexpr int kMaxStages = 8;
 constexpr int kSlots = 2;              // converted stages of X in flight
 constexpr int kSmallTokens = 64, kSmallThreads = 768, kSmallA = 3;    // A slots: TMEM columns 128 + (block * 3 + slot) * 64
-constexpr int kPairTokens = 256, kPairThreads = 512, kPairA = 4;      // A slots: TMEM columns 256 + slot * 64
-constexpr int kPairX = 3, kPairLag = 2;
+constexpr int kPairTokens = 256, kPairThreads = 512, kPairStages = 4;  // A: TMEM columns 256 + stage * 64
 constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
 constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
 
@@ -186,16 +185,16 @@ __device__ __forceinline__ void convert_w(uint32_t from, int row, uint32_t taddr
 // values], swizzled. t: thread of 128. A warp has the 16-byte pieces of 8 rows' half; eight lanes have four pieces of rows r and
 // r ^ 5, so that their reads and their writes meet no bank twice.
 __device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, int t) {
-  const int c = t & 3, pair = (t >> 3) & 3, half = (t >> 5) & 1, r = (t >> 6) * 8 + ((t & 4) ? pair ^ 5 : pair), sw = r & 7;
+  const int c = t & 3, pair = (t >> 3) & 3, half = (t >> 5) & 1, w = (t >> 6) * 8, r = w + ((t & 4) ? pair ^ 5 : pair), sw = r & 7;
   const uint32_t src = from + r * 128 + (((half * 4 + c) ^ sw) << 4), dst = to + (half * rows + r) * 128;
   const uint32_t d0 = ((2 * c) ^ sw) << 4, d1 = ((2 * c + 1) ^ sw) << 4;
   uint4 v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (r + 16 * e < rows) v[e] = ld_shared(src + e * 2048);
+    if (w + 16 * e < rows) v[e] = ld_shared(src + e * 2048);
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (r + 16 * e < rows) {
+    if (w + 16 * e < rows) {
       uint32_t h[8];
       convert4(v[e].x, h[0], h[1]);
       convert4(v[e].y, h[2], h[3]);
@@ -204,7 +203,6 @@ __device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, 
       st_shared(dst + e * 2048 + d0, h[0], h[1], h[2], h[3]);
       st_shared(dst + e * 2048 + d1, h[4], h[5], h[6], h[7]);
     }
-  fence_async_smem();
 }
 
 // Adds accumulator columns 0 .. n - 1 of the thread's lane, exact integers, to its sums
@@ -396,6 +394,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     for (int i = 0; i < total; ++i) {
       wait(bar_x_empty + slot, sphase, bar_full + stage, phase);
       convert_x(ring + stage * stage_bytes + 32768, xring + slot * slot_bytes, nt, tid & 127);
+      fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar_x_full + slot);
@@ -516,34 +515,55 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
+// X for pair_kernel: rows of `pitch` binary16 values (K rounded up to 64), in convert4's order, zeros past K. 16 codes a thread.
+__global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, uint32_t pieces, uint8_t* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // (pair_kernel may set itself up meanwhile)
+  const uint32_t step = gridDim.x * 256u, first = blockIdx.x * 256u + threadIdx.x, step_rows = step / pieces, step_k = step % pieces;
+  uint32_t k = first % pieces;
+  for (int64_t row = first / pieces; row < rows; row += step_rows) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if ((int)(k * 16) < K) v = __ldg(reinterpret_cast<const uint4*>(x + row * stride + k * 16));
+    uint32_t h[8];
+    convert4(v.x, h[0], h[1]);
+    convert4(v.y, h[2], h[3]);
+    convert4(v.z, h[4], h[5]);
+    convert4(v.w, h[6], h[7]);
+    uint4* to = reinterpret_cast<uint4*>(out) + (row * pieces + k) * 2;
+    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    k += step_k;
+    if (k >= pieces) { k -= pieces; ++row; }
+  }
+}
+
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
                 const __grid_constant__ CUtensorMap map_w1) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
-  __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];      // packed tiles
-  __shared__ uint64_t bar_a_full[kPairA], bar_a_empty[kPairA];          // converted W (full: CTA 0's, for both)
-  __shared__ uint64_t bar_x_full[2][kPairX], bar_x_empty[2][kPairX];    // converted X of the halves (likewise)
+  // A stage: W's codes, X in binary16. It is full when its copies have landed, ready when W has been converted (CTA 0's barrier: its
+  // four warps, and one arrival that passes on CTA 1's), and empty when both halves' products are done; then its columns of A
+  // are free as well.
+  __shared__ uint64_t bar_full[kPairStages], bar_ready[kPairStages], bar_empty[kPairStages];
   __shared__ uint64_t bar_d_full[2], bar_d_empty[2];                    // accumulators of the halves (empty: CTA 0's)
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
-  const int half = a.nt / 2, part = half / 2, stages = a.stages;        // tokens of a half, and of it this CTA converts
-  const uint32_t stage_bytes = 16384 + half * 128, slot_bytes = part * 256;
-  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + 2 * kPairX * slot_bytes;
+  const int half = a.nt / 2, part = half / 2;                           // tokens of a half, and of it in this CTA
+  const uint32_t stage_bytes = 16384 + half * 256;
+  const uint32_t ring = smem_u32(smem), xchg = ring + kPairStages * stage_bytes;
   const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step_tiles = gridDim.x / 2;
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
 
   if (tid == 0) {
-    for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 12); }
-    for (int i = 0; i < kPairA; ++i) { mbar_init(bar_a_full + i, 8); mbar_init(bar_a_empty + i, 2); }
-    for (int d = 0; d < 2; ++d) {
-      for (int i = 0; i < kPairX; ++i) { mbar_init(&bar_x_full[d][i], 8); mbar_init(&bar_x_empty[d][i], 1); }
-      mbar_init(bar_d_full + d, 1);
-      mbar_init(bar_d_empty + d, 8);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(bar_full + i, 1);
+      mbar_init(bar_ready + i, 5 - rank);
+      mbar_init(bar_empty + i, 2);
     }
+    for (int d = 0; d < 2; ++d) { mbar_init(bar_d_full + d, 1); mbar_init(bar_d_empty + d, 8); }
     fence_mbar_init();
   }
   if (warp == 13) {
@@ -562,6 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (warp == 12) {
       // ================================================================ copies
       if (lane == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // X in binary16 is there
         int stage = 0, phase = 1;                         // (the first pass over the ring finds it empty)
         for (int j = 0; j < my_tiles; ++j) {
           const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + rank * part;
@@ -575,43 +596,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             } else {
               tma_load_2d(to, &map_w0, k * kTileK, tn * 256 + rank * 128, bar_full + stage);
             }
-            tma_load_2d(to + 16384, &map_x, k * kTileK, t0, bar_full + stage);
-            tma_load_2d(to + 16384 + part * 128, &map_x, k * kTileK, t0 + half, bar_full + stage);
-            if (++stage == stages) { stage = 0; phase ^= 1; }
+            tma_load_3d(to + 16384, &map_x, 0, t0, 2 * k, bar_full + stage);
+            tma_load_3d(to + 16384 + part * 256, &map_x, 0, t0 + half, 2 * k, bar_full + stage);
+            if (++stage == kPairStages) { stage = 0; phase ^= 1; }
           }
         }
         // (where waits have run out, copies may still be in flight)
         wait.dead = false;
-        for (int t = max(0, total - stages); t < total; ++t) wait(bar_full + t % stages, (t / stages) & 1);
+        for (int t = max(0, total - kPairStages); t < total; ++t) wait(bar_full + t % kPairStages, (t / kPairStages) & 1);
       }
     } else if (warp <= 14 && rank == 0) {
       // ================================================================ products of half d (both CTAs')
       const int d = warp - 13;
       const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * 128;
-      const uint64_t dx = umma_desc_sw128(xring + d * kPairX * slot_bytes);
-      int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
+      const uint64_t dx = umma_desc_sw128(ring + 16384 + d * part * 256);
+      int stage = 0, phase = 0, seg = 0;
       for (int j = 0; j < my_tiles; ++j) {
         bool fresh = true;
         for (int s = 0; s < nk; ++s) {
           if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
-          wait(&bar_x_full[d][xslot], xphase, bar_a_full + slot, phase);
+          wait(bar_ready + stage, phase);
           tc_fence_after();
-          const uint32_t ta = tmem + 256 + slot * 64;
-          const uint64_t dxs = dx + xslot * (slot_bytes / 16);
+          const uint32_t ta = tmem + 256 + stage * 64;
+          const uint64_t dxs = dx + stage * (stage_bytes / 16);
           const bool ends = ends_segment(s, nk, d);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_f16_ts_pair(td, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
-            commit_pair(bar_a_empty + slot);
-            commit_pair(&bar_x_empty[d][xslot]);
+            commit_pair(bar_empty + stage);
             if (ends) commit_pair(bar_d_full + d);
           }
           __syncwarp();
           fresh = ends;
           seg += ends;
-          if (++slot == kPairA) { slot = 0; phase ^= 1; }
-          if (++xslot == kPairX) { xslot = 0; xphase ^= 1; }
+          if (++stage == kPairStages) { stage = 0; phase ^= 1; }
         }
+      }
+    } else if (warp == 13) {
+      // ================================================================ CTA 1: stages that are ready here, passed on to CTA 0
+      // (an arrival in the other CTA takes 100 cycles more than one here, which the converting warps do not have)
+      int stage = 0, phase = 0;
+      for (int i = 0; i < total; ++i) {
+        wait(bar_ready + stage, phase);
+        if (lane == 0) arrive_first(bar_ready + stage);
+        if (++stage == kPairStages) { stage = 0; phase ^= 1; }
       }
     }
   } else if (wg == 2) {
@@ -619,22 +647,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     regs_less<40>();
     const int row = tid & 127;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 256;
-    int stage = 0, phase = 0, slot = 0, sphase = 1;
+    int stage = 0, phase = 0;
     for (int i = 0; i < total; ++i) {
-      wait(bar_a_empty + slot, sphase, bar_full + stage, phase);
+      wait(bar_full + stage, phase);
       tc_fence_after();
-      convert_w(ring + stage * stage_bytes + row * 128, row, ta + slot * 64);
+      convert_w(ring + stage * stage_bytes + row * 128, row, ta + stage * 64);
       __syncwarp();
-      if (lane == 0) {
-        arrive_first(bar_a_full + slot);
-        mbar_arrive_relaxed(bar_empty + stage);
-      }
-      if (++stage == stages) { stage = 0; phase ^= 1; }
-      if (++slot == kPairA) { slot = 0; sphase ^= 1; }
+      if (lane == 0) mbar_arrive(bar_ready + stage);
+      if (++stage == kPairStages) { stage = 0; phase ^= 1; }
     }
   } else {
-    // ================================================================ half d: conversion of its tokens, sums, outputs
-    // A segment's sums are taken when two more stages have been converted, so that the tensor cores have some to go on with.
+    // ================================================================ half d's sums and outputs
     regs_more<216>();
     const int d = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * 128;
@@ -642,27 +665,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
     for (int t = 0; t < kPairTokens / 2; ++t) sum[t] = 0;
     Scales<kPairTokens / 2> scales;
-    int stage = 0, phase = 0, slot = 0, sphase = 1, seg = 0, ds = 0, tile = first, t0 = 0, n = 0;
-    for (int at = 0; at < total + kPairLag; ++at) {
-      if (at < total) {
-        wait(&bar_x_empty[d][slot], sphase, bar_full + stage, phase);
-        convert_x(ring + stage * stage_bytes + 16384 + d * part * 128, xring + (d * kPairX + slot) * slot_bytes, part, tid & 127);
-        __syncwarp();
-        if (lane == 0) {
-          arrive_first(&bar_x_full[d][slot]);
-          mbar_arrive_relaxed(bar_empty + stage);
-        }
-        if (++stage == stages) { stage = 0; phase ^= 1; }
-        if (++slot == kPairX) { slot = 0; sphase ^= 1; }
-      }
-      if (at < kPairLag) continue;
-      if (ds == 0) {
-        const int tn = tile % a.tiles_n;
-        t0 = tile / a.tiles_n * a.nt + d * half;
-        n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
-        scales.load(a.m, a.m.ws[GATED ? row >> 6 : 0], t0, n);
-      }
-      if (ends_segment(ds, nk, d)) {
+    int seg = 0;
+    for (int j = 0; j < my_tiles; ++j) {
+      const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + d * half;
+      const int n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
+      scales.load(a.m, a.m.ws[GATED ? row >> 6 : 0], t0, n);
+      for (int s = 0; s < nk; ++s) {
+        if (!ends_segment(s, nk, d)) continue;
         wait(bar_d_full + d, seg & 1);
         ++seg;
         tc_fence_after();
@@ -670,11 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_first(bar_d_empty + d);
       }
-      if (++ds == nk) {
-        output_sums<GATED>(a.m, sum, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
-        ds = 0;
-        tile += step_tiles;
-      }
+      output_sums<GATED>(a.m, sum, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
     }
   }
   __syncwarp();
@@ -707,9 +712,8 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms, const int (&clusters)[
       const long long tiles = (long long)p.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms / 2 - 1) / (sms / 2) * (nt + 16);
       if (best == 0 || cost < best) { best = cost; p.nt = nt; }
     }
-    const int stage = 16384 + p.nt * 64, rest = fixed + kPairX * p.nt * 128;
-    p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
-    p.smem = 1024 + rest + p.stages * stage;
+    p.stages = kPairStages;
+    p.smem = 1024 + fixed + kPairStages * (16384 + p.nt * 128);
   } else {
     p.nt = (a.T + 15) / 16 * 16;
     while (p.split < 8 && p.split * 2 <= nk && p.tiles_n <= clusters[p.split == 1 ? 1 : p.split == 2 ? 2 : 3]) p.split *= 2;
@@ -766,6 +770,10 @@ static bool prepare(Device& d) {
   return true;
 }
 
+size_t tc_workspace_bytes(int K, int T_max) {
+  return T_max > kSmallTokens ? (size_t)T_max * ((K + 63) / 64 * 128) : 0;
+}
+
 moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   const bool gated = a.w[1] != nullptr;
   int dev = 0;
@@ -775,15 +783,30 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   const TcPlan p = plan(a, gated, sms, g_device[dev].clusters);
   CUtensorMap mx, m0, m1;
   const int box_w = p.pair && gated ? 64 : 128;
-  if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.pair ? p.nt / 4 : p.nt) || !map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w))
+  const uint32_t pieces = (uint32_t)((a.K + 63) / 64 * 4);
+  uint8_t* wide = reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader);
+  if (!map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w)) return MOE_ERR_CUDA;
+  if (p.pair) {
+    const uint64_t dims[3] = {128, (uint64_t)a.T, pieces / 4}, strides[2] = {(uint64_t)pieces * 32, 128};
+    const uint32_t box[3] = {128, (uint32_t)p.nt / 4, 2};
+    if (!moe_internal::tmap_u8(&mx, wide, 3, dims, strides, box)) return MOE_ERR_CUDA;
+  } else if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.nt)) {
     return MOE_ERR_CUDA;
+  }
   m1 = m0;
   if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
   const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages};
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    const cudaLaunchConfig_t cfg = config(2 * min(p.tiles, sms / 2), kPairThreads, p.smem, 1, &at, stream);
+    const int64_t ctas = ((int64_t)a.T * pieces + 255) / 256;
+    widen_kernel<<<(int)min(ctas, (int64_t)sms * 8), 256, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = config(2 * min(p.tiles, sms / 2), kPairThreads, p.smem, 1, &at, stream);
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     e = gated ? cudaLaunchKernelEx(&cfg, pair_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, pair_kernel<false>, args, mx, m0, m1);
   } else {
     const cudaLaunchConfig_t cfg =
