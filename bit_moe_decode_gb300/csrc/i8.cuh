@@ -28,7 +28,8 @@ struct MatArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ float product(int acc, float xs, float ws) { return __fmul_rn(__fmul_rn((float)acc, xs), ws); }
+__device__ __forceinline__ float scaled(float sum, float xs, float ws) { return __fmul_rn(__fmul_rn(sum, xs), ws); }
+__device__ __forceinline__ float product(int acc, float xs, float ws) { return scaled((float)acc, xs, ws); }
 __device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v) {
   if (a.base) v = __fadd_rn(v, a.base[t * a.base_stride + n]);
   if (a.y) a.y[t * a.y_stride + n] = v;

@@ -40,6 +40,8 @@ struct TcArgs {
   int tiles_n, tiles;  // tiles of 256 channels (gated: 128), times the tiles of nt tokens
   int split;           // CTAs (a cluster) that share a tile of small_kernel
   int stages;
+  const uint32_t* squares;   // pair_kernel: the tokens' sums of squares, and
+  uint32_t most;             //   up to which a tile is one segment: |sum| <= sqrt(sum w^2 sum x^2) <= 128 sqrt(K sum x^2) <= 2^24
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -151,10 +153,10 @@ struct Waits {
   }
 };
 
-// Stage i of a tile's `stages` ends a segment of accumulator d: every kSegment stages, the second's half as many earlier, and
-// the last
-__device__ __forceinline__ bool ends_segment(int i, int stages, int d) {
-  return i == stages - 1 || (i + 1 + d * (kSegment / 2)) % kSegment == 0;
+// Stage i of a tile's `stages` ends a segment of accumulator d: the last, and unless fp32 is known to add the whole tile exactly
+// (`single`) every kSegment stages, the second's half as many earlier
+__device__ __forceinline__ bool ends_segment(int i, int stages, int d, bool single) {
+  return i == stages - 1 || (!single && (i + 1 + d * (kSegment / 2)) % kSegment == 0);
 }
 
 // 128 codes of a weight row (row: its place in the tile, for the swizzle) -> 64 TMEM columns of the thread's lane
@@ -205,9 +207,28 @@ __device__ __forceinline__ void convert_x(uint32_t from, uint32_t to, int rows, 
     }
 }
 
-// Adds accumulator columns 0 .. n - 1 of the thread's lane, exact integers, to its sums
+// A tile's first segment: accumulator columns 0 .. n - 1 (a multiple of 16) of the thread's lane, as they are (fp32)
 template <int COLS>
-__device__ __forceinline__ void take_sums(uint32_t taddr, int n, int (&sum)[COLS]) {
+__device__ __forceinline__ void first_sums(uint32_t taddr, int n, int (&sum)[COLS]) {
+#pragma unroll
+  for (int c = 0; c < COLS / 16; ++c)
+    if (c * 16 < n) tc_ld16(taddr + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&sum[16 * c]));
+  tc_wait_ld();
+  tc_fence_before();
+}
+// The first segment's sums as integers
+template <int COLS>
+__device__ __forceinline__ void integer_sums(int n, int (&sum)[COLS]) {
+#pragma unroll
+  for (int c = 0; c < COLS / 16; ++c)
+    if (c * 16 < n) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[16 * c + e] = __float2int_rn(__int_as_float(sum[16 * c + e]));
+    }
+}
+// A further segment: adds its accumulators, exact integers in fp32, to the sums
+template <int COLS>
+__device__ __forceinline__ void more_sums(uint32_t taddr, int n, int (&sum)[COLS]) {
   uint32_t r[2][8];
   tc_ld8(taddr, r[0]);
 #pragma unroll
@@ -220,18 +241,15 @@ __device__ __forceinline__ void take_sums(uint32_t taddr, int n, int (&sum)[COLS
     }
   tc_fence_before();
 }
-// Tokens 16 c .. of the sums, which start again at 0: a rolled loop over c keeps the code of the outputs small (unrolled it was
-// 130 KB, and a tile's end took 15 us longer, of instruction misses)
+// Tokens 16 c .. of the sums. (A rolled loop over c keeps the code of the outputs small: unrolled it was 130 KB, and a tile's end
+// took 15 us longer, of instruction misses.)
 template <int COLS>
-__device__ __forceinline__ void give_sums(int c, int (&sum)[COLS], int (&r)[16]) {
+__device__ __forceinline__ void give_sums(int c, const int (&sum)[COLS], int (&r)[16]) {
 #pragma unroll
   for (int k = 0; k < COLS / 16; ++k)
     if (c == k) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        r[e] = sum[16 * k + e];
-        sum[16 * k + e] = 0;
-      }
+      for (int e = 0; e < 16; ++e) r[e] = sum[16 * k + e];
     }
 }
 // The scales that a tile's outputs need, loaded long before: tokens t0 + lane, + 32, ... of the warp's lanes, and channel n's.
@@ -244,13 +262,13 @@ struct Scales {
     w = __ldg(ws + min(n, a.N - 1));
   }
 };
-// The outputs of `count` tokens from t0 on, channel n (none if n >= N). Gated: the thread has gate's (side 0) or up's sums, and
+// The outputs of `count` tokens from t0 on, channel n (none if n >= N), from sums that are still fp32 (single) or integers. Gated: the thread has gate's (side 0) or up's sums, and
 // the thread with the other of the same n is at the same idx (of `width`) on the other side; of 16 tokens side 0 finishes the first
 // eight, side 1 the last, and what the other needs goes through shared memory (two buffers in turn), ordered by barrier `bar` among
 // 2 width threads.
 template <bool GATED, int COLS>
-__device__ __forceinline__ void output_sums(const MatArgs& a, int (&sum)[COLS], const Scales<COLS>& sc, int t0, int count, int n, int side,
-                                            uint32_t xchg, int idx, int width, int bar) {
+__device__ __forceinline__ void output_sums(const MatArgs& a, const int (&sum)[COLS], bool single, const Scales<COLS>& sc, int t0, int count,
+                                            int n, int side, uint32_t xchg, int idx, int width, int bar) {
   int r[16];
 #pragma unroll 1
   for (int c = 0; c * 16 < count; ++c) {
@@ -262,7 +280,8 @@ __device__ __forceinline__ void output_sums(const MatArgs& a, int (&sum)[COLS], 
       if (c >> 1 == i) xs = sc.x[i];
     float v[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = product(r[e], __shfl_sync(0xFFFFFFFFu, xs, 16 * (c & 1) + e), sc.w);
+    for (int e = 0; e < 16; ++e)
+      v[e] = scaled(single ? __int_as_float(r[e]) : (float)r[e], __shfl_sync(0xFFFFFFFFu, xs, 16 * (c & 1) + e), sc.w);
     if (!GATED) {
       if (n < a.N) put_tokens<16>(a, t1, a.T - t1, n, v);
     } else {
@@ -317,6 +336,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     else tma_load_2d(to + 16384, &map_w0, k * kTileK, tn * 256 + 128, bar_full + stage);
     tma_load_2d(to + 32768, &map_x, k * kTileK, tt * nt, bar_full + stage);
   };
+  const bool single = per_tile <= kSegment;
   const int early = min(stages, per_tile);                 // stages copied before the roles begin (of the first tile)
   if (warp == 20 && lane == 0) {
     for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 12); }
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
           tc_fence_after();
           const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
           const uint64_t dxs = dx + xslot * (slot_bytes / 16);
-          const bool ends = ends_segment(s, per_tile, b);
+          const bool ends = ends_segment(s, per_tile, b, single);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_f16_ts(td, ta + 8 * k, dxs + (k >> 2) * (nt * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
@@ -431,24 +451,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     const int b = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
     int sum[kSmallTokens];
-#pragma unroll
-    for (int t = 0; t < kSmallTokens; ++t) sum[t] = 0;
     int seg = 0;
     Scales<kSmallTokens> scales;
     for (int j = 0; j < my_tiles; ++j) {
       const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
       const int n = GATED ? tn * 128 + row : tn * 256 + b * 128 + row;
       scales.load(a.m, a.m.ws[GATED ? b : 0], t0, n);
+      bool begun = false;
       for (int s = 0; s < per_tile; ++s) {
-        if (!ends_segment(s, per_tile, b)) continue;
+        if (!ends_segment(s, per_tile, b, single)) continue;
         wait(bar_d_full + b, seg & 1);
         ++seg;
         tc_fence_after();
-        take_sums(td, nt, sum);
+        if (begun) more_sums(td, nt, sum);
+        else first_sums(td, nt, sum);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_d_empty + b);
+        if (!begun && (!single || a.split > 1)) integer_sums(nt, sum);
+        begun = true;
       }
-      if (a.split == 1) output_sums<GATED>(a.m, sum, scales, t0, nt, n, b, xchg, row, 128, 1);
+      if (a.split == 1) output_sums<GATED>(a.m, sum, single, scales, t0, nt, n, b, xchg, row, 128, 1);
     }
     if (a.split > 1) {
       // every CTA of the cluster is through with its rings; token t is finished by CTA t / per
@@ -515,25 +537,44 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-// X for pair_kernel: rows of `pitch` binary16 values (K rounded up to 64), in convert4's order, zeros past K. 16 codes a thread.
-__global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, uint32_t pieces, uint8_t* out) {
+// X for pair_kernel: rows of binary16 values (`pieces` of 16: K rounded up to 64), in convert4's order, zeros past K; and each row's sum of
+// squares (below 2^31). One row a CTA at a time.
+__global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, int pieces, uint8_t* out,
+                                                    uint32_t* squares) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // (pair_kernel may set itself up meanwhile)
-  const uint32_t step = gridDim.x * 256u, first = blockIdx.x * 256u + threadIdx.x, step_rows = step / pieces, step_k = step % pieces;
-  uint32_t k = first % pieces;
-  for (int64_t row = first / pieces; row < rows; row += step_rows) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if ((int)(k * 16) < K) v = __ldg(reinterpret_cast<const uint4*>(x + row * stride + k * 16));
-    uint32_t h[8];
-    convert4(v.x, h[0], h[1]);
-    convert4(v.y, h[2], h[3]);
-    convert4(v.z, h[4], h[5]);
-    convert4(v.w, h[6], h[7]);
-    uint4* to = reinterpret_cast<uint4*>(out) + (row * pieces + k) * 2;
-    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    k += step_k;
-    if (k >= pieces) { k -= pieces; ++row; }
+  __shared__ uint32_t part[4];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    uint32_t sq = 0;
+    for (int k = threadIdx.x; k < pieces; k += 128) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (16 * k < K) v = __ldg(reinterpret_cast<const uint4*>(x + row * stride) + k);
+      sq = (uint32_t)__dp4a((int)v.x, (int)v.x, __dp4a((int)v.y, (int)v.y, __dp4a((int)v.z, (int)v.z, __dp4a((int)v.w, (int)v.w, (int)sq))));
+      uint32_t h[8];
+      convert4(v.x, h[0], h[1]);
+      convert4(v.y, h[2], h[3]);
+      convert4(v.z, h[4], h[5]);
+      convert4(v.w, h[6], h[7]);
+      uint4* to = reinterpret_cast<uint4*>(out) + (row * pieces + k) * 2;
+      to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    sq = __reduce_add_sync(0xFFFFFFFFu, sq);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sq;
+    __syncthreads();
+    if (threadIdx.x == 0) squares[row] = part[0] + part[1] + part[2] + part[3];
+    __syncthreads();
   }
+}
+
+// The largest of a tile's sums of squares that a lane has (of its tokens t0 + lane, + 32, ...).
+__device__ __forceinline__ uint32_t tile_squares(const TcArgs& a, int t0) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kPairTokens / 32; ++i) {
+    const int t = t0 + 32 * i + (int)(threadIdx.x & 31);
+    if (32 * i < a.nt && t < a.m.T) m = max(m, a.squares[t]);
+  }
+  return m;
 }
 
 template <bool GATED>
@@ -611,7 +652,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * 128;
       const uint64_t dx = umma_desc_sw128(ring + 16384 + d * part * 256);
       int stage = 0, phase = 0, seg = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      uint32_t squares = tile_squares(a, first / a.tiles_n * a.nt);
       for (int j = 0; j < my_tiles; ++j) {
+        const bool single = __reduce_max_sync(0xFFFFFFFFu, squares) <= a.most;
+        squares = tile_squares(a, (first + (j + 1) * step_tiles) / a.tiles_n * a.nt);     // the next tile's
         bool fresh = true;
         for (int s = 0; s < nk; ++s) {
           if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
@@ -619,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tc_fence_after();
           const uint32_t ta = tmem + 256 + stage * 64;
           const uint64_t dxs = dx + stage * (stage_bytes / 16);
-          const bool ends = ends_segment(s, nk, d);
+          const bool ends = ends_segment(s, nk, d, single);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_f16_ts_pair(td, ta + 8 * k, dxs + (k >> 2) * (part * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
@@ -662,24 +707,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int d = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * 128;
     int sum[kPairTokens / 2];
-#pragma unroll
-    for (int t = 0; t < kPairTokens / 2; ++t) sum[t] = 0;
     Scales<kPairTokens / 2> scales;
     int seg = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int j = 0; j < my_tiles; ++j) {
       const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + d * half;
       const int n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
       scales.load(a.m, a.m.ws[GATED ? row >> 6 : 0], t0, n);
+      const bool single = __reduce_max_sync(0xFFFFFFFFu, tile_squares(a, t0 - d * half)) <= a.most;
+      bool begun = false;
       for (int s = 0; s < nk; ++s) {
-        if (!ends_segment(s, nk, d)) continue;
+        if (!ends_segment(s, nk, d, single)) continue;
         wait(bar_d_full + d, seg & 1);
         ++seg;
         tc_fence_after();
-        take_sums(td, half, sum);
+        if (begun) more_sums(td, half, sum);
+        else first_sums(td, half, sum);
         __syncwarp();
         if (lane == 0) arrive_first(bar_d_empty + d);
+        if (!begun && !single) integer_sums(half, sum);
+        begun = true;
       }
-      output_sums<GATED>(a.m, sum, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
+      output_sums<GATED>(a.m, sum, single, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
     }
   }
   __syncwarp();
@@ -770,8 +819,10 @@ static bool prepare(Device& d) {
   return true;
 }
 
+// (the tokens' sums of squares, then their binary16 values)
+static size_t squares_bytes(int T) { return ((size_t)T * 4 + 255) & ~(size_t)255; }
 size_t tc_workspace_bytes(int K, int T_max) {
-  return T_max > kSmallTokens ? (size_t)T_max * ((K + 63) / 64 * 128) : 0;
+  return T_max > kSmallTokens ? squares_bytes(T_max) + (size_t)T_max * ((K + 63) / 64 * 128) : 0;
 }
 
 moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
@@ -783,11 +834,12 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   const TcPlan p = plan(a, gated, sms, g_device[dev].clusters);
   CUtensorMap mx, m0, m1;
   const int box_w = p.pair && gated ? 64 : 128;
-  const uint32_t pieces = (uint32_t)((a.K + 63) / 64 * 4);
-  uint8_t* wide = reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader);
+  const int pieces = (a.K + 63) / 64 * 4;
+  uint32_t* squares = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader));
+  uint8_t* wide = reinterpret_cast<uint8_t*>(squares) + squares_bytes(a.T);
   if (!map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w)) return MOE_ERR_CUDA;
   if (p.pair) {
-    const uint64_t dims[3] = {128, (uint64_t)a.T, pieces / 4}, strides[2] = {(uint64_t)pieces * 32, 128};
+    const uint64_t dims[3] = {128, (uint64_t)a.T, (uint64_t)pieces / 4}, strides[2] = {(uint64_t)pieces * 32, 128};
     const uint32_t box[3] = {128, (uint32_t)p.nt / 4, 2};
     if (!moe_internal::tmap_u8(&mx, wide, 3, dims, strides, box)) return MOE_ERR_CUDA;
   } else if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.nt)) {
@@ -795,12 +847,11 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   }
   m1 = m0;
   if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
-  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages};
+  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages, squares, (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    const int64_t ctas = ((int64_t)a.T * pieces + 255) / 256;
-    widen_kernel<<<(int)min(ctas, (int64_t)sms * 8), 256, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide);
+    widen_kernel<<<min(a.T, sms * 16), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = config(2 * min(p.tiles, sms / 2), kPairThreads, p.smem, 1, &at, stream);
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
