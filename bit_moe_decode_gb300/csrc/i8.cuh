@@ -17,6 +17,14 @@ inline moe_status_t check_rows(const moe_i8_rows_t* r) {
   return MOE_OK;
 }
 
+// Four codes (one word) -> binary16, exactly: a byte under the exponent of 1024, sign bit flipped, is 1024 + 128 + code. The order
+// is codes 0, 2, 1, 3 (a shift instead of two permutations); W and X have the same, so the sums are those of the same products.
+__device__ __forceinline__ void convert4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = lop3_and_xor(w, 0x00FF00FFu, 0x64806480u), b = lop3_and_xor(w >> 8, 0x00FF00FFu, 0x64806480u);
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0xE480E480u));     // - 1152
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0xE480E480u));
+}
+
 // A product's arguments: x [T, K], one or two weight matrices [N, K] (gated: gate and up), outputs [T, N].
 struct MatArgs {
   const int8_t *x, *w[2];

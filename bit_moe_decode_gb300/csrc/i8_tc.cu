@@ -93,14 +93,6 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b,
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Four codes (one word) -> binary16, exactly: a byte under the exponent of 1024, sign bit flipped, is 1024 + 128 + code. The order
-// is codes 0, 2, 1, 3 (a shift instead of two permutations); W and X have the same, so the sums are those of the same products.
-__device__ __forceinline__ void convert4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = lop3_and_xor(w, 0x00FF00FFu, 0x64806480u), b = lop3_and_xor(w >> 8, 0x00FF00FFu, 0x64806480u);
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0xE480E480u));     // - 1152
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0xE480E480u));
-}
-
 // Outputs of channel n for the `count` (up to E) tokens from t on. Loads and stores go in groups, so that their latencies overlap.
 template <int E>
 __device__ __forceinline__ void put_tokens(const MatArgs& a, int64_t t, int count, int n, float (&v)[E]) {
