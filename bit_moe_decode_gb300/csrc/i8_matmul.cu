@@ -1,181 +1,218 @@
 // i8_matmul.cu -- product of 8-bit integers with scales for each token and output channel, and the gated block: the entry points,
 // and the kernel for a few tokens (i8_tc.cu has the one for more).
 //
-// A few tokens: the weights are read once, and that is all the time there is. They go from global memory straight into registers, 16
-// channels a CTA at a time, whose 8 warps share K; codes become binary16 (exactly) and mma.sync (m16n8k16) multiplies them with
-// the tokens, which the CTA keeps in shared memory in binary16. fp32 adds 1024 products exactly; then the accumulators are
-// added to integers. The order of k within a block is the one in which a lane gets its codes: 16 contiguous bytes of two rows.
+// A few tokens: the weights are read once, and that is all the time there is. One CTA an SM goes through groups of 16 channels;
+// one copy (TMA) brings 1024 codes of each of the 16 rows a stage, as many stages ahead as shared memory holds. (16 copies of a
+// row each took 100 cycles apiece to issue, which held the stream at 3 TB/s.) 16 warps (two sets
+// that take stages in turn, 128 codes a warp) make the codes binary16 (exactly), and mma.sync (m16n8k16) multiplies them with the
+// tokens, which the CTA keeps in shared memory in binary16. fp32 adds 1024 products exactly; then the accumulators are added to
+// integers. Four more warps add the 16 warps' sums and write a group's outputs while the next group is under way.
+// The order of k within a block is the one in which a lane reads its codes: 16 contiguous bytes of two rows.
 // Gated: rows 0-7 of the 16 are gate's, 8-15 up's of the same channels, so that a thread has both.
 #include "i8.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace i8 {
 
-constexpr int kRowThreads = 256, kRowWarps = 8;
-constexpr int kAhead = 2;                     // blocks of 128 codes of 16 rows that a warp has in flight
-constexpr int kExactBlocks = 8;               // blocks whose products fp32 adds exactly
+constexpr int kRowTokens = 8;
+constexpr int kRowWarps = 16, kOutWarps = 4, kRowThreads = (kRowWarps + kOutWarps + 1) * 32;
+// A stage: 8 blocks of 128 codes of the 16 rows (gated: gate's 8 blocks of 8 rows, then up's), 128-byte rows, swizzled; then the
+// block that K ends in, if it is not a whole one.
+constexpr int kRowStageK = 1024, kRowStage = 9 * 2048;
+constexpr int kExactStages = 8;               // stages whose products of a warp fp32 adds exactly
+constexpr int kMaxRowStages = 12;
+constexpr int kRowSmem = 225 * 1024 - 2 * kRowWarps * 128 * 4;
 
-__device__ __forceinline__ uint4 load_codes(const int8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
+template <bool GATED>
+__global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int groups, int stages, const __grid_constant__ CUtensorMap map0,
+                                                                  const __grid_constant__ CUtensorMap map1,
+                                                                  const __grid_constant__ CUtensorMap tail0,
+                                                                  const __grid_constant__ CUtensorMap tail1) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  __shared__ uint64_t bar_full[kMaxRowStages], bar_empty[kMaxRowStages], bar_sum_full[2], bar_sum_empty[2];
+  __shared__ int part[2][kRowWarps][128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int channels = GATED ? 8 : 16, blocks = (a.K + 127) / 128, pitch = blocks * 256 + 16;
+  const int per_group = (a.K + kRowStageK - 1) / kRowStageK, mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  uint8_t* xs = smem + stages * kRowStage;
 
-// NT tiles of 8 tokens. x in shared memory: T rows of `pitch` bytes (2 K rounded up to 256, and 16).
-template <bool GATED, int NT>
-__global__ void __launch_bounds__(kRowThreads, NT == 1 ? 3 : 2) rows_kernel(MatArgs a, int groups) {
-  extern __shared__ uint8_t smem[];
-  __shared__ int part[kRowWarps][16 * 8 * NT];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int blocks = (a.K + 127) / 128, pitch = blocks * 256 + 16;
-  const int mine = (blocks - warp + kRowWarps - 1) / kRowWarps;           // blocks of a group that this warp has (may be <= 0)
-  const int channels = GATED ? 8 : 16;
-
-  // ---- the next block of the warp's list (group after group): four pieces of 16 codes
-  uint4 buf[kAhead][4];
-  int lg = blockIdx.x, lb = 0;
-  auto fetch = [&](uint4 (&v)[4]) {
-    if (lg < groups && mine > 0) {
-      const int n0 = lg * channels + g, k = (warp + lb * kRowWarps) * 128 + 16 * c;
-      const int r0 = min(n0, a.N - 1), r1 = min(GATED ? n0 : n0 + 8, a.N - 1);
-      const int8_t *p0 = a.w[0] + r0 * a.w_stride[0] + k, *p1 = a.w[GATED ? 1 : 0] + r1 * a.w_stride[GATED ? 1 : 0] + k;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = k + 64 * h < a.K;
-        v[2 * h] = in ? load_codes(p0 + 64 * h) : make_uint4(0, 0, 0, 0);
-        v[2 * h + 1] = in ? load_codes(p1 + 64 * h) : make_uint4(0, 0, 0, 0);
-      }
-      if (++lb == mine) { lb = 0; lg += gridDim.x; }
+  bool dead = false;
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (mbar_try_wait(bar, parity) || dead) return;
+    if (!mbar_wait(bar, parity, kDefaultWaitNs)) {
+      record_error(a.status, MOE_ERR_DEVICE_TIMEOUT);
+      dead = true;
     }
   };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(buf[i]);
-
-  // ---- the tokens, in convert4's order
-  const int pieces = blocks * 8;
-  for (int i = tid; i < a.T * pieces; i += kRowThreads) {
-    const int t = i / pieces, k = (i - t * pieces) * 16;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (k < a.K) v = *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + k);
-    uint32_t h[8];
-    convert4(v.x, h[0], h[1]);
-    convert4(v.y, h[2], h[3]);
-    convert4(v.z, h[4], h[5]);
-    convert4(v.w, h[6], h[7]);
-    uint4* to = reinterpret_cast<uint4*>(smem + t * pitch + k * 2);
-    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  // part s of the CTA's gi-th group into a slot
+  const int whole = a.K / 128;
+  auto copy = [&](int gi, int s, int slot) {
+    const int n0 = ((int)blockIdx.x + gi * (int)gridDim.x) * channels;
+    const bool main = 8 * s < whole, tail = s == per_group - 1 && whole < blocks;
+    uint8_t* to = smem + slot * kRowStage;
+    mbar_arrive_expect_tx(bar_full + slot, (main ? 16384 : 0) + (tail ? 2048 : 0));
+    if (main) {
+      tma_load_3d(to, &map0, 0, n0, 8 * s, bar_full + slot);
+      if (GATED) tma_load_3d(to + 8192, &map1, 0, n0, 8 * s, bar_full + slot);
+    }
+    if (tail) {
+      tma_load_2d(to + 16384, &tail0, whole * 128, n0, bar_full + slot);
+      if (GATED) tma_load_2d(to + 17408, &tail1, whole * 128, n0, bar_full + slot);
+    }
+  };
+  const int total = mine * per_group, early = min(stages, total);
+  if (warp == kRowWarps + kOutWarps) {
+    if (lane == 0) {
+      for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 8); }
+      for (int i = 0; i < 2; ++i) { mbar_init(bar_sum_full + i, kRowWarps); mbar_init(bar_sum_empty + i, kOutWarps); }
+      fence_mbar_init();
+    }
+    __syncwarp();
+    if (lane == 0)
+      for (int i = 0; i < early; ++i) copy(i / per_group, i % per_group, i);
+  } else {
+    // ---- the tokens, in convert4's order, zeros past K
+    const int pieces = blocks * 8;
+    for (int i = tid; i < a.T * pieces; i += (kRowWarps + kOutWarps) * 32) {
+      const int t = i / pieces, k = (i - t * pieces) * 16;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (k < a.K) v = *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + k);
+      uint32_t h[8];
+      convert4(v.x, h[0], h[1]);
+      convert4(v.y, h[2], h[3]);
+      convert4(v.z, h[4], h[5]);
+      convert4(v.w, h[6], h[7]);
+      uint4* to = reinterpret_cast<uint4*>(xs + t * pitch + k * 2);
+      to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
   }
   __syncthreads();
-  const uint8_t* xr[NT];                     // (columns past the last token repeat it and are not used)
-#pragma unroll
-  for (int t = 0; t < NT; ++t) xr[t] = smem + min(8 * t + g, a.T - 1) * pitch + c * 32;
 
-  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
-    float acc[NT][4] = {};
-    int sum[NT][4] = {};
-    auto add = [&]() {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
+  if (warp == kRowWarps + kOutWarps) {
+    // ================================================================ copies
+    if (lane == 0) {
+      int slot = early % stages, phase = early == stages ? 0 : 1;
+      for (int i = early; i < total; ++i) {
+        wait(bar_empty + slot, phase);
+        copy(i / per_group, i % per_group, slot);
+        if (++slot == stages) { slot = 0; phase ^= 1; }
+      }
+      dead = false;                            // (where waits have run out, copies may still be in flight)
+      for (int i = max(0, total - stages); i < total; ++i) wait(bar_full + i % stages, (i / stages) & 1);
+    }
+  } else if (warp < kRowWarps) {
+    // ================================================================ products: stages i = set, set + 2, ..., 128 codes a warp
+    const int g = lane >> 2, c = lane & 3, set = warp >> 3, block = warp & 7;
+    const uint8_t* xr = xs + min(g, a.T - 1) * pitch + c * 32;      // (columns past the last token repeat it and are not used)
+    const uint8_t* wr = smem + g * 128;
+    int i = set, slot = set % stages, phase = (set / stages) & 1;
+    for (int gi = 0; gi < mine; ++gi) {
+      float acc[2][4] = {};
+      int sum[4] = {}, n = 0;
+      auto add = [&]() {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sum[t][e] += __float2int_rn(acc[t][e]);
-          acc[t][e] = 0.f;
+          sum[e] += __float2int_rn(acc[0][e]) + __float2int_rn(acc[1][e]);
+          acc[0][e] = acc[1][e] = 0.f;
         }
-    };
-    for (int i = 0; i < mine; i += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i + j < mine) {
-          const int at = (warp + (i + j) * kRowWarps) * 256;
+      };
+      for (; i < (gi + 1) * per_group; i += 2) {
+        const int at = (i - gi * per_group) * 8 + block;            // the warp's block of 128
+        wait(bar_full + slot, phase);
+        if (at < blocks) {
+          const uint8_t *ws = wr + slot * kRowStage + (at < whole ? block * (GATED ? 1024 : 2048) : 16384);
+          const int other = GATED && at < whole ? 8192 : 1024;       // the second eight rows
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const uint8_t *w = ws + (((4 * h + c) ^ g) << 4), *x = xr + at * 256 + 128 * h;
+            const uint4 v0 = *reinterpret_cast<const uint4*>(w), v1 = *reinterpret_cast<const uint4*>(w + other);
+            const uint4 b0 = *reinterpret_cast<const uint4*>(x), b1 = *reinterpret_cast<const uint4*>(x + 16);
             uint32_t w0[8], w1[8];
-            const uint4 v0 = buf[j][2 * h], v1 = buf[j][2 * h + 1];
             convert4(v0.x, w0[0], w0[1]);
-            convert4(v0.y, w0[2], w0[3]);
-            convert4(v0.z, w0[4], w0[5]);
-            convert4(v0.w, w0[6], w0[7]);
             convert4(v1.x, w1[0], w1[1]);
+            convert4(v0.y, w0[2], w0[3]);
             convert4(v1.y, w1[2], w1[3]);
+            convert4(v0.z, w0[4], w0[5]);
             convert4(v1.z, w1[4], w1[5]);
+            convert4(v0.w, w0[6], w0[7]);
             convert4(v1.w, w1[6], w1[7]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 b0 = *reinterpret_cast<const uint4*>(xr[t] + at + 128 * h), b1 = *reinterpret_cast<const uint4*>(xr[t] + at + 128 * h + 16);
-              mma_f16(acc[t], w0[0], w1[0], w0[1], w1[1], b0.x, b0.y, acc[t]);
-              mma_f16(acc[t], w0[2], w1[2], w0[3], w1[3], b0.z, b0.w, acc[t]);
-              mma_f16(acc[t], w0[4], w1[4], w0[5], w1[5], b1.x, b1.y, acc[t]);
-              mma_f16(acc[t], w0[6], w1[6], w0[7], w1[7], b1.z, b1.w, acc[t]);
-            }
+            mma_f16(acc[h], w0[0], w1[0], w0[1], w1[1], b0.x, b0.y, acc[h]);
+            mma_f16(acc[h], w0[2], w1[2], w0[3], w1[3], b0.z, b0.w, acc[h]);
+            mma_f16(acc[h], w0[4], w1[4], w0[5], w1[5], b1.x, b1.y, acc[h]);
+            mma_f16(acc[h], w0[6], w1[6], w0[7], w1[7], b1.z, b1.w, acc[h]);
           }
-          fetch(buf[j]);
-          if ((i + j) % kExactBlocks == kExactBlocks - 1) add();
         }
-    }
-    // (the ring's first place has the next group's first block only if this one's count is a multiple of the ring's)
-    if (mine > 0 && mine % kAhead != 0) {
-#pragma unroll
-      for (int j = 0; j < kAhead - 1; ++j) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 v = buf[0][e];
-          buf[0][e] = buf[1][e];
-          buf[1][e] = v;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(bar_empty + slot);
+        if (++n % kExactStages == 0) add();
+        slot += 2;
+        if (slot >= stages) { slot -= stages; phase ^= 1; }
       }
+      add();
+      const int buf = gi & 1;
+      wait(bar_sum_empty + buf, ((gi >> 1) & 1) ^ 1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[buf][warp][(2 * c + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sum_full + buf);
     }
-    add();
+  } else {
+    // ================================================================ sums of the warps, outputs: channel r, token t
+    const int id = tid - kRowWarps * 32, r = id & 15, t = id >> 4, up = GATED ? r >> 3 : 0;
+    const float scale = a.xs[min(t, a.T - 1)];
+    for (int gi = 0; gi < mine; ++gi) {
+      const int n = ((int)blockIdx.x + gi * (int)gridDim.x) * channels + (GATED ? r & 7 : r), buf = gi & 1;
+      const float ws = a.ws[up][min(n, a.N - 1)];
+      wait(bar_sum_full + buf, (gi >> 1) & 1);
+      int s = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[warp][(8 * t + 2 * c + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[t][e];
-    __syncthreads();
-    for (int i = tid; i < channels * a.T; i += kRowThreads) {
-      const int t = i / channels, r = i % channels, n = group * channels + r;
-      int s0 = 0, s1 = 0;
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
-        s0 += part[w][t * 16 + r];
-        if (GATED) s1 += part[w][t * 16 + 8 + r];
-      }
-      if (n < a.N) {
-        const float xs = a.xs[t], p = product(s0, xs, a.ws[0][n]);
-        put(a, t, n, GATED ? silu_mul(p, product(s1, xs, a.ws[GATED ? 1 : 0][n])) : p);
-      }
+      for (int w = 0; w < kRowWarps; ++w) s += part[buf][w][id];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sum_empty + buf);
+      float v = product(s, scale, ws);
+      if (GATED) v = silu_mul(v, __shfl_down_sync(0xFFFFFFFFu, v, 8));
+      if (t < a.T && n < a.N && !(GATED && r >= 8)) put(a, t, n, v);
     }
-    __syncthreads();
   }
 }
 
-// MOE_OK, or MOE_ERR_SHAPE: the tokens do not fit.
-static bool rows_fit(int T, int K) { return T <= 16 && (int64_t)T * ((K + 127) / 128 * 256 + 16) <= (T <= 8 ? 72 : 100) * 1024; }
-template <bool GATED, int NT>
-static moe_status_t launch_rows(const MatArgs& a, int sms, cudaStream_t stream) {
-  const int groups = (a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16);
-  const int smem = a.T * ((a.K + 127) / 128 * 256 + 16), fit = min(NT == 1 ? 3 : 2, 220 * 1024 / (smem + 8192 * NT));
-  rows_kernel<GATED, NT><<<min(groups, sms * fit), kRowThreads, smem, stream>>>(a, groups);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+// Stages that fit beside the tokens; below 5 the tensor cores' kernel is faster.
+static int rows_stages(int T, int K) {
+  if (T > kRowTokens) return 0;
+  const int left = kRowSmem - 1024 - T * ((K + 127) / 128 * 256 + 16), n = left < 0 ? 0 : left / kRowStage;
+  return n < 5 ? 0 : n < kMaxRowStages ? n : kMaxRowStages;
 }
-static moe_status_t rows_multiply(const MatArgs& a, cudaStream_t stream) {
+static moe_status_t rows_multiply(const MatArgs& a, int stages, cudaStream_t stream) {
   static int configured[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!configured[dev]) {
-    const int most = 104 * 1024;
-    if (cudaFuncSetAttribute(rows_kernel<false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-        cudaFuncSetAttribute(rows_kernel<true, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-        cudaFuncSetAttribute(rows_kernel<false, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-        cudaFuncSetAttribute(rows_kernel<true, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+    if (cudaFuncSetAttribute(rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem) != cudaSuccess) {
       cudaGetLastError();
       return MOE_ERR_CUDA;
     }
     configured[dev] = 1;
   }
-  const int sms = moe_internal::num_sms();
+  const int sms = moe_internal::num_sms(), channels = a.w[1] ? 8 : 16, groups = (a.N + channels - 1) / channels;
   if (sms <= 0) return MOE_ERR_CUDA;
-  if (a.w[1]) return a.T <= 8 ? launch_rows<true, 1>(a, sms, stream) : launch_rows<true, 2>(a, sms, stream);
-  return a.T <= 8 ? launch_rows<false, 1>(a, sms, stream) : launch_rows<false, 2>(a, sms, stream);
+  const int smem = 1024 + stages * kRowStage + a.T * ((a.K + 127) / 128 * 256 + 16), whole = a.K / 128;
+  CUtensorMap map[2], tail[2];
+  for (int i = 0; i < 2; ++i) {
+    const int m = a.w[1] ? i : 0;
+    const uint64_t dims[3] = {128, (uint64_t)a.N, (uint64_t)whole}, strides[2] = {(uint64_t)a.w_stride[m], 128};
+    const uint32_t box[3] = {128, (uint32_t)channels, 8};
+    const uint64_t tdims[2] = {(uint64_t)a.K, (uint64_t)a.N};
+    if (!moe_internal::tmap_u8(&tail[i], a.w[m], 2, tdims, strides, box)) return MOE_ERR_CUDA;
+    map[i] = tail[i];
+    if (whole > 0 && !moe_internal::tmap_u8(&map[i], a.w[m], 3, dims, strides, box)) return MOE_ERR_CUDA;
+  }
+  if (a.w[1]) rows_kernel<true><<<min(groups, sms), kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
+  else rows_kernel<false><<<min(groups, sms), kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 static bool out_ok(const void* p, int64_t stride, int64_t cols, int size) {
@@ -198,7 +235,8 @@ static moe_status_t multiply(const moe_i8_rows_t* x, const moe_i8_rows_t* w, con
   if (st != MOE_OK) return st;
   MatArgs a{x->q, {w->q, w2 ? w2->q : nullptr}, x->scale, {w->scale, w2 ? w2->scale : nullptr}, base, y, (uint16_t*)y_bf16,
             x->stride, {w->stride, w2 ? w2->stride : 0}, base_stride, y_stride, yb_stride, x->rows, w->rows, x->cols, (int32_t*)ws};
-  return rows_fit(a.T, a.K) ? rows_multiply(a, (cudaStream_t)stream) : tc_multiply(a, (cudaStream_t)stream);
+  const int stages = rows_stages(a.T, a.K);
+  return stages ? rows_multiply(a, stages, (cudaStream_t)stream) : tc_multiply(a, (cudaStream_t)stream);
 }
 
 }  // namespace i8
