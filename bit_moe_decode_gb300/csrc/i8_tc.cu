@@ -330,18 +330,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   };
   const bool single = per_tile <= kSegment;
   const int early = min(stages, per_tile);                 // stages copied before the roles begin (of the first tile)
-  if (warp == 20 && lane == 0) {
-    for (int i = 0; i < stages; ++i) { mbar_init(bar_full + i, 1); mbar_init(bar_empty + i, 12); }
+  if (warp == 20) {
+    if (lane < 3) prefetch_map(lane == 0 ? &map_w0 : lane == 1 ? &map_x : &map_w1);
+    if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 12); }
     fence_mbar_init();
-    for (int i = 0; i < early; ++i) copy(i, first, k_begin + i);
+    __syncwarp();
+    if (lane == 0)
+      for (int i = 0; i < early; ++i) copy(i, first, k_begin + i);
   }
-  if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
-      for (int i = 0; i < kSmallA; ++i) { mbar_init(&bar_a_full[b][i], 4); mbar_init(&bar_a_empty[b][i], 1); }
-      mbar_init(bar_d_full + b, 1);
-      mbar_init(bar_d_empty + b, 4);
-    }
-    for (int i = 0; i < kSlots; ++i) { mbar_init(bar_x_full + i, 4); mbar_init(bar_x_empty + i, 2); }
+  if (warp == 0) {
+    if (lane < 2 * kSmallA) { mbar_init(&bar_a_full[0][0] + lane, 4); mbar_init(&bar_a_empty[0][0] + lane, 1); }
+    if (lane < 2) { mbar_init(bar_d_full + lane, 1); mbar_init(bar_d_empty + lane, 4); }
+    if (lane < kSlots) { mbar_init(bar_x_full + lane, 4); mbar_init(bar_x_empty + lane, 2); }
     fence_mbar_init();
   }
   if (warp == 21) tc_alloc(&s_tmem, 512);
@@ -590,13 +590,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
 
-  if (tid == 0) {
-    for (int i = 0; i < kPairStages; ++i) {
-      mbar_init(bar_full + i, 1);
-      mbar_init(bar_ready + i, 5 - rank);
-      mbar_init(bar_empty + i, 2);
-    }
-    for (int d = 0; d < 2; ++d) { mbar_init(bar_d_full + d, 1); mbar_init(bar_d_empty + d, 8); }
+  if (warp == 0) {
+    if (lane < 3) prefetch_map(lane == 0 ? &map_w0 : lane == 1 ? &map_x : &map_w1);
+    if (lane < kPairStages) { mbar_init(bar_full + lane, 1); mbar_init(bar_ready + lane, 5 - rank); mbar_init(bar_empty + lane, 2); }
+    if (lane < 2) { mbar_init(bar_d_full + lane, 1); mbar_init(bar_d_empty + lane, 8); }
     fence_mbar_init();
   }
   if (warp == 13) {
