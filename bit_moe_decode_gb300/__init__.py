@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -110,7 +111,7 @@ def lib() -> C.CDLL:
             "moe_logits_probs": (C.c_int, [C.POINTER(moe_logits_t), P, P, P]),
             "moe_i8_quantize": (C.c_int, [C.c_int, P, i64, RP, P]),
             "moe_i8_values": (C.c_int, [RP, P, P]),
-            "moe_rms_norm_i8": (C.c_int, [C.POINTER(moe_norm_t), RP, P]),
+            "moe_rms_norm_i8": (C.c_int, [P, RP, P]),
             "moe_i8_workspace_bytes": (sz, [RP, i32]),
             "moe_i8_matmul": (C.c_int, [RP, RP, P, i64, P, i64, P, i64, P, sz, P]),
             "moe_i8_gated": (C.c_int, [RP, RP, RP, P, i64, P, i64, P, sz, P]),
@@ -319,17 +320,21 @@ def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, 
 
 
 # ------------------------------------------------------------------------------------------------ the dense half in 8 bits
+_F32 = torch.float32
+_NORM = struct.Struct("@iiiiPqPqPf4xPqP")          # moe_norm_t (packed: a ctypes structure takes a microsecond more to fill)
+
+
 def _typed_rows(t, shape):
     """Pointer, type and row stride (elements) of an fp32 or bf16 [n, m] tensor whose rows may be slices of wider ones."""
-    f32 = t.dtype == torch.float32
-    assert t.is_cuda and (f32 or t.dtype in _BF16_SIZED) and t.shape == shape and t.stride(1) == 1, \
+    dtype = t.dtype
+    assert t.is_cuda and (dtype is _F32 or dtype in _BF16_SIZED) and t.shape == shape and t.stride(1) == 1, \
         "expected fp32 or bf16 rows %s, got %s %s" % (shape, t.dtype, tuple(t.shape))
-    return t.data_ptr(), MOE_TYPE_F32 if f32 else MOE_TYPE_BF16, _row_stride(t)
+    return t.data_ptr(), MOE_TYPE_F32 if dtype is _F32 else MOE_TYPE_BF16, _row_stride(t, shape)
 
 
-def _row_stride(t) -> int:
+def _row_stride(t, shape) -> int:
     # (the stride of a single row means nothing: any that is wide and aligned enough will do)
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
 def _out_rows(t, dtypes, shape):
@@ -343,7 +348,7 @@ def _out_rows(t, dtypes, shape):
 
 def moe_i8_quantize(src, dst: "I8Rows", stream=None):
     """Rows of src [rows, cols] (fp32 or bf16) to 8 bits with a scale each."""
-    p, type_, stride = _typed_rows(src, (dst.rows, dst.cols))
+    p, type_, stride = _typed_rows(src, dst.shape)
     st = lib().moe_i8_quantize(type_, p, stride, dst.ref, _raw_stream(stream, src))
     if st:
         raise MoeError(st, "moe_i8_quantize")
@@ -351,7 +356,7 @@ def moe_i8_quantize(src, dst: "I8Rows", stream=None):
 
 def moe_i8_values(src: "I8Rows", out, stream=None):
     """The values that rows stand for, fp32 [rows, cols]."""
-    st = lib().moe_i8_values(src.ref, _dense(out, torch.float32, (src.rows, src.cols)), _raw_stream(stream, out))
+    st = lib().moe_i8_values(src.ref, _dense(out, _F32, src.shape), _raw_stream(stream, out))
     if st:
         raise MoeError(st, "moe_i8_values")
 
@@ -359,14 +364,15 @@ def moe_i8_values(src: "I8Rows", out, stream=None):
 def moe_rms_norm_i8(h, xq: "I8Rows" = None, r=None, gain=None, eps: float = 1e-6, h_out=None, x_bf16=None, stream=None):
     """s = h + r (to h_out), RMS norm of s with a gain: bf16 to x_bf16 and 8 bits to xq (at least one of them). h, r and h_out
     [tokens, hidden] fp32 or bf16 (h_out has h's type), rows with any stride; gain [hidden] fp32."""
-    T, H = h.shape
-    hp, ht, hs = _typed_rows(h, (T, H))
-    rp, rt, rs = _typed_rows(r, (T, H)) if r is not None else (None, 0, 0)
-    op, ot, os_ = _typed_rows(h_out, (T, H)) if h_out is not None else (None, ht, 0)
+    shape = h.shape
+    T, H = shape
+    hp, ht, hs = _typed_rows(h, shape)
+    rp, rt, rs = _typed_rows(r, shape) if r is not None else (0, 0, 0)
+    op, ot, os_ = _typed_rows(h_out, shape) if h_out is not None else (0, ht, 0)
     assert ot == ht, "h_out has h's type"
-    c = moe_norm_t(T, H, ht, rt, hp, hs, rp, rs, _dense(gain, torch.float32, (H,)), eps, op, os_,
-                   None if x_bf16 is None else _dense_bf16(x_bf16, (T, H)))
-    st = lib().moe_rms_norm_i8(C.byref(c), xq.ref if xq is not None else None, _raw_stream(stream, h))
+    args = _NORM.pack(T, H, ht, rt, hp, hs, rp, rs, _dense(gain, _F32, (H,)) or 0, eps, op, os_,
+                      0 if x_bf16 is None else _dense_bf16(x_bf16, shape))
+    st = lib().moe_rms_norm_i8(args, xq.ref if xq is not None else None, _raw_stream(stream, h))
     if st:
         raise MoeError(st, "moe_rms_norm_i8")
 
@@ -577,9 +583,9 @@ class I8Rows:
             q = torch.empty((rows, cols), dtype=torch.int8, device=device)
             scale = torch.empty(rows, dtype=torch.float32, device=device)
         assert q.is_cuda and q.dtype == torch.int8 and q.dim() == 2 and q.stride(1) == 1, "q: int8 rows [rows, cols]"
-        self.rows, self.cols = q.shape
+        self.rows, self.cols = self.shape = tuple(q.shape)
         self.q, self.scale = q, scale
-        self.c = moe_i8_rows_t(self.rows, self.cols, _row_stride(q), q.data_ptr(), _dense(scale, torch.float32, (self.rows,)))
+        self.c = moe_i8_rows_t(self.rows, self.cols, _row_stride(q, self.shape), q.data_ptr(), _dense(scale, _F32, (self.rows,)))
         self.ref = C.byref(self.c)
 
     @classmethod
