@@ -22,6 +22,7 @@ constexpr int kRowWarps = 16, kOutWarps = 4, kRowThreads = (kRowWarps + kOutWarp
 constexpr int kRowStageK = 1024, kRowStage = 9 * 2048;
 constexpr int kExactStages = 8;               // stages whose products of a warp fp32 adds exactly
 constexpr int kMaxRowStages = 12;
+static_assert(kMaxRowStages % 2 == 0, "slots belong to sets");
 constexpr int kRowSmem = 225 * 1024 - 2 * kRowWarps * 128 * 4;
 
 template <bool GATED>
@@ -188,11 +189,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
   }
 }
 
-// Stages that fit beside the tokens; below 5 the tensor cores' kernel is faster.
+// Stages that fit beside the tokens; below 4 the tensor cores' kernel is faster. An even number, so that a slot always belongs to the
+// same set of warps: a set that waited for a slot's next use before the other set's copy into it had landed would take that wait
+// for done (a barrier's parity tells only neighbouring phases apart).
 static int rows_stages(int T, int K) {
   if (T > kRowTokens) return 0;
   const int left = kRowSmem - 1024 - T * ((K + 127) / 128 * 256 + 16), n = left < 0 ? 0 : left / kRowStage;
-  return n < 5 ? 0 : n < kMaxRowStages ? n : kMaxRowStages;
+  return n < 4 ? 0 : n < kMaxRowStages ? n & ~1 : kMaxRowStages;
 }
 static moe_status_t rows_multiply(const MatArgs& a, int stages, cudaStream_t stream) {
   static int configured[64] = {0};

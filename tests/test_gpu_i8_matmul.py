@@ -211,6 +211,32 @@ def test_in_a_graph_and_on_two_streams(m, T):
     assert m.moe_get_device_status(wsp) == 0
 
 
+@pytest.mark.parametrize("T,N,K,gated", [(1, 6144, 4096, False), (8, 16384, 4096, False), (8, 4096, 2048, True), (5, 4096, 6144, False),
+                                          (30, 8192, 4096, False), (200, 4096, 4096, True)])
+def test_many_launches_one_after_another(m, T, N, K, gated):
+    """Weights from memory each time (three sets, more than the cache holds together with what lies between), always the same bits."""
+    x = device_rows(m, *codes(T, K, 1, "normal"))
+    sets = [[device_rows(m, *codes(N, K, 10 * i + j, "normal")) for j in range(2 if gated else 1)] for i in range(3)]
+    flush = torch.empty(1 << 27, dtype=torch.uint8, device=DEV)
+    wsp = sets[0][0].workspace(T)
+
+    def run(w, y):
+        if gated:
+            m.moe_i8_gated(x, *w, y=y, ws=wsp)
+        else:
+            m.moe_i8_matmul(x, w[0], y=y, ws=wsp)
+    first = [torch.empty(T, N, device=DEV) for _ in sets]
+    for w, y in zip(sets, first):
+        run(w, y)
+    for i in range(60):
+        if i % 5 == 0:
+            flush.fill_(i)
+        y = torch.empty(T, N, device=DEV)
+        run(sets[i % 3], y)
+        assert torch.equal(y, first[i % 3]), i
+    assert m.moe_get_device_status(wsp) == 0
+
+
 def test_products_refuse(m):
     x, w = m.I8Rows(4, 64), m.I8Rows(8, 64)
     ws = w.workspace(4)
