@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
           __syncwarp();
           fresh = ends;
           seg += ends;
+          if (j == my_tiles - 1 && s == per_tile - 1)       // no arrival of a commit is in flight when the CTA ends
+            wait(&bar_a_empty[b][slot], phase, bar_x_empty + xslot, xphase);
           if (++slot == kSmallA) { slot = 0; phase ^= 1; }
           if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
         }
@@ -631,9 +633,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (++stage == kPairStages) { stage = 0; phase ^= 1; }
           }
         }
-        // (where waits have run out, copies may still be in flight)
+        // no copy (where waits have run out) and no arrival of a commit is in flight when the CTA ends
         wait.dead = false;
-        for (int t = max(0, total - kPairStages); t < total; ++t) wait(bar_full + t % kPairStages, (t / kPairStages) & 1);
+        for (int t = max(0, total - kPairStages); t < total; ++t)
+          wait(bar_full + t % kPairStages, (t / kPairStages) & 1, bar_empty + t % kPairStages, (t / kPairStages) & 1);
       }
     } else if (warp <= 14 && rank == 0) {
       // ================================================================ products of half d (both CTAs')
