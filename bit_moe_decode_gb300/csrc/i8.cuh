@@ -25,9 +25,6 @@ __device__ __forceinline__ void convert4(uint32_t w, uint32_t& lo, uint32_t& hi)
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0xE480E480u));
 }
 
-// Has a tensor map fetched, before the copies that need it
-__device__ __forceinline__ void prefetch_map(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
-
 // A product's arguments: x [T, K], one or two weight matrices [N, K] (gated: gate and up), outputs [T, N].
 struct MatArgs {
   const int8_t *x, *w[2];

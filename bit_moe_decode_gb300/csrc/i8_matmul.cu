@@ -66,7 +66,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
   };
   const int total = mine * per_group, early = min(stages, total);
   if (warp == kRowWarps + kOutWarps) {
-    if (lane < (GATED ? 4 : 2)) prefetch_map(lane == 0 ? &map0 : lane == 1 ? &tail0 : lane == 2 ? &map1 : &tail1);
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 8); }
     else if (lane >= 30) { mbar_init(bar_sum_full + lane - 30, kRowWarps); mbar_init(bar_sum_empty + lane - 30, kOutWarps); }
     fence_mbar_init();

@@ -14,9 +14,12 @@
 // apart, each with a thread of its own that issues its products, so that one's products run while the other is read; the
 // outputs of a tile are written while the next one's products run.
 //
-// small_kernel: a CTA has 256 channels (two blocks of 128; gated: 128 of gate and the same 128 of up) and up to 64 tokens. Where
-// that makes few tiles, a cluster of CTAs shares one, each with a part of K; the integer parts are exchanged through
-// distributed shared memory, each CTA finishing some of the tokens.
+// small_kernel: a tile is 256 channels (two blocks of 128; gated: 128 of gate and the same 128 of up) and up to 64 tokens. The tiles'
+// stages are laid end to end and dealt out evenly over one CTA per SM; the sums of tiles that CTAs share go to the workspace, as
+// integers, and a second launch adds them up and writes the outputs. (A cluster a tile, its parts exchanged through
+// distributed shared memory, took 29 us for gated 48 x 4096 x 11008: 86 tiles leave 66 SMs idle, and the exchange runs at 20
+// bytes a cycle; adding to the workspace with atomics runs at 9; and the last of a tile's CTAs adding up all parts took 50 us
+// for gated 64 x 4096 x 4096, where all SMs together take @@.)
 // pair_kernel: two CTAs (cta_group::2) have 256 channels (128 each; gated: 64 of gate and 64 of up each) and up to 256 tokens (two
 // halves); each converts its own channels and half of the tokens, which halves the conversions and the reads of X.
 #include "i8.cuh"
@@ -30,6 +33,7 @@ constexpr int kSegment = 8;            // stages that fp32 adds exactly
 constexpr int kMaxStages = 8;
 constexpr int kSlots = 2;              // converted stages of X in flight
 constexpr int kSmallTokens = 64, kSmallThreads = 768, kSmallA = 3;    // A slots: TMEM columns 128 + (block * 3 + slot) * 64
+constexpr int kMaxCtas = 192;
 constexpr int kPairTokens = 256, kPairThreads = 512, kPairStages = 4;  // A: TMEM columns 256 + stage * 64
 constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
 constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
@@ -38,8 +42,11 @@ struct TcArgs {
   MatArgs m;
   int nt;              // tokens of a tile: a multiple of 16 (pairs: 32)
   int tiles_n, tiles;  // tiles of 256 channels (gated: 128), times the tiles of nt tokens
-  int split;           // CTAs (a cluster) that share a tile of small_kernel
   int stages;
+  // small_kernel: CTA c has `share` stages, the first `extra` CTAs one more; sums [CTA][its tail of a tile, its head of one]
+  // [nt / 4 tokens][256][4] of tiles that are shared
+  int share, extra;
+  int* parts;
   const uint32_t* squares;   // pair_kernel: the tokens' sums of squares, and
   uint32_t most;             //   up to which a tile is one segment: |sum| <= sqrt(sum w^2 sum x^2) <= 128 sqrt(K sum x^2) <= 2^24
 };
@@ -78,11 +85,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t rank, uint32_t v) {
-  asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.u32 [p], %2;\n\t}" ::"r"(addr), "r"(rank),
-               "r"(v)
-               : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
   uint4 v;
@@ -293,11 +295,52 @@ __device__ __forceinline__ void output_sums(const MatArgs& a, const int (&sum)[C
   if (GATED) named_bar(bar, 2 * width);   // the next tile's first buffer is free
 }
 
+// The first stage that a CTA has, and the CTA that has a stage.
+__device__ __forceinline__ int first_stage(const TcArgs& a, int cta) { return cta * a.share + min(cta, a.extra); }
+__device__ __forceinline__ int cta_of(const TcArgs& a, int stage) {
+  const int longer = a.extra * (a.share + 1);
+  return stage < longer ? stage / (a.share + 1) : a.extra + (stage - longer) / a.share;
+}
+
+// The tiles that small_kernel's CTAs share: their parts added up, and the outputs. blockIdx.x + 1: a CTA that begins within a tile (the
+// first of them in its tile does it); blockIdx.y: four tokens; 128 channels a block (not gated: blockIdx.z's).
+template <bool GATED>
+__global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int nk = (a.m.K + kTileK - 1) / kTileK, cta = blockIdx.x + 1, begin = first_stage(a, cta), tile = begin / nk;
+  if (begin == tile * nk || first_stage(a, cta - 1) > tile * nk) return;
+  const int from = cta - 1, to = cta_of(a, tile * nk + nk - 1);
+  const int row = threadIdx.x + (GATED ? 0 : blockIdx.z * 128), slab = 256 * a.nt;
+  const int n = tile % a.tiles_n * (GATED ? 128 : 256) + row, t = tile / a.tiles_n * a.nt + 4 * blockIdx.y;
+  if (n >= a.m.N || t >= a.m.T) return;
+  const float w0 = __ldg(a.m.ws[0] + n), w1 = GATED ? __ldg(a.m.ws[1] + n) : 0.f;
+  float xs[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) xs[e] = __ldg(a.m.xs + min(t + e, a.m.T - 1));
+  const int* p = a.parts + (blockIdx.y * 256 + row) * 4;
+  int g[4] = {}, u[4] = {};
+#pragma unroll 4
+  for (int k = from; k <= to; ++k) {
+    const int* q = p + (int64_t)(2 * k + (k == from)) * slab;      // the tile's head is the second of its CTA's parts
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(q));
+    g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+    if (GATED) {
+      const int4 y = __ldcg(reinterpret_cast<const int4*>(q + 512));
+      u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+    }
+  }
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = GATED ? silu_mul(product(g[e], xs[e], w0), product(u[e], xs[e], w1)) : product(g[e], xs[e], w0);
+  put_tokens<4>(a.m, t, a.m.T - t, n, v);
+}
+
 // ------------------------------------------------------------------------------------------------ one CTA, up to 64 tokens
 template <bool GATED>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x,
                                                                  const __grid_constant__ CUtensorMap map_w0,
                                                                  const __grid_constant__ CUtensorMap map_w1) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");           // (finish_kernel waits for this grid's end)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];          // packed tiles
@@ -311,12 +354,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   const uint32_t stage_bytes = 32768 + nt * 128, slot_bytes = nt * 256;
   const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
 
-  // ---- this CTA's tiles and its part of K (in stages of 128)
-  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / a.split, step_tiles = gridDim.x / a.split;
-  const int nk = (a.m.K + kTileK - 1) / kTileK;
-  const int k_begin = (int)((long long)rank * nk / a.split), k_end = (int)((long long)(rank + 1) * nk / a.split);
-  const int per_tile = k_end - k_begin, my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * per_tile;
+  // ---- this CTA's stages: `total` from stage `s_first` of tile `first` on
+  const int nk = (a.m.K + kTileK - 1) / kTileK, cta = blockIdx.x;
+  const int begin = first_stage(a, cta), total = a.share + (cta < a.extra);
+  const int first = begin / nk, s_first = begin - first * nk;
 
   // the copies' barriers first: the first stages are on their way while the rest is set up
   auto copy = [&](int stage, int tile, int k) {
@@ -328,15 +369,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     else tma_load_2d(to + 16384, &map_w0, k * kTileK, tn * 256 + 128, bar_full + stage);
     tma_load_2d(to + 32768, &map_x, k * kTileK, tt * nt, bar_full + stage);
   };
-  const bool single = per_tile <= kSegment;
-  const int early = min(stages, per_tile);                 // stages copied before the roles begin (of the first tile)
+  const int early = min(stages, total);                    // stages copied before the roles begin
+  int c_tile = first, c_s = s_first;                       // the next stage to be copied
+  auto copy_next = [&](int stage) {
+    copy(stage, c_tile, c_s);
+    if (++c_s == nk) { c_s = 0; ++c_tile; }
+  };
   if (warp == 20) {
-    if (lane < 3) prefetch_map(lane == 0 ? &map_w0 : lane == 1 ? &map_x : &map_w1);
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 12); }
     fence_mbar_init();
     __syncwarp();
     if (lane == 0)
-      for (int i = 0; i < early; ++i) copy(i, first, k_begin + i);
+      for (int i = 0; i < early; ++i) copy_next(i);
   }
   if (warp == 0) {
     if (lane < 2 * kSmallA) { mbar_init(&bar_a_full[0][0] + lane, 4); mbar_init(&bar_a_empty[0][0] + lane, 1); }
@@ -357,12 +401,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
       // ================================================================ copies
       if (lane == 0) {
         int stage = early % stages, phase = early == stages ? 0 : 1;   // (the first pass over the ring finds it empty)
-        for (int j = 0; j < my_tiles; ++j)
-          for (int k = k_begin + (j ? 0 : early); k < k_end; ++k) {
-            wait(bar_empty + stage, phase);
-            copy(stage, first + j * step_tiles, k);
-            if (++stage == stages) { stage = 0; phase ^= 1; }
-          }
+        for (int i = early; i < total; ++i) {
+          wait(bar_empty + stage, phase);
+          copy_next(stage);
+          if (++stage == stages) { stage = 0; phase ^= 1; }
+        }
         // (where waits have run out, copies may still be in flight)
         wait.dead = false;
         for (int t = max(0, total - stages); t < total; ++t) wait(bar_full + t % stages, (t / stages) & 1);
@@ -373,15 +416,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
       const uint32_t idesc = idesc_f16(nt), td = tmem + b * 64;
       const uint64_t dx = umma_desc_sw128(xring);
       int slot = 0, phase = 0, xslot = 0, xphase = 0, seg = 0;
-      for (int j = 0; j < my_tiles; ++j) {
+      for (int s0 = s_first, left = total; left > 0;) {        // a tile's stages s0 .. s1 - 1
+        const int s1 = min(nk, s0 + left), part = s1 - s0;
         bool fresh = true;
-        for (int s = 0; s < per_tile; ++s) {
+        for (int s = 0; s < part; ++s) {
           if (fresh) wait(bar_d_empty + b, (seg & 1) ^ 1);
           wait(bar_x_full + xslot, xphase, &bar_a_full[b][slot], phase);
           tc_fence_after();
           const uint32_t ta = tmem + 128 + (b * kSmallA + slot) * 64;
           const uint64_t dxs = dx + xslot * (slot_bytes / 16);
-          const bool ends = ends_segment(s, per_tile, b, single);
+          const bool ends = ends_segment(s, part, b, part <= kSegment);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_f16_ts(td, ta + 8 * k, dxs + (k >> 2) * (nt * 8) + 2 * (k & 3), idesc, k > 0 || !fresh);
@@ -392,15 +436,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
           __syncwarp();
           fresh = ends;
           seg += ends;
-          if (j == my_tiles - 1 && s == per_tile - 1)       // no arrival of a commit is in flight when the CTA ends
+          if (part == left && s == part - 1)                // no arrival of a commit is in flight when the CTA ends
             wait(&bar_a_empty[b][slot], phase, bar_x_empty + xslot, xphase);
           if (++slot == kSmallA) { slot = 0; phase ^= 1; }
           if (++xslot == kSlots) { xslot = 0; xphase ^= 1; }
         }
+        left -= part;
+        s0 = 0;
       }
     }
     __syncwarp();
-    if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else if (wg == 4) {
     // ================================================================ conversion of X
     regs_less<40>();
@@ -418,7 +463,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
       if (++slot == kSlots) { slot = 0; sphase ^= 1; }
     }
     __syncwarp();
-    if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else if (wg >= 2) {
     // ================================================================ conversion of block b's W
     regs_less<48>();
@@ -438,22 +482,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
       if (++slot == kSmallA) { slot = 0; sphase ^= 1; }
     }
     __syncwarp();
-    if (a.split > 1) { cluster_sync(); cluster_sync(); }
   } else {
     // ================================================================ block b's sums and outputs
     regs_more<152>();
     const int b = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
     int sum[kSmallTokens];
-    int seg = 0;
+    int seg = 0, tile = first;
     Scales<kSmallTokens> scales;
-    for (int j = 0; j < my_tiles; ++j) {
-      const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
+    for (int s0 = s_first, left = total; left > 0; ++tile) {
+      const int part = min(nk - s0, left), tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
       const int n = GATED ? tn * 128 + row : tn * 256 + b * 128 + row;
+      const bool whole = part == nk;
+      bool single = part <= kSegment, begun = false;
       scales.load(a.m, a.m.ws[GATED ? b : 0], t0, n);
-      bool begun = false;
-      for (int s = 0; s < per_tile; ++s) {
-        if (!ends_segment(s, per_tile, b, single)) continue;
+      for (int s = 0; s < part; ++s) {
+        if (!ends_segment(s, part, b, part <= kSegment)) continue;
         wait(bar_d_full + b, seg & 1);
         ++seg;
         tc_fence_after();
@@ -461,43 +505,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
         else first_sums(td, nt, sum);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_d_empty + b);
-        if (!begun && (!single || a.split > 1)) integer_sums(nt, sum);
+        if (!begun && !(single && whole)) integer_sums(nt, sum);
         begun = true;
       }
-      if (a.split == 1) output_sums<GATED>(a.m, sum, single, scales, t0, nt, n, b, xchg, row, 128, 1);
-    }
-    if (a.split > 1) {
-      // every CTA of the cluster is through with its rings; token t is finished by CTA t / per
-      const int per = (nt + a.split - 1) / a.split;
-      cluster_sync();
-      int r[16], to = 0, at = 0;                    // token t goes to place t % per of CTA t / per
-#pragma unroll 1
-      for (int c = 0; c * 16 < nt; ++c) {
-        give_sums(c, sum, r);
+      if (whole) {
+        output_sums<GATED>(a.m, sum, single, scales, t0, nt, n, b, xchg, row, 128, 1);
+      } else {
+        int* mine = a.parts + (int64_t)(2 * cta + (s0 == 0)) * 256 * nt + tid * 4;
+        const int count = min(nt, T - t0);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          st_peer(ring + ((rank * per + at) * 256 + (b * 128 + row)) * 4, to, (uint32_t)r[e]);
-          if (++at == per) { at = 0; ++to; }
-        }
+        for (int k = 0; k < kSmallTokens / 4; ++k)
+          if (4 * k < count) *reinterpret_cast<int4*>(mine + 1024 * k) = make_int4(sum[4 * k], sum[4 * k + 1], sum[4 * k + 2], sum[4 * k + 3]);
       }
-      cluster_sync();
-      const int tn = first % a.tiles_n, t0 = first / a.tiles_n * nt + rank * per, count = min(min(per, nt - rank * per), T - t0);
-      const int* got = reinterpret_cast<const int*>(smem);
-      const int n = GATED ? tn * 128 + row : tn * 256 + tid;
-      if (n < N) {
-        const float w0 = a.m.ws[0][n], w1 = GATED ? a.m.ws[1][n] : 0.f;
-        for (int t = GATED ? b : 0; t < count; t += GATED ? 2 : 1) {
-          int g = 0, u = 0;
-          for (int s = 0; s < a.split; ++s) {
-            const int* p = got + (s * per + t) * 256;
-            g += p[GATED ? row : tid];
-            if (GATED) u += p[128 + row];
-          }
-          const float xs = __ldg(a.m.xs + t0 + t);
-          float v[1] = {GATED ? silu_mul(product(g, xs, w0), product(u, xs, w1)) : product(g, xs, w0)};
-          put_tokens<1>(a.m, t0 + t, 1, n, v);
-        }
-      }
+      left -= part;
+      s0 = 0;
     }
   }
   tc_fence_before();
@@ -593,7 +614,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
 
   if (warp == 0) {
-    if (lane < 3) prefetch_map(lane == 0 ? &map_w0 : lane == 1 ? &map_x : &map_w1);
     if (lane < kPairStages) { mbar_init(bar_full + lane, 1); mbar_init(bar_ready + lane, 5 - rank); mbar_init(bar_empty + lane, 2); }
     if (lane < 2) { mbar_init(bar_d_full + lane, 1); mbar_init(bar_d_empty + lane, 8); }
     fence_mbar_init();
@@ -733,19 +753,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// Which kernel, and how the work is cut, by an estimate in units of a stage's time of products with 128 tokens (0.5 us).
+// Which kernel, and how the work is cut
 struct TcPlan {
   bool pair;
-  int nt, tiles_n, tiles, split, stages;
+  int nt, tiles_n, tiles, stages, ctas, share, extra;
   uint32_t smem;
 };
 
-static TcPlan plan(const MatArgs& a, bool gated, int sms, const int (&clusters)[4]) {
-  TcPlan p;
+static TcPlan plan(const MatArgs& a, bool gated, int sms) {
+  TcPlan p{};
   p.tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
   const int nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
   p.pair = a.T > kSmallTokens;
-  p.split = 1;
   if (p.pair) {
     // tokens of a tile: as few columns as the waves of tiles need in all
     long long best = 0;
@@ -755,14 +774,18 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms, const int (&clusters)[
     }
     p.stages = kPairStages;
     p.smem = 1024 + fixed + kPairStages * (16384 + p.nt * 128);
+    p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
+    p.ctas = 2 * min(p.tiles, sms / 2);
   } else {
-    p.nt = (a.T + 15) / 16 * 16;
-    while (p.split < 8 && p.split * 2 <= nk && p.tiles_n <= clusters[p.split == 1 ? 1 : p.split == 2 ? 2 : 3]) p.split *= 2;
-    const int stage = 32768 + p.nt * 128, rest = fixed + kSlots * p.nt * 256;
+    p.nt = (min(a.T, kSmallTokens) + 15) / 16 * 16;
+    p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
+    const int stage = 32768 + p.nt * 128, rest = fixed + kSlots * p.nt * 256, all = p.tiles * nk;
     p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
     p.smem = 1024 + rest + p.stages * stage;
+    p.ctas = min(all, min(sms, kMaxCtas));
+    p.share = all / p.ctas;
+    p.extra = all % p.ctas;
   }
-  p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
   return p;
 }
 
@@ -772,62 +795,49 @@ static bool map_rows(CUtensorMap* m, const int8_t* q, int rows, int cols, int64_
   return moe_internal::tmap_u8(m, q, 2, dims, strides, box);
 }
 
-static cudaLaunchConfig_t config(int grid, int threads, uint32_t smem, int cluster, cudaLaunchAttribute* at, cudaStream_t stream) {
+static cudaLaunchConfig_t config(const TcPlan& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(p.pair ? kPairThreads : kSmallThreads);
+  cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
-  if (cluster > 1) {
-    at->id = cudaLaunchAttributeClusterDimension;
-    at->val.clusterDim.x = cluster;
-    at->val.clusterDim.y = at->val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-  }
   return cfg;
 }
 
-// Per device, once: the kernels' shared memory, and how many clusters of 2, 4, 8 CTAs of small_kernel run at a time.
-struct Device {
-  bool ready;
-  int clusters[4];
-};
-static Device g_device[64];
-
-static bool prepare(Device& d) {
-  if (d.ready) return true;
-  if (cudaFuncSetAttribute(small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-      cudaFuncSetAttribute(small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-      cudaFuncSetAttribute(pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-      cudaFuncSetAttribute(pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
+// Once per device: the kernels' shared memory
+static bool prepare(int dev) {
+  static bool ready[64];
+  if (ready[dev]) return true;
+  const int most = kSmemLimit;
+  if (cudaFuncSetAttribute(small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return false;
-  for (int i = 1; i < 4; ++i) {
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = config(1 << i, kSmallThreads, kSmemLimit, 1 << i, &at, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&d.clusters[i], small_kernel<false>, &cfg) != cudaSuccess) return false;
-  }
-  d.ready = true;
+  ready[dev] = true;
   return true;
 }
 
-// (the tokens' sums of squares, then their binary16 values)
+// The workspace behind its header: either the sums of shared tiles, or the tokens' sums of squares and their binary16 values.
 static size_t squares_bytes(int T) { return ((size_t)T * 4 + 255) & ~(size_t)255; }
 size_t tc_workspace_bytes(int K, int T_max) {
-  return T_max > kSmallTokens ? squares_bytes(T_max) + (size_t)T_max * ((K + 63) / 64 * 128) : 0;
+  const size_t parts = (size_t)kMaxCtas * 2048 * ((min(T_max, kSmallTokens) + 15) / 16 * 16);
+  const size_t wide = T_max > kSmallTokens ? squares_bytes(T_max) + (size_t)T_max * ((K + 63) / 64 * 128) : 0;
+  return parts > wide ? parts : wide;
 }
 
 moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   const bool gated = a.w[1] != nullptr;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(g_device[dev])) { cudaGetLastError(); return MOE_ERR_CUDA; }
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(dev)) { cudaGetLastError(); return MOE_ERR_CUDA; }
   const int sms = moe_internal::num_sms();
   if (sms <= 1) return MOE_ERR_CUDA;
-  const TcPlan p = plan(a, gated, sms, g_device[dev].clusters);
+  const TcPlan p = plan(a, gated, sms);
   CUtensorMap mx, m0, m1;
   const int box_w = p.pair && gated ? 64 : 128;
   const int pieces = (a.K + 63) / 64 * 4;
-  uint32_t* squares = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader));
+  int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader));
+  uint32_t* squares = reinterpret_cast<uint32_t*>(parts);
   uint8_t* wide = reinterpret_cast<uint8_t*>(squares) + squares_bytes(a.T);
   if (!map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w)) return MOE_ERR_CUDA;
   if (p.pair) {
@@ -839,22 +849,32 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   }
   m1 = m0;
   if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
-  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.split, p.stages, squares, (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
+  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.share, p.extra, parts, squares,
+                    (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
+  cudaLaunchConfig_t cfg = config(p, stream);
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
     widen_kernel<<<min(a.T, sms * 16), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = config(2 * min(p.tiles, sms / 2), kPairThreads, p.smem, 1, &at, stream);
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     e = gated ? cudaLaunchKernelEx(&cfg, pair_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, pair_kernel<false>, args, mx, m0, m1);
   } else {
-    const cudaLaunchConfig_t cfg =
-        config(p.split > 1 ? p.tiles * p.split : min(p.tiles, sms), kSmallThreads, p.smem, p.split, &at, stream);
     e = gated ? cudaLaunchKernelEx(&cfg, small_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, small_kernel<false>, args, mx, m0, m1);
+    const int nk = (a.K + kTileK - 1) / kTileK;
+    if (e == cudaSuccess && (p.extra || p.share % nk)) {                    // (else every CTA has whole tiles)
+      cfg.gridDim = dim3(p.ctas - 1, p.nt / 4, gated ? 1 : 2);
+      cfg.blockDim = dim3(128);
+      cfg.dynamicSmemBytes = 0;
+      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      e = gated ? cudaLaunchKernelEx(&cfg, finish_kernel<true>, args) : cudaLaunchKernelEx(&cfg, finish_kernel<false>, args);
+    }
   }
   if (e != cudaSuccess) { cudaGetLastError(); return MOE_ERR_CUDA; }
   return MOE_OK;

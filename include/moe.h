@@ -475,10 +475,10 @@ typedef struct {
  *   multiples of 16. */
 moe_status_t moe_rms_norm_i8(const moe_norm_t* norm, const moe_i8_rows_t* xq, void* stream);
 
-/* Workspace of moe_i8_matmul and moe_i8_gated with weights like w and up to T_max tokens (0 for unsupported sizes). Its
- * first word is the device status word (moe_get_device_status): MOE_ERR_DEVICE_TIMEOUT where a wait ran out (the call's
- * outputs are void). Zero it once with moe_workspace_init(); the calls write nothing else to it, so calls that overlap on the
- * GPU may share one. */
+/* Workspace of moe_i8_matmul and moe_i8_gated with weights like w and up to T_max tokens (0 for unsupported sizes). Zero it once
+ * with moe_workspace_init(); it serves calls of any weights and tokens that it is large enough for, one after another (calls
+ * that overlap on the GPU must not share one). Its first word is the device status word (moe_get_device_status):
+ * MOE_ERR_DEVICE_TIMEOUT where a wait ran out; the call's outputs are void then. */
 size_t moe_i8_workspace_bytes(const moe_i8_rows_t* w, int32_t T_max);
 
 /* Product of 8-bit integers, x [T, K] tokens, w [N, K] output channels (K = cols of both):

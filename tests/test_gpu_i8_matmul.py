@@ -177,7 +177,7 @@ def test_nan_scales_stay_in_their_rows(m, T):
 
 @pytest.mark.parametrize("T", [1, 8, 24, 140, 300])
 def test_in_a_graph_and_on_two_streams(m, T):
-    """Captured calls follow their inputs; calls on two streams may share the workspace."""
+    """Captured calls follow their inputs; calls on two streams, each with a workspace of its own."""
     N, K = 320, 2064
     (wq, ws) = codes(N, K, 9, "normal")
     w = device_rows(m, wq, ws)
@@ -199,16 +199,16 @@ def test_in_a_graph_and_on_two_streams(m, T):
     torch.cuda.synchronize()
     want_h = h.clone()
     streams = [torch.cuda.Stream() for _ in range(2)]
-    outs = [[torch.empty_like(y), torch.empty_like(h)] for _ in streams]
-    for _ in range(4):
-        for s, (a, b) in zip(streams, outs):
-            with torch.cuda.stream(s):
-                m.moe_i8_matmul(x, w, y=a, ws=wsp)
-                m.moe_i8_gated(x, w, w, y_bf16=b, ws=wsp)
+    outs = [[torch.empty_like(y), torch.empty_like(h), w.workspace(T)] for _ in streams]
     torch.cuda.synchronize()
-    for a, b in outs:
-        assert torch.equal(a, y) and torch.equal(b, want_h)
-    assert m.moe_get_device_status(wsp) == 0
+    for _ in range(4):
+        for s, (a, b, own) in zip(streams, outs):
+            with torch.cuda.stream(s):
+                m.moe_i8_matmul(x, w, y=a, ws=own)
+                m.moe_i8_gated(x, w, w, y_bf16=b, ws=own)
+    torch.cuda.synchronize()
+    for a, b, own in outs:
+        assert torch.equal(a, y) and torch.equal(b, want_h) and m.moe_get_device_status(own) == 0
 
 
 @pytest.mark.parametrize("T,N,K,gated", [(1, 6144, 4096, False), (8, 16384, 4096, False), (8, 4096, 2048, True), (5, 4096, 6144, False),

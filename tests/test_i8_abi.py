@@ -93,10 +93,10 @@ def test_norm_refuses(m, monkeypatch):
 def test_products_refuse(m, monkeypatch):
     L = m.lib()
 
-    def matmul(x=None, w=None, base=None, bs=0, y=P(), ys=8, yb=None, ybs=0, ws=P(), n=256):
+    def matmul(x=None, w=None, base=None, bs=0, y=P(), ys=8, yb=None, ybs=0, ws=P(), n=1 << 24):
         return L.moe_i8_matmul(x or rows(m), w or rows(m, rows=8), base, bs, y, ys, yb, ybs, ws, n, None)
 
-    def gated(x=None, g=None, u=None, y=P(), ys=8, yb=None, ybs=0, ws=P(), n=256):
+    def gated(x=None, g=None, u=None, y=P(), ys=8, yb=None, ybs=0, ws=P(), n=1 << 24):
         return L.moe_i8_gated(x or rows(m), g or rows(m, rows=8), u or rows(m, rows=8), y, ys, yb, ybs, ws, n, None)
 
     for call in (matmul, gated):
@@ -112,9 +112,9 @@ def test_products_refuse(m, monkeypatch):
         assert gated(u=rows(m, **bad)) == st, bad
     assert matmul(base=P(2), bs=8) == 1 and matmul(base=P(), bs=7) == 1
     assert gated(u=rows(m, rows=9)) == 2 and gated(u=rows(m, rows=8, cols=48)) == 2
-    assert L.moe_i8_gated(rows(m), rows(m, rows=8), None, P(), 8, None, 0, P(), 256, None) == 1
-    assert L.moe_i8_matmul(None, rows(m), None, 0, P(), 8, None, 0, P(), 256, None) == 1
-    assert L.moe_i8_matmul(rows(m), None, None, 0, P(), 8, None, 0, P(), 256, None) == 1
+    assert L.moe_i8_gated(rows(m), rows(m, rows=8), None, P(), 8, None, 0, P(), 1 << 24, None) == 1
+    assert L.moe_i8_matmul(None, rows(m), None, 0, P(), 8, None, 0, P(), 1 << 24, None) == 1
+    assert L.moe_i8_matmul(rows(m), None, None, 0, P(), 8, None, 0, P(), 1 << 24, None) == 1
     for name, call in (("i8_matmul", matmul), ("i8_gated", gated)):
         monkeypatch.setenv("MOE_FAULT", name)
         assert call() == 8
