@@ -43,9 +43,9 @@ struct TcArgs {
   int nt;              // tokens of a tile: a multiple of 16 (pairs: 32)
   int tiles_n, tiles;  // tiles of 256 channels (gated: 128), times the tiles of nt tokens
   int stages;
-  // small_kernel: CTA c has `share` stages, the first `extra` CTAs one more; sums [CTA][its tail of a tile, its head of one]
-  // [nt / 4 tokens][256][4] of tiles that are shared
-  int share, extra;
+  // small_kernel: CTA c has `share` grains of stages (1, or a tile's), the first `extra` CTAs one more; sums [CTA][its tail of a tile, its
+  // head of one][nt / 4 tokens][256][4] of tiles that are shared
+  int grain, share, extra;
   int* parts;
   const uint32_t* squares;   // pair_kernel: the tokens' sums of squares, and
   uint32_t most;             //   up to which a tile is one segment: |sum| <= sqrt(sum w^2 sum x^2) <= 128 sqrt(K sum x^2) <= 2^24
@@ -295,21 +295,24 @@ __device__ __forceinline__ void output_sums(const MatArgs& a, const int (&sum)[C
   if (GATED) named_bar(bar, 2 * width);   // the next tile's first buffer is free
 }
 
-// The first stage that a CTA has, and the CTA that has a stage.
-__device__ __forceinline__ int first_stage(const TcArgs& a, int cta) { return cta * a.share + min(cta, a.extra); }
+// The first stage that a CTA has, and (for a grain of 1) the CTA that has a stage.
+__device__ __forceinline__ int first_stage(const TcArgs& a, int cta) { return (cta * a.share + min(cta, a.extra)) * a.grain; }
 __device__ __forceinline__ int cta_of(const TcArgs& a, int stage) {
   const int longer = a.extra * (a.share + 1);
   return stage < longer ? stage / (a.share + 1) : a.extra + (stage - longer) / a.share;
 }
 
-// The tiles that small_kernel's CTAs share: their parts added up, and the outputs. blockIdx.x + 1: a CTA that begins within a tile (the
-// first of them in its tile does it); blockIdx.y: four tokens; 128 channels a block (not gated: blockIdx.z's).
+// The tiles that small_kernel's CTAs share: their parts added up, and the outputs. blockIdx.x: the tile, or where there are more tiles
+// than CTAs, a CTA less one that begins within a tile (the only one in it); blockIdx.y: four tokens; 128 channels a block (not
+// gated: blockIdx.z's).
 template <bool GATED>
 __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
+  const int nk = (a.m.K + kTileK - 1) / kTileK;
+  const bool by_tile = a.tiles < (int)gridDim.x + 1;
+  const int tile = by_tile ? blockIdx.x : first_stage(a, blockIdx.x + 1) / nk;
+  const int from = cta_of(a, tile * nk), to = cta_of(a, tile * nk + nk - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int nk = (a.m.K + kTileK - 1) / kTileK, cta = blockIdx.x + 1, begin = first_stage(a, cta), tile = begin / nk;
-  if (begin == tile * nk || first_stage(a, cta - 1) > tile * nk) return;
-  const int from = cta - 1, to = cta_of(a, tile * nk + nk - 1);
+  if (from == to || (!by_tile && from != (int)blockIdx.x)) return;
   const int row = threadIdx.x + (GATED ? 0 : blockIdx.z * 128), slab = 256 * a.nt;
   const int n = tile % a.tiles_n * (GATED ? 128 : 256) + row, t = tile / a.tiles_n * a.nt + 4 * blockIdx.y;
   if (n >= a.m.N || t >= a.m.T) return;
@@ -350,13 +353,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
-  const int nt = a.nt, stages = a.stages, T = a.m.T, N = a.m.N;
+  const int nt = a.nt, stages = a.stages, T = a.m.T;
   const uint32_t stage_bytes = 32768 + nt * 128, slot_bytes = nt * 256;
   const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
 
   // ---- this CTA's stages: `total` from stage `s_first` of tile `first` on
   const int nk = (a.m.K + kTileK - 1) / kTileK, cta = blockIdx.x;
-  const int begin = first_stage(a, cta), total = a.share + (cta < a.extra);
+  const int begin = first_stage(a, cta), total = (a.share + (cta < a.extra)) * a.grain;
   const int first = begin / nk, s_first = begin - first * nk;
 
   // the copies' barriers first: the first stages are on their way while the rest is set up
@@ -756,37 +759,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // Which kernel, and how the work is cut
 struct TcPlan {
   bool pair;
-  int nt, tiles_n, tiles, stages, ctas, share, extra;
+  int nt, tiles_n, tiles, stages, ctas, grain, share, extra;
   uint32_t smem;
 };
 
+// small_kernel: a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3 TB/s. A second
+// launch that adds up `ctas` parts of nt tokens takes 0.5 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x
+// 4096 (16 tiles): 28.2 us a tile a CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6;
+// 16 x 4096 x 32768 (128 tiles): 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
+// pair_kernel: 1.2 us more than small_kernel to begin with; a stage takes 0.34 us and 0.65 ns a token (converting W), or with all SMs at
+// it 2.5 ns a token (the products).
 static TcPlan plan(const MatArgs& a, bool gated, int sms) {
-  TcPlan p{};
-  p.tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-  const int nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
-  p.pair = a.T > kSmallTokens;
-  if (p.pair) {
-    // tokens of a tile: as few columns as the waves of tiles need in all
-    long long best = 0;
-    for (int nt = kPairTokens; nt >= 96; nt -= 32) {
-      const long long tiles = (long long)p.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms / 2 - 1) / (sms / 2) * (nt + 16);
-      if (best == 0 || cost < best) { best = cost; p.nt = nt; }
+  TcPlan best{};
+  double least = 0;
+  const int tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
+  auto consider = [&](const TcPlan& p, double ns) {
+    if (least == 0 || ns < least) {
+      least = ns;
+      best = p;
     }
-    p.stages = kPairStages;
-    p.smem = 1024 + fixed + kPairStages * (16384 + p.nt * 128);
-    p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
-    p.ctas = 2 * min(p.tiles, sms / 2);
-  } else {
-    p.nt = (min(a.T, kSmallTokens) + 15) / 16 * 16;
-    p.tiles = p.tiles_n * ((a.T + p.nt - 1) / p.nt);
+  };
+  if (a.T <= 2 * kSmallTokens) {
+    TcPlan p{};
+    const int tiles_t = (a.T + kSmallTokens - 1) / kSmallTokens, most = min(sms, kMaxCtas);
+    p.nt = ((a.T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
+    p.tiles_n = tiles_n;
+    p.tiles = tiles_n * tiles_t;
     const int stage = 32768 + p.nt * 128, rest = fixed + kSlots * p.nt * 256, all = p.tiles * nk;
     p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
     p.smem = 1024 + rest + p.stages * stage;
-    p.ctas = min(all, min(sms, kMaxCtas));
-    p.share = all / p.ctas;
-    p.extra = all % p.ctas;
+    const double stage_ns = 530 + 4 * p.nt, memory = (double)tiles_n * 256 * a.K / 6300;
+    auto time = [&](int stages) { return stages * stage_ns > memory ? stages * stage_ns : memory; };
+    p.ctas = min(p.tiles, most);
+    p.grain = nk;
+    p.share = p.tiles / p.ctas;
+    p.extra = p.tiles % p.ctas;
+    consider(p, time((p.tiles + p.ctas - 1) / p.ctas * nk));
+    p.grain = 1;
+    for (int m = 1; m <= most / p.tiles + 1; ++m) {           // m CTAs a tile, and all there are
+      p.ctas = min(all, m <= most / p.tiles ? m * p.tiles : most);
+      p.share = all / p.ctas;
+      p.extra = all % p.ctas;
+      const double parts = (p.ctas + p.tiles - 1) / p.tiles;
+      if (p.ctas > p.tiles || m > most / p.tiles)
+        consider(p, time((all + p.ctas - 1) / p.ctas) + 500 + 340 * (parts + (p.ctas % p.tiles ? 1 : 0)) + 0.73 * p.ctas * p.nt);
+    }
   }
-  return p;
+  if (a.T > kSmallTokens) {
+    for (int nt = min(kPairTokens, (a.T + 31) / 32 * 32); nt >= 96; nt -= 32) {
+      TcPlan p{};
+      p.pair = true;
+      p.nt = nt;
+      p.tiles_n = tiles_n;
+      p.tiles = tiles_n * ((a.T + nt - 1) / nt);
+      p.stages = kPairStages;
+      p.smem = 1024 + fixed + kPairStages * (16384 + nt * 128);
+      p.ctas = 2 * min(p.tiles, sms / 2);
+      const int pairs = sms / 2, waves = (p.tiles + pairs - 1) / pairs;
+      const double alone = 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
+      consider(p, 1200 + (double)waves * nk * (alone > full ? alone : full));
+    }
+  }
+  return best;
 }
 
 static bool map_rows(CUtensorMap* m, const int8_t* q, int rows, int cols, int64_t stride, int box_rows) {
@@ -849,7 +883,7 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   }
   m1 = m0;
   if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
-  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.share, p.extra, parts, squares,
+  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.grain, p.share, p.extra, parts, squares,
                     (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
   cudaLaunchConfig_t cfg = config(p, stream);
   cudaLaunchAttribute at;
@@ -864,9 +898,8 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
     e = gated ? cudaLaunchKernelEx(&cfg, pair_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, pair_kernel<false>, args, mx, m0, m1);
   } else {
     e = gated ? cudaLaunchKernelEx(&cfg, small_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, small_kernel<false>, args, mx, m0, m1);
-    const int nk = (a.K + kTileK - 1) / kTileK;
-    if (e == cudaSuccess && (p.extra || p.share % nk)) {                    // (else every CTA has whole tiles)
-      cfg.gridDim = dim3(p.ctas - 1, p.nt / 4, gated ? 1 : 2);
+    if (e == cudaSuccess && p.grain == 1 && p.ctas > 1) {
+      cfg.gridDim = dim3(min(p.tiles, p.ctas - 1), p.nt / 4, gated ? 1 : 2);
       cfg.blockDim = dim3(128);
       cfg.dynamicSmemBytes = 0;
       at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
