@@ -34,7 +34,14 @@ constexpr int kMaxStages = 8;
 constexpr int kSlots = 2;              // converted stages of X in flight
 constexpr int kSmallTokens = 64, kSmallThreads = 768, kSmallA = 3;    // A slots: TMEM columns 128 + (block * 3 + slot) * 64
 constexpr int kMaxCtas = 192;
-constexpr int kPairTokens = 256, kPairThreads = 512, kPairStages = 4;  // A: TMEM columns 256 + stage * 64
+// pair_kernel with tiles of up to 256 tokens, and of up to 128 with more stages and two warpgroups that convert W (stages in turn; an
+// even number of stages, so that each has its own)
+template <int TOKENS> struct Pair {
+  static constexpr int kStages = TOKENS == 256 ? 4 : 6, kConverters = TOKENS == 256 ? 1 : 2, kThreads = (3 + kConverters) * 128;
+  static constexpr int kSumRegs = TOKENS == 256 ? 216 : 152, kConvertRegs = TOKENS == 256 ? 40 : 48;
+  static constexpr uint32_t kTmemA = TOKENS;             // accumulators of the halves at 0 and TOKENS / 2, then 64 columns of A a stage
+};
+constexpr int kPairTokens = 256;
 constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
 constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
 
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     __syncwarp();
   } else if (wg == 4) {
     // ================================================================ conversion of X
-    regs_less<40>();
+    regs_less<56>();
     int stage = 0, phase = 0, slot = 0, sphase = 1;
     for (int i = 0; i < total; ++i) {
       wait(bar_x_empty + slot, sphase, bar_full + stage, phase);
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     __syncwarp();
   } else if (wg >= 2) {
     // ================================================================ conversion of block b's W
-    regs_less<48>();
+    regs_less<56>();
     const int b = wg - 2, row = tid & 127;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 128 + b * kSmallA * 64;
     int stage = 0, phase = 0, slot = 0, sphase = 1;
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     __syncwarp();
   } else {
     // ================================================================ block b's sums and outputs
-    regs_more<152>();
+    regs_more<136>();
     const int b = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
     int sum[kSmallTokens];
@@ -595,33 +602,35 @@ __device__ __forceinline__ uint32_t tile_squares(const TcArgs& a, int t0) {
   return m;
 }
 
-template <bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <bool GATED, int TOKENS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThreads, 1)
     pair_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
                 const __grid_constant__ CUtensorMap map_w1) {
+  using P = Pair<TOKENS>;
+  constexpr int kStages = P::kStages, kControl = 2 + P::kConverters, kCopier = 4 * kControl;      // (warpgroup, warp)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   // A stage: W's codes, X in binary16. It is full when its copies have landed, ready when W has been converted (CTA 0's barrier: its
   // four warps, and one arrival that passes on CTA 1's), and empty when both halves' products are done; then its columns of A
   // are free as well.
-  __shared__ uint64_t bar_full[kPairStages], bar_ready[kPairStages], bar_empty[kPairStages];
+  __shared__ uint64_t bar_full[kStages], bar_ready[kStages], bar_empty[kStages];
   __shared__ uint64_t bar_d_full[2], bar_d_empty[2];                    // accumulators of the halves (empty: CTA 0's)
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
   const int half = a.nt / 2, part = half / 2;                           // tokens of a half, and of it in this CTA
   const uint32_t stage_bytes = 16384 + half * 256;
-  const uint32_t ring = smem_u32(smem), xchg = ring + kPairStages * stage_bytes;
+  const uint32_t ring = smem_u32(smem), xchg = ring + kStages * stage_bytes;
   const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step_tiles = gridDim.x / 2;
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
 
   if (warp == 0) {
-    if (lane < kPairStages) { mbar_init(bar_full + lane, 1); mbar_init(bar_ready + lane, 5 - rank); mbar_init(bar_empty + lane, 2); }
+    if (lane < kStages) { mbar_init(bar_full + lane, 1); mbar_init(bar_ready + lane, 5 - rank); mbar_init(bar_empty + lane, 2); }
     if (lane < 2) { mbar_init(bar_d_full + lane, 1); mbar_init(bar_d_empty + lane, 8); }
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == kCopier + 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
@@ -632,9 +641,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = s_tmem;
   Waits wait{a.m.status, false};
 
-  if (wg == 3) {
+  if (wg == kControl) {
     regs_less<40>();
-    if (warp == 12) {
+    if (warp == kCopier) {
       // ================================================================ copies
       if (lane == 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");  // X in binary16 is there
@@ -653,18 +662,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             tma_load_3d(to + 16384, &map_x, 0, t0, 2 * k, bar_full + stage);
             tma_load_3d(to + 16384 + part * 256, &map_x, 0, t0 + half, 2 * k, bar_full + stage);
-            if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+            if (++stage == kStages) { stage = 0; phase ^= 1; }
           }
         }
         // no copy (where waits have run out) and no arrival of a commit is in flight when the CTA ends
         wait.dead = false;
-        for (int t = max(0, total - kPairStages); t < total; ++t)
-          wait(bar_full + t % kPairStages, (t / kPairStages) & 1, bar_empty + t % kPairStages, (t / kPairStages) & 1);
+        for (int t = max(0, total - kStages); t < total; ++t)
+          wait(bar_full + t % kStages, (t / kStages) & 1, bar_empty + t % kStages, (t / kStages) & 1);
       }
-    } else if (warp <= 14 && rank == 0) {
+    } else if (warp <= kCopier + 2 && rank == 0) {
       // ================================================================ products of half d (both CTAs')
-      const int d = warp - 13;
-      const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * 128;
+      const int d = warp - kCopier - 1;
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * (TOKENS / 2);
       const uint64_t dx = umma_desc_sw128(ring + 16384 + d * part * 256);
       int stage = 0, phase = 0, seg = 0;
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -677,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
           wait(bar_ready + stage, phase);
           tc_fence_after();
-          const uint32_t ta = tmem + 256 + stage * 64;
+          const uint32_t ta = tmem + P::kTmemA + stage * 64;
           const uint64_t dxs = dx + stage * (stage_bytes / 16);
           const bool ends = ends_segment(s, nk, d, single);
           if (elect_one()) {
@@ -689,40 +698,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           fresh = ends;
           seg += ends;
-          if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
       }
-    } else if (warp == 13) {
+    } else if (warp == kCopier + 1) {
       // ================================================================ CTA 1: stages that are ready here, passed on to CTA 0
       // (an arrival in the other CTA takes 100 cycles more than one here, which the converting warps do not have)
       int stage = 0, phase = 0;
       for (int i = 0; i < total; ++i) {
         wait(bar_ready + stage, phase);
         if (lane == 0) arrive_first(bar_ready + stage);
-        if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
     }
-  } else if (wg == 2) {
-    // ================================================================ conversion of W
-    regs_less<40>();
+  } else if (wg >= 2) {
+    // ================================================================ conversion of W: stages wg - 2, + kConverters, ...
+    regs_less<P::kConvertRegs>();
     const int row = tid & 127;
-    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 256;
-    int stage = 0, phase = 0;
-    for (int i = 0; i < total; ++i) {
+    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + P::kTmemA;
+    int stage = wg - 2, phase = 0;
+    for (int i = wg - 2; i < total; i += P::kConverters) {
       wait(bar_full + stage, phase);
       tc_fence_after();
       convert_w(ring + stage * stage_bytes + row * 128, row, ta + stage * 64);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ready + stage);
-      if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+      if ((stage += P::kConverters) >= kStages) { stage -= kStages; phase ^= 1; }
     }
   } else {
     // ================================================================ half d's sums and outputs
-    regs_more<216>();
+    regs_more<P::kSumRegs>();
     const int d = wg, row = tid & 127;
-    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * 128;
-    int sum[kPairTokens / 2];
-    Scales<kPairTokens / 2> scales;
+    const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * (TOKENS / 2);
+    int sum[TOKENS / 2];
+    Scales<TOKENS / 2> scales;
     int seg = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int j = 0; j < my_tiles; ++j) {
@@ -750,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                         // no CTA leaves while the other's barriers or columns are in use
-  if (warp == 13) {
+  if (warp == kCopier + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
@@ -758,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // Which kernel, and how the work is cut
 struct TcPlan {
-  bool pair;
+  int pair;               // 0, or pair_kernel's TOKENS
   int nt, tiles_n, tiles, stages, ctas, grain, share, extra;
   uint32_t smem;
 };
@@ -767,8 +776,9 @@ struct TcPlan {
 // launch that adds up `ctas` parts of nt tokens takes 0.5 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x
 // 4096 (16 tiles): 28.2 us a tile a CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6;
 // 16 x 4096 x 32768 (128 tiles): 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
-// pair_kernel: 1.2 us more than small_kernel to begin with; a stage takes 0.34 us and 0.65 ns a token (converting W), or with all SMs at
-// it 2.5 ns a token (the products).
+// pair_kernel: 1.2 us more than small_kernel to begin with; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token,
+// or with all SMs at it 2.5 ns a token (the products). (201 x 4096 x 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one
+// warpgroup that converts, 24.5 with 256.)
 static TcPlan plan(const MatArgs& a, bool gated, int sms) {
   TcPlan best{};
   double least = 0;
@@ -806,17 +816,17 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
     }
   }
   if (a.T > kSmallTokens) {
+    const int pairs = sms / 2;
     for (int nt = min(kPairTokens, (a.T + 31) / 32 * 32); nt >= 96; nt -= 32) {
       TcPlan p{};
-      p.pair = true;
+      p.pair = nt <= 128 ? 128 : 256;
       p.nt = nt;
       p.tiles_n = tiles_n;
       p.tiles = tiles_n * ((a.T + nt - 1) / nt);
-      p.stages = kPairStages;
-      p.smem = 1024 + fixed + kPairStages * (16384 + nt * 128);
-      p.ctas = 2 * min(p.tiles, sms / 2);
-      const int pairs = sms / 2, waves = (p.tiles + pairs - 1) / pairs;
-      const double alone = 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
+      p.smem = 1024 + fixed + (p.pair == 128 ? Pair<128>::kStages : Pair<256>::kStages) * (16384 + nt * 128);
+      p.ctas = 2 * min(p.tiles, pairs);
+      const int waves = (p.tiles + pairs - 1) / pairs;
+      const double alone = p.pair == 128 ? 370 : 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
       consider(p, 1200 + (double)waves * nk * (alone > full ? alone : full));
     }
   }
@@ -832,7 +842,7 @@ static bool map_rows(CUtensorMap* m, const int8_t* q, int rows, int cols, int64_
 static cudaLaunchConfig_t config(const TcPlan& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ctas);
-  cfg.blockDim = dim3(p.pair ? kPairThreads : kSmallThreads);
+  cfg.blockDim = dim3(p.pair == 0 ? kSmallThreads : p.pair == 128 ? Pair<128>::kThreads : Pair<256>::kThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
   return cfg;
@@ -845,8 +855,10 @@ static bool prepare(int dev) {
   const int most = kSmemLimit;
   if (cudaFuncSetAttribute(small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
       cudaFuncSetAttribute(small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+      cudaFuncSetAttribute(pair_kernel<false, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<true, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<false, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaFuncSetAttribute(pair_kernel<true, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return false;
   ready[dev] = true;
   return true;
@@ -895,7 +907,9 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = gated ? cudaLaunchKernelEx(&cfg, pair_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, pair_kernel<false>, args, mx, m0, m1);
+    auto* kernel = p.pair == 128 ? (gated ? pair_kernel<true, 128> : pair_kernel<false, 128>)
+                                 : (gated ? pair_kernel<true, 256> : pair_kernel<false, 256>);
+    e = cudaLaunchKernelEx(&cfg, kernel, args, mx, m0, m1);
   } else {
     e = gated ? cudaLaunchKernelEx(&cfg, small_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, small_kernel<false>, args, mx, m0, m1);
     if (e == cudaSuccess && p.grain == 1 && p.ctas > 1) {
