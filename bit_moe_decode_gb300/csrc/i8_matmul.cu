@@ -261,7 +261,7 @@ using namespace moe::i8;
 
 extern "C" size_t moe_i8_workspace_bytes(const moe_i8_rows_t* w, int32_t T_max) {
   if (check_rows(w) != MOE_OK || T_max < 1 || T_max > kMaxRows) return 0;
-  return sizeof(WsHeader) + tc_workspace_bytes(w->cols, T_max);
+  return sizeof(WsHeader) + (rows_stages(T_max, w->cols) ? 0 : tc_workspace_bytes(w->cols, T_max));   // (rows_kernel needs none)
 }
 
 extern "C" moe_status_t moe_i8_matmul(const moe_i8_rows_t* x, const moe_i8_rows_t* w, const float* base, int64_t base_stride,

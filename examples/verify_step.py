@@ -5,7 +5,10 @@ paged cache (rotated on the way), the new rows attend to it, and the routed expe
 last layer the logits become probabilities (penalties, temperature) and moe_spec_accept keeps the drafts that the model
 agrees with. Rejected tokens stay in the cache past the sequence's length and are overwritten by the next step.
 
-    python examples/verify_step.py --seqs 2 --drafts 3 --steps 20
+With --dense8 what stands around the attention and the routed experts runs in 8 bits too: the norms with the residual's addition,
+the projections of q, k, v, of attention's output and to the vocabulary, and a shared expert in every layer.
+
+    python examples/verify_step.py --seqs 2 --drafts 3 --steps 20 [--dense8]
 """
 import argparse
 import os
@@ -20,7 +23,7 @@ import bit_moe_decode_gb300 as m  # noqa: E402
 
 class Decoder:
     def __init__(self, seqs=2, drafts=3, layers=2, H=512, I=256, E=8, k=2, heads=8, kv_heads=2, D=64, vocab=1024, max_len=512,
-                 fmt=None, temperature=0.8, seed=0, device="cuda"):
+                 fmt=None, temperature=0.8, seed=0, device="cuda", dense8=False, shared_I=512):
         rows = seqs * (1 + drafts)
         assert rows <= 8, "the experts' verify sweep takes up to 8 rows"
         self.S, self.K, self.R, self.H, self.E, self.k, self.V, self.D = seqs, drafts, rows, H, E, k, vocab, D
@@ -63,6 +66,20 @@ class Decoder:
         self.attn = torch.empty_like(self.q)
         self.probs = torch.empty(rows, vocab, device=device)
         self.result = torch.empty(seqs, 2, dtype=torch.int32, device=device)
+        self.dense8 = dense8
+        if dense8:
+            for lay in self.layers:
+                for name in ("qkv", "out"):
+                    lay[name + "8"] = m.I8Rows.of(lay[name])
+                lay["gate8"], lay["up8"] = (m.I8Rows.of(rand(shared_I, H)) for _ in range(2))
+                lay["down8"] = m.I8Rows.of(rand(H, shared_I))
+            self.head8 = m.I8Rows.of(self.head)
+            self.x8, self.attn8, self.act8 = m.I8Rows(rows, H), m.I8Rows(rows, heads * D), m.I8Rows(rows, shared_I)
+            self.qkv = torch.empty(rows, (heads + 2 * kv_heads) * D, dtype=torch.bfloat16, device=device)
+            self.act = torch.empty(rows, shared_I, dtype=torch.bfloat16, device=device)
+            self.logits = torch.empty(rows, vocab, device=device)
+            # one workspace for all products: they run one after another
+            self.ws8 = max((w.workspace(rows) for w in (self.head8, *(lay[n] for n in ("qkv8", "out8", "gate8", "down8")))), key=torch.numel)
 
     def forward(self, tokens):
         """Logits [rows, V] of the rows' next tokens; seq_len holds the lengths with these rows."""
@@ -82,6 +99,30 @@ class Decoder:
         m.moe_rms_norm_bf16(h, self.R, self.H, 1e-6, self.x)
         return (self.x @ self.head.T).float() + self.bigram[tokens]
 
+    def forward8(self, tokens):
+        """The same with the dense half in 8 bits."""
+        h, r = self.embed[tokens].float(), None
+        for lay in self.layers:
+            m.moe_rms_norm_i8(h, self.x8, r=r, h_out=h)              # the last layer's experts are added on the way
+            m.moe_i8_matmul(self.x8, lay["qkv8"], y_bf16=self.qkv, ws=self.ws8)
+            qkv = self.qkv.view(self.R, -1, self.D)
+            a, b = self.heads, self.heads + self.kv_heads
+            m.moe_kv_append(lay["cache"], self.batch, qkv[:, a:b], qkv[:, b:], q=qkv[:, :a], q_out=self.q, cos=self.cos,
+                            sin=self.sin, ws=self.kv_ws)
+            m.moe_kv_attention(lay["cache"], self.batch, self.q, self.D ** -0.5, self.attn, ws=self.kv_ws)
+            m.moe_i8_quantize(self.attn.view(self.R, -1), self.attn8)
+            m.moe_i8_matmul(self.attn8, lay["out8"], y=h, base=h, ws=self.ws8)
+            m.moe_rms_norm_i8(h, self.x8, x_bf16=self.x)             # bf16 for the router and the routed experts
+            m.moe_route_topk(lay["router"], self.x, self.R, self.H, self.E, self.k, None, None, 0, self.idx, self.w)
+            m.moe_expert_ffn_verify(lay["experts"], self.x, self.R, self.idx, self.w, self.k, self.y, ws=self.ws)
+            m.moe_i8_gated(self.x8, lay["gate8"], lay["up8"], y_bf16=self.act, ws=self.ws8)
+            m.moe_i8_quantize(self.act, self.act8)
+            m.moe_i8_matmul(self.act8, lay["down8"], y=h, base=h, ws=self.ws8)
+            r = self.y
+        m.moe_rms_norm_i8(h, self.x8, r=r)
+        m.moe_i8_matmul(self.x8, self.head8, y=self.logits, ws=self.ws8)
+        return self.logits + self.bigram[tokens]
+
     def step(self, last):
         """last [S]: each sequence's last token, not yet in the cache. Returns per sequence the tokens that follow it."""
         S, K, V = self.S, self.K, self.V
@@ -94,7 +135,7 @@ class Decoder:
         before = self.seq_len.clone()
         self.seq_len += 1 + K
         self.counts.scatter_add_(1, last[:, None], torch.ones_like(last[:, None], dtype=torch.int32))
-        logits = self.forward(rows.reshape(-1))
+        logits = (self.forward8 if self.dense8 else self.forward)(rows.reshape(-1))
         m.moe_logits_probs(logits, self.params, self.probs, rows_per_seq=1 + K, counts=self.counts, draft=self.draft)
         u = torch.rand(S, K + 1, generator=self.gen, device=self.dev)
         q = torch.stack(dist, 1).contiguous() if K else [None] * S
@@ -114,7 +155,7 @@ class Decoder:
                 break
             for s, new in enumerate(self.step(torch.tensor([o[-1] for o in out], device=self.dev))):
                 out[s] += new
-        for ws in (self.ws, self.kv_ws):
+        for ws in (self.ws, self.kv_ws) + ((self.ws8,) if self.dense8 else ()):
             if m.moe_get_device_status(ws) != 0:
                 raise RuntimeError("device status not OK")
         return out
@@ -126,8 +167,9 @@ def main():
     ap.add_argument("--drafts", type=int, default=3)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--temperature", type=float, default=0.8)
+    ap.add_argument("--dense8", action="store_true")
     a = ap.parse_args()
-    d = Decoder(a.seqs, a.drafts, temperature=a.temperature)
+    d = Decoder(a.seqs, a.drafts, temperature=a.temperature, dense8=a.dense8)
     t0 = time.time()
     out = d.generate([7 + s for s in range(a.seqs)], a.steps)
     n = sum(len(o) - 1 for o in out)
