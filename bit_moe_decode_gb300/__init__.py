@@ -321,29 +321,27 @@ def moe_logits_probs(logits, params, probs, rows_per_seq: int = 1, counts=None, 
 
 # ------------------------------------------------------------------------------------------------ the dense half in 8 bits
 _F32 = torch.float32
+_TYPE = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.int16: MOE_TYPE_BF16}
 _NORM = struct.Struct("@iiiiPqPqPf4xPqP")          # moe_norm_t (packed: a ctypes structure takes a microsecond more to fill)
 
 
 def _typed_rows(t, shape):
     """Pointer, type and row stride (elements) of an fp32 or bf16 [n, m] tensor whose rows may be slices of wider ones."""
-    dtype = t.dtype
-    assert t.is_cuda and (dtype is _F32 or dtype in _BF16_SIZED) and t.shape == shape and t.stride(1) == 1, \
-        "expected fp32 or bf16 rows %s, got %s %s" % (shape, t.dtype, tuple(t.shape))
-    return t.data_ptr(), MOE_TYPE_F32 if dtype is _F32 else MOE_TYPE_BF16, _row_stride(t, shape)
-
-
-def _row_stride(t, shape) -> int:
+    type_, strides = _TYPE.get(t.dtype), t.stride()
+    assert type_ is not None and t.is_cuda and t.shape == shape and strides[1] == 1, \
+        "expected fp32 or bf16 rows %s, got %s %s" % (tuple(shape), t.dtype, tuple(t.shape))
     # (the stride of a single row means nothing: any that is wide and aligned enough will do)
-    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
+    return t.data_ptr(), type_, strides[0] if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
 def _out_rows(t, dtypes, shape):
     """Pointer and row stride of an output of one of these types (None: not wanted)."""
     if t is None:
         return None, 0
-    assert t.is_cuda and t.dtype in dtypes and t.shape == shape and (t.stride(1) == 1 or shape[1] == 1), \
+    strides = t.stride()
+    assert t.dtype in dtypes and t.is_cuda and t.shape == shape and (strides[1] == 1 or shape[1] == 1), \
         "expected %s rows %s, got %s %s" % (dtypes[0], shape, t.dtype, tuple(t.shape))
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
 
 
 def moe_i8_quantize(src, dst: "I8Rows", stream=None):
@@ -585,7 +583,7 @@ class I8Rows:
         assert q.is_cuda and q.dtype == torch.int8 and q.dim() == 2 and q.stride(1) == 1, "q: int8 rows [rows, cols]"
         self.rows, self.cols = self.shape = tuple(q.shape)
         self.q, self.scale = q, scale
-        self.c = moe_i8_rows_t(self.rows, self.cols, _row_stride(q, self.shape), q.data_ptr(), _dense(scale, _F32, (self.rows,)))
+        self.c = moe_i8_rows_t(self.rows, self.cols, q.stride(0) if self.rows > 1 else -(-self.cols // 16) * 16, q.data_ptr(), _dense(scale, _F32, (self.rows,)))
         self.ref = C.byref(self.c)
 
     @classmethod
