@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   constexpr int channels = GATED ? 8 : 16;
   const int blocks = (a.K + 127) / 128, pitch = blocks * 256 + 16;
-  const int per_group = (a.K + kRowStageK - 1) / kRowStageK, mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int per_group = (a.K + kRowStageK - 1) / kRowStageK;
   uint8_t* xs = smem + stages * kRowStage;
 
   bool dead = false;
@@ -48,10 +48,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
       dead = true;
     }
   };
-  // part s of the CTA's gi-th group into a slot
+  // the next part of the CTA's groups into a slot
   const int whole = a.K / 128;
-  auto copy = [&](int gi, int s, int slot) {
-    const int n0 = ((int)blockIdx.x + gi * (int)gridDim.x) * channels;
+  int c_group = blockIdx.x, c_part = 0;
+  auto copy_next = [&](int slot) {
+    const int n0 = c_group * channels, s = c_part;
     const bool main = 8 * s < whole, tail = s == per_group - 1 && whole < blocks;
     uint8_t* to = smem + slot * kRowStage;
     mbar_arrive_expect_tx(bar_full + slot, (main ? 16384 : 0) + (tail ? 2048 : 0));
@@ -63,29 +64,34 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
       tma_load_2d(to + 16384, &tail0, whole * 128, n0, bar_full + slot);
       if (GATED) tma_load_2d(to + 17408, &tail1, whole * 128, n0, bar_full + slot);
     }
+    if (++c_part == per_group) {
+      c_part = 0;
+      c_group += gridDim.x;
+    }
   };
-  const int total = mine * per_group, early = min(stages, total);
+  int issued = 0;                              // stages (of the copying lane)
   if (warp == kRowWarps + kOutWarps) {
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 8); }
     else if (lane >= 30) { mbar_init(bar_sum_full + lane - 30, kRowWarps); mbar_init(bar_sum_empty + lane - 30, kOutWarps); }
     fence_mbar_init();
     __syncwarp();
     if (lane == 0)
-      for (int i = 0; i < early; ++i) copy(i / per_group, i % per_group, i);
+      for (; issued < stages && c_group < groups; ++issued) copy_next(issued);
   } else {
     // ---- the tokens, in convert4's order, zeros past K
     const int pieces = blocks * 8, all = a.T * pieces, threads = (kRowWarps + kOutWarps) * 32;
+    const float per = 1.0f / (float)pieces;                      // (i + 1/2) per is never nearer than 1/2 per to an integer
     for (int i0 = tid; i0 < all; i0 += 4 * threads) {
       uint4 v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e * threads, t = i / pieces, k = (i - t * pieces) * 16;
+        const int i = i0 + e * threads, t = (int)(((float)i + 0.5f) * per), k = (i - t * pieces) * 16;
         v[e] = make_uint4(0, 0, 0, 0);
         if (i < all && k < a.K) v[e] = *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + k);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e * threads, t = i / pieces, k = (i - t * pieces) * 16;
+        const int i = i0 + e * threads, t = (int)(((float)i + 0.5f) * per), k = (i - t * pieces) * 16;
         if (i >= all) break;
         uint32_t h[8];
         convert4(v[e].x, h[0], h[1]);
@@ -99,18 +105,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
     }
   }
   __syncthreads();
+  const int mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;      // groups
 
   if (warp == kRowWarps + kOutWarps) {
     // ================================================================ copies
     if (lane == 0) {
-      int slot = early % stages, phase = early == stages ? 0 : 1;
-      for (int i = early; i < total; ++i) {
+      for (int slot = 0, phase = 0; c_group < groups; ++issued) {          // (the ring is full)
         wait(bar_empty + slot, phase);
-        copy(i / per_group, i % per_group, slot);
+        copy_next(slot);
         if (++slot == stages) { slot = 0; phase ^= 1; }
       }
       dead = false;                            // (where waits have run out, copies may still be in flight)
-      for (int i = max(0, total - stages); i < total; ++i) wait(bar_full + i % stages, (i / stages) & 1);
+      for (int i = max(0, issued - stages); i < issued; ++i) wait(bar_full + i % stages, (i / stages) & 1);
     }
   } else if (warp < kRowWarps) {
     // ================================================================ products: stages i = set, set + 2, ..., 128 codes a warp

@@ -370,20 +370,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   const int first = begin / nk, s_first = begin - first * nk;
 
   // the copies' barriers first: the first stages are on their way while the rest is set up
-  auto copy = [&](int stage, int tile, int k) {
-    const int tn = tile % a.tiles_n, tt = tile / a.tiles_n;
+  const int early = min(stages, total);                    // stages copied before the roles begin
+  int c_s = s_first, c_n = first % a.tiles_n, c_t = first / a.tiles_n;        // the next stage to be copied: of K, of its tile
+  auto copy_next = [&](int stage) {
     uint8_t* to = smem + stage * stage_bytes;
     mbar_arrive_expect_tx(bar_full + stage, stage_bytes);
-    tma_load_2d(to, &map_w0, k * kTileK, tn * (GATED ? 128 : 256), bar_full + stage);
-    if (GATED) tma_load_2d(to + 16384, &map_w1, k * kTileK, tn * 128, bar_full + stage);
-    else tma_load_2d(to + 16384, &map_w0, k * kTileK, tn * 256 + 128, bar_full + stage);
-    tma_load_2d(to + 32768, &map_x, k * kTileK, tt * nt, bar_full + stage);
-  };
-  const int early = min(stages, total);                    // stages copied before the roles begin
-  int c_tile = first, c_s = s_first;                       // the next stage to be copied
-  auto copy_next = [&](int stage) {
-    copy(stage, c_tile, c_s);
-    if (++c_s == nk) { c_s = 0; ++c_tile; }
+    tma_load_2d(to, &map_w0, c_s * kTileK, c_n * (GATED ? 128 : 256), bar_full + stage);
+    if (GATED) tma_load_2d(to + 16384, &map_w1, c_s * kTileK, c_n * 128, bar_full + stage);
+    else tma_load_2d(to + 16384, &map_w0, c_s * kTileK, c_n * 256 + 128, bar_full + stage);
+    tma_load_2d(to + 32768, &map_x, c_s * kTileK, c_t * nt, bar_full + stage);
+    if (++c_s == nk) {
+      c_s = 0;
+      if (++c_n == a.tiles_n) { c_n = 0; ++c_t; }
+    }
   };
   if (warp == 20) {
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 12); }
