@@ -44,9 +44,13 @@ __device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v)
   if (a.yb) a.yb[t * a.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// tcgen05 (i8_tc.cu); arguments checked by the caller. The workspace's header is at a.status, then tc_workspace_bytes.
+// tcgen05 (i8_tc.cu), and a small CTA a tile (i8_tile.cu); arguments checked by the caller. The estimates are nanoseconds; the
+// workspace's header is at a.status, then tc_workspace_bytes.
 size_t tc_workspace_bytes(int K, int T_max);
-moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream);
+double tc_estimate(const MatArgs& a, int sms);
+moe_status_t tc_multiply(const MatArgs& a, int sms, cudaStream_t stream);
+double tile_estimate(const MatArgs& a, int sms);
+moe_status_t tile_multiply(const MatArgs& a, cudaStream_t stream);
 
 // SiLU(g) u in fp32: one exponential (2 units in the last place at the most times |g|'s rounding in its argument), one IEEE
 // reciprocal. g = -inf gives NaN as the formula does; exp(-g) = inf gives the formula's zero.

@@ -1,12 +1,13 @@
 // i8_matmul.cu -- product of 8-bit integers with scales for each token and output channel, and the gated block: the entry points,
-// and the kernel for a few tokens (i8_tc.cu has the one for more).
+// the choice among the kernels, and the kernel for a few tokens (i8_tc.cu: tcgen05, for more; i8_tile.cu: for small products).
 //
-// A few tokens: the weights are read once, and that is all the time there is. One CTA an SM goes through groups of 16 channels;
-// one copy (TMA) brings 1024 codes of each of the 16 rows a stage, as many stages ahead as shared memory holds. (16 copies of a
-// row each took 100 cycles apiece to issue, which held the stream at 3 TB/s.) 16 warps (two sets
-// that take stages in turn, 128 codes a warp) make the codes binary16 (exactly), and mma.sync (m16n8k16) multiplies them with the
-// tokens, which the CTA keeps in shared memory in binary16. fp32 adds 1024 products exactly; then the accumulators are added to
-// integers. Four more warps add the 16 warps' sums and write a group's outputs while the next group is under way.
+// A few tokens (up to 32): the weights are read once, and that is most of the time there is. One CTA an SM goes through groups of
+// 16 channels; one copy (TMA) brings 1024 codes of each of the 16 rows a stage, as many stages ahead as shared memory holds. (16
+// copies of a row each took 100 cycles apiece to issue, which held the stream at 3 TB/s.) 16 warps (two sets that take stages in
+// turn, 128 codes a warp) make the codes binary16 (exactly), and mma.sync (m16n8k16) multiplies them with the tokens, which the CTA
+// keeps in shared memory in binary16. fp32 adds 1024 products exactly; then the accumulators are added to integers. Four more
+// warps add the 16 warps' sums and write a group's outputs while the next group is under way. (1 x 4096 x 4096 6.7 us; 1 x 4096 x
+// 32768 23 us, 5.9 TB/s.)
 // The order of k within a block is the one in which a lane reads its codes: 16 contiguous bytes of two rows.
 // Gated: rows 0-7 of the 16 are gate's, 8-15 up's of the same channels, so that a thread has both.
 #include "i8.cuh"
@@ -15,7 +16,7 @@
 namespace moe {
 namespace i8 {
 
-constexpr int kRowTokens = 8;
+constexpr int kRowTokens = 32;
 constexpr int kRowWarps = 16, kOutWarps = 4, kRowThreads = (kRowWarps + kOutWarps + 1) * 32;
 // A stage: 8 blocks of 128 codes of the 16 rows (gated: gate's 8 blocks of 8 rows, then up's), 128-byte rows, swizzled; then the
 // block that K ends in, if it is not a whole one.
@@ -23,22 +24,23 @@ constexpr int kRowStageK = 1024, kRowStage = 9 * 2048;
 constexpr int kExactStages = 8;               // stages whose products of a warp fp32 adds exactly
 constexpr int kMaxRowStages = 12;
 static_assert(kMaxRowStages % 2 == 0, "slots belong to sets");
-constexpr int kRowSmem = 225 * 1024 - 2 * kRowWarps * 128 * 4;
+constexpr int row_smem(int nt) { return 225 * 1024 - 2 * kRowWarps * 128 * nt * 4; }     // beside the sums of NT tiles of 8 tokens
 
-template <bool GATED>
+// NT: tiles of 8 tokens.
+template <bool GATED, int NT>
 __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int groups, int stages, const __grid_constant__ CUtensorMap map0,
                                                                   const __grid_constant__ CUtensorMap map1,
                                                                   const __grid_constant__ CUtensorMap tail0,
                                                                   const __grid_constant__ CUtensorMap tail1) {
+  __shared__ uint64_t bar_full[kMaxRowStages], bar_empty[kMaxRowStages], bar_sum_full[2], bar_sum_empty[2];
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
-  __shared__ uint64_t bar_full[kMaxRowStages], bar_empty[kMaxRowStages], bar_sum_full[2], bar_sum_empty[2];
-  __shared__ int part[2][kRowWarps][128];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   constexpr int channels = GATED ? 8 : 16;
   const int blocks = (a.K + 127) / 128, pitch = blocks * 256 + 16;
   const int per_group = (a.K + kRowStageK - 1) / kRowStageK;
   uint8_t* xs = smem + stages * kRowStage;
+  int* parts = reinterpret_cast<int*>(xs + (a.T * pitch + 127) / 128 * 128);      // [two groups][warp][8 NT tokens][16]
 
   bool dead = false;
   auto wait = [&](uint64_t* bar, int parity) {
@@ -121,18 +123,25 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
   } else if (warp < kRowWarps) {
     // ================================================================ products: stages i = set, set + 2, ..., 128 codes a warp
     const int g = lane >> 2, c = lane & 3, set = warp >> 3, block = warp & 7;
-    const uint8_t* xr = xs + min(g, a.T - 1) * pitch + c * 32;      // (columns past the last token repeat it and are not used)
+    const uint8_t* xr[NT];                                          // (columns past the last token repeat it and are not used)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xr[t] = xs + min(8 * t + g, a.T - 1) * pitch + c * 32;
     const uint8_t* wr = smem + g * 128;
     int i = set, slot = set % stages, phase = (set / stages) & 1;
     for (int gi = 0; gi < mine; ++gi) {
-      float acc[2][4] = {};
-      int sum[4] = {}, n = 0;
+      constexpr int C = NT == 1 ? 2 : 1;           // chains of products a tile of tokens
+      float acc[C][NT][4] = {};
+      int sum[NT][4] = {}, n = 0;
       auto add = [&]() {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[e] += __float2int_rn(acc[0][e]) + __float2int_rn(acc[1][e]);
-          acc[0][e] = acc[1][e] = 0.f;
-        }
+        for (int k = 0; k < C; ++k)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sum[t][e] += __float2int_rn(acc[k][t][e]);
+              acc[k][t][e] = 0.f;
+            }
       };
       for (; i < (gi + 1) * per_group; i += 2) {
         const int at = (i - gi * per_group) * 8 + block;            // the warp's block of 128
@@ -142,9 +151,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
           const int other = GATED && at < whole ? 8192 : 1024;       // the second eight rows
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint8_t *w = ws + (((4 * h + c) ^ g) << 4), *x = xr + at * 256 + 128 * h;
+            const uint8_t* w = ws + (((4 * h + c) ^ g) << 4);
             const uint4 v0 = *reinterpret_cast<const uint4*>(w), v1 = *reinterpret_cast<const uint4*>(w + other);
-            const uint4 b0 = *reinterpret_cast<const uint4*>(x), b1 = *reinterpret_cast<const uint4*>(x + 16);
             uint32_t w0[8], w1[8];
             convert4(v0.x, w0[0], w0[1]);
             convert4(v1.x, w1[0], w1[1]);
@@ -154,10 +162,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
             convert4(v1.z, w1[4], w1[5]);
             convert4(v0.w, w0[6], w0[7]);
             convert4(v1.w, w1[6], w1[7]);
-            mma_f16(acc[h], w0[0], w1[0], w0[1], w1[1], b0.x, b0.y, acc[h]);
-            mma_f16(acc[h], w0[2], w1[2], w0[3], w1[3], b0.z, b0.w, acc[h]);
-            mma_f16(acc[h], w0[4], w1[4], w0[5], w1[5], b1.x, b1.y, acc[h]);
-            mma_f16(acc[h], w0[6], w1[6], w0[7], w1[7], b1.z, b1.w, acc[h]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint8_t* x = xr[t] + at * 256 + 128 * h;
+              const uint4 b0 = *reinterpret_cast<const uint4*>(x), b1 = *reinterpret_cast<const uint4*>(x + 16);
+              float(&d)[4] = acc[h % C][t];
+              mma_f16(d, w0[0], w1[0], w0[1], w1[1], b0.x, b0.y, d);
+              mma_f16(d, w0[2], w1[2], w0[3], w1[3], b0.z, b0.w, d);
+              mma_f16(d, w0[4], w1[4], w0[5], w1[5], b1.x, b1.y, d);
+              mma_f16(d, w0[6], w1[6], w0[7], w1[7], b1.z, b1.w, d);
+            }
           }
         }
         __syncwarp();
@@ -169,57 +183,84 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
       add();
       const int buf = gi & 1;
       wait(bar_sum_empty + buf, ((gi >> 1) & 1) ^ 1);
+      int* part = parts + (buf * kRowWarps + warp) * (128 * NT) + g;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) part[buf][warp][(2 * c + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[e];
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[(8 * t + 2 * c + (e & 1)) * 16 + 8 * (e >> 1)] = sum[t][e];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sum_full + buf);
     }
   } else {
-    // ================================================================ sums of the warps, outputs: channel r, token t
+    // ================================================================ sums of the warps, outputs: channel r, tokens t, t + 8, ...
     const int id = tid - kRowWarps * 32, r = id & 15, t = id >> 4, up = GATED ? r >> 3 : 0;
-    const float scale = a.xs[min(t, a.T - 1)];
+    float scale[NT];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) scale[k] = a.xs[min(8 * k + t, a.T - 1)];
     for (int gi = 0; gi < mine; ++gi) {
       const int n = ((int)blockIdx.x + gi * (int)gridDim.x) * channels + (GATED ? r & 7 : r), buf = gi & 1;
       const float ws = a.ws[up][min(n, a.N - 1)];
       wait(bar_sum_full + buf, (gi >> 1) & 1);
-      int s = 0;
+      int s[NT] = {};
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) s += part[buf][w][id];
+      for (int w = 0; w < kRowWarps; ++w)
+#pragma unroll
+        for (int k = 0; k < NT; ++k) s[k] += parts[(buf * kRowWarps + w) * (128 * NT) + 128 * k + id];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sum_empty + buf);
-      float v = product(s, scale, ws);
-      if (GATED) v = silu_mul(v, __shfl_down_sync(0xFFFFFFFFu, v, 8));
-      if (t < a.T && n < a.N && r < channels) put(a, t, n, v);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        float v = product(s[k], scale[k], ws);
+        if (GATED) v = silu_mul(v, __shfl_down_sync(0xFFFFFFFFu, v, 8));
+        if (8 * k + t < a.T && n < a.N && r < channels) put(a, 8 * k + t, n, v);
+      }
     }
   }
 }
 
-// Stages that fit beside the tokens; below 4 the tensor cores' kernel is faster. An even number, so that a slot always belongs to the
-// same set of warps: a set that waited for a slot's next use before the other set's copy into it had landed would take that wait
-// for done (a barrier's parity tells only neighbouring phases apart).
+// Stages that fit beside the tokens (0: fewer than 4). An even number, so that a slot always belongs to the same set of warps: a set
+// that waited for a slot's next use before the other set's copy into it had landed would take that wait for done (a barrier's
+// parity tells only neighbouring phases apart).
+static int rows_tiles(int T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+static int tokens_bytes(int T, int K) { return (T * ((K + 127) / 128 * 256 + 16) + 127) / 128 * 128; }
 static int rows_stages(int T, int K) {
   if (T > kRowTokens) return 0;
-  const int left = kRowSmem - 1024 - T * ((K + 127) / 128 * 256 + 16), n = left < 0 ? 0 : left / kRowStage;
+  const int left = row_smem(rows_tiles(T)) - 1024 - tokens_bytes(T, K), n = left < 0 ? 0 : left / kRowStage;
   return n < 4 ? 0 : n < kMaxRowStages ? n & ~1 : kMaxRowStages;
 }
-static moe_status_t rows_multiply(const MatArgs& a, int stages, cudaStream_t stream) {
-  static int configured[64] = {0};
+// Nanoseconds: the tokens' way into shared memory, then a CTA's groups of channels, a stage 0.375 us with up to 8 tokens (0.5 with 16,
+// 0.8 with 32), a group of one stage twice that; or the weights at 6.5 TB/s. (8 x 4096 x 32768 24.6 us, small_kernel 26.7; 12 x 4096 x
+// 32768 30.3 and 26.6; 16 x 2048 x 4096 5.8 and 7.5; 20 x 4096 x 512 8.2 both; 30 x 1024 x 32768 23 and 12.)
+static double rows_estimate(const MatArgs& a, int sms) {
+  if (!rows_stages(a.T, a.K)) return 1e30;
+  const int nt = rows_tiles(a.T), channels = a.w[1] ? 8 : 16, groups = (a.N + channels - 1) / channels;
+  const double stage = nt == 1 ? 375 : nt == 2 ? 500 : 800, group = nt == 1 ? 780 : nt == 2 ? 900 : 1500;
+  const double part = (a.K + kRowStageK - 1) / kRowStageK * stage, work = (groups + sms - 1) / sms * (part > group ? part : group);
+  const double memory = (double)a.N * a.K * (a.w[1] ? 2 : 1) / 6500;
+  return 2600 + (double)a.T * a.K / 40 + (work > memory ? work : memory);
+}
+template <bool GATED, int NT>
+static cudaError_t launch_rows(const MatArgs& a, int ctas, int groups, int stages, const CUtensorMap (&map)[2], const CUtensorMap (&tail)[2],
+                               cudaStream_t stream) {
+  static bool ready[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  if (!configured[dev]) {
-    if (cudaFuncSetAttribute(rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem) != cudaSuccess) {
-      cudaGetLastError();
-      return MOE_ERR_CUDA;
-    }
-    configured[dev] = 1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(rows_kernel<GATED, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
   }
-  const int sms = moe_internal::num_sms();
-  if (sms <= 0) return MOE_ERR_CUDA;
+  const int smem = 1024 + stages * kRowStage + tokens_bytes(a.T, a.K) + 2 * kRowWarps * 128 * NT * 4;
+  rows_kernel<GATED, NT><<<ctas, kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
+  return cudaGetLastError();
+}
+static moe_status_t rows_multiply(const MatArgs& a, int sms, cudaStream_t stream) {
+  const int stages = rows_stages(a.T, a.K);
   // (Groups of fewer channels, which would share N more evenly among the SMs, were slower: copies of 9 to 15 rows, 1 x 4096 x 32768
   // 28 us against 23, 1 x 4096 x 4096 with 14 rows 7.7 against 7.1.)
   const int channels = a.w[1] ? 8 : 16, groups = (a.N + channels - 1) / channels;
-  const int smem = 1024 + stages * kRowStage + a.T * ((a.K + 127) / 128 * 256 + 16), whole = a.K / 128;
+  const int whole = a.K / 128;
   CUtensorMap map[2], tail[2];
   for (int i = 0; i < 2; ++i) {
     const int m = a.w[1] ? i : 0;
@@ -230,9 +271,12 @@ static moe_status_t rows_multiply(const MatArgs& a, int stages, cudaStream_t str
     map[i] = tail[i];
     if (whole > 0 && !moe_internal::tmap_u8(&map[i], a.w[m], 3, dims, strides, box)) return MOE_ERR_CUDA;
   }
-  if (a.w[1]) rows_kernel<true><<<min(groups, sms), kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
-  else rows_kernel<false><<<min(groups, sms), kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int nt = rows_tiles(a.T), ctas = min(groups, sms);
+  auto* launch = a.w[1] ? (nt == 1 ? launch_rows<true, 1> : nt == 2 ? launch_rows<true, 2> : launch_rows<true, 4>)
+                        : (nt == 1 ? launch_rows<false, 1> : nt == 2 ? launch_rows<false, 2> : launch_rows<false, 4>);
+  if (launch(a, ctas, groups, stages, map, tail, stream) == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
 }
 
 static bool out_ok(const void* p, int64_t stride, int64_t cols, int size) {
@@ -255,8 +299,12 @@ static moe_status_t multiply(const moe_i8_rows_t* x, const moe_i8_rows_t* w, con
   if (st != MOE_OK) return st;
   MatArgs a{x->q, {w->q, w2 ? w2->q : nullptr}, x->scale, {w->scale, w2 ? w2->scale : nullptr}, base, y, (uint16_t*)y_bf16,
             x->stride, {w->stride, w2 ? w2->stride : 0}, base_stride, y_stride, yb_stride, x->rows, w->rows, x->cols, (int32_t*)ws};
-  const int stages = rows_stages(a.T, a.K);
-  return stages ? rows_multiply(a, stages, (cudaStream_t)stream) : tc_multiply(a, (cudaStream_t)stream);
+  // the fastest way by the ways' own estimates
+  const int sms = moe_internal::num_sms();
+  if (sms <= 1) return MOE_ERR_CUDA;
+  const double rows = rows_estimate(a, sms), tile = tile_estimate(a, sms), tc = tc_estimate(a, sms);
+  if (rows <= tile && rows <= tc) return rows_multiply(a, sms, (cudaStream_t)stream);
+  return tile < tc ? tile_multiply(a, (cudaStream_t)stream) : tc_multiply(a, sms, (cudaStream_t)stream);
 }
 
 }  // namespace i8
@@ -267,7 +315,7 @@ using namespace moe::i8;
 
 extern "C" size_t moe_i8_workspace_bytes(const moe_i8_rows_t* w, int32_t T_max) {
   if (check_rows(w) != MOE_OK || T_max < 1 || T_max > kMaxRows) return 0;
-  return sizeof(WsHeader) + (rows_stages(T_max, w->cols) ? 0 : tc_workspace_bytes(w->cols, T_max));   // (rows_kernel needs none)
+  return sizeof(WsHeader) + tc_workspace_bytes(w->cols, T_max);
 }
 
 extern "C" moe_status_t moe_i8_matmul(const moe_i8_rows_t* x, const moe_i8_rows_t* w, const float* base, int64_t base_stride,

@@ -19,7 +19,7 @@
 // integers, and a second launch adds them up and writes the outputs. (A cluster a tile, its parts exchanged through
 // distributed shared memory, took 29 us for gated 48 x 4096 x 11008: 86 tiles leave 66 SMs idle, and the exchange runs at 20
 // bytes a cycle; adding to the workspace with atomics runs at 9; and the last of a tile's CTAs adding up all parts took 50 us
-// for gated 64 x 4096 x 4096, where all SMs together take @@.)
+// for gated 64 x 4096 x 4096, where the second launch takes 15.8 in all.)
 // pair_kernel: two CTAs (cta_group::2) have 256 channels (128 each; gated: 64 of gate and 64 of up each) and up to 256 tokens (two
 // halves); each converts its own channels and half of the tokens, which halves the conversions and the reads of X.
 #include "i8.cuh"
@@ -562,31 +562,37 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
       : "memory");
 }
 // X for pair_kernel: rows of binary16 values (`pieces` of 16: K rounded up to 64), in convert4's order, zeros past K; and each row's sum of
-// squares (below 2^31). One row a CTA at a time.
+// squares (below 2^31). A warp a row.
 __global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, int pieces, uint8_t* out,
                                                     uint32_t* squares) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // (pair_kernel may set itself up meanwhile)
-  __shared__ uint32_t part[4];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 4) {
     uint32_t sq = 0;
-    for (int k = threadIdx.x; k < pieces; k += 128) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (16 * k < K) v = __ldg(reinterpret_cast<const uint4*>(x + row * stride) + k);
-      sq = (uint32_t)__dp4a((int)v.x, (int)v.x, __dp4a((int)v.y, (int)v.y, __dp4a((int)v.z, (int)v.z, __dp4a((int)v.w, (int)v.w, (int)sq))));
-      uint32_t h[8];
-      convert4(v.x, h[0], h[1]);
-      convert4(v.y, h[2], h[3]);
-      convert4(v.z, h[4], h[5]);
-      convert4(v.w, h[6], h[7]);
-      uint4* to = reinterpret_cast<uint4*>(out) + (row * pieces + k) * 2;
-      to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    for (int k0 = lane; k0 < pieces; k0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (16 * (k0 + 32 * j) < K) v[j] = __ldg(reinterpret_cast<const uint4*>(x + row * stride) + k0 + 32 * j);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + 32 * j;
+        if (k >= pieces) break;
+        sq = (uint32_t)__dp4a((int)v[j].x, (int)v[j].x, __dp4a((int)v[j].y, (int)v[j].y, __dp4a((int)v[j].z, (int)v[j].z, __dp4a((int)v[j].w, (int)v[j].w, (int)sq))));
+        uint32_t h[8];
+        convert4(v[j].x, h[0], h[1]);
+        convert4(v[j].y, h[2], h[3]);
+        convert4(v[j].z, h[4], h[5]);
+        convert4(v[j].w, h[6], h[7]);
+        uint4* to = reinterpret_cast<uint4*>(out) + (row * pieces + k) * 2;
+        to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
     }
     sq = __reduce_add_sync(0xFFFFFFFFu, sq);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sq;
-    __syncthreads();
-    if (threadIdx.x == 0) squares[row] = part[0] + part[1] + part[2] + part[3];
-    __syncthreads();
+    if (lane == 0) squares[row] = sq;
   }
 }
 
@@ -769,23 +775,23 @@ struct TcPlan {
   int pair;               // 0, or pair_kernel's TOKENS
   int nt, tiles_n, tiles, stages, ctas, grain, share, extra;
   uint32_t smem;
+  double ns;
 };
 
-// small_kernel: a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3 TB/s. A second
+// small_kernel: 3.5 us; a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3 TB/s. A second
 // launch that adds up `ctas` parts of nt tokens takes 0.5 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x
 // 4096 (16 tiles): 28.2 us a tile a CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6;
 // 16 x 4096 x 32768 (128 tiles): 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
-// pair_kernel: 1.2 us more than small_kernel to begin with; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token,
+// pair_kernel: 7.5 us with the widening; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token,
 // or with all SMs at it 2.5 ns a token (the products). (201 x 4096 x 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one
 // warpgroup that converts, 24.5 with 256.)
 static TcPlan plan(const MatArgs& a, bool gated, int sms) {
   TcPlan best{};
-  double least = 0;
   const int tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
   auto consider = [&](const TcPlan& p, double ns) {
-    if (least == 0 || ns < least) {
-      least = ns;
+    if (best.ns == 0 || ns < best.ns) {
       best = p;
+      best.ns = ns;
     }
   };
   if (a.T <= 2 * kSmallTokens) {
@@ -803,7 +809,7 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
     p.grain = nk;
     p.share = p.tiles / p.ctas;
     p.extra = p.tiles % p.ctas;
-    consider(p, time((p.tiles + p.ctas - 1) / p.ctas * nk));
+    consider(p, 3500 + time((p.tiles + p.ctas - 1) / p.ctas * nk));
     p.grain = 1;
     for (int m = 1; m <= most / p.tiles + 1; ++m) {           // m CTAs a tile, and all there are
       p.ctas = min(all, m <= most / p.tiles ? m * p.tiles : most);
@@ -811,7 +817,7 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
       p.extra = all % p.ctas;
       const double parts = (p.ctas + p.tiles - 1) / p.tiles;
       if (p.ctas > p.tiles || m > most / p.tiles)
-        consider(p, time((all + p.ctas - 1) / p.ctas) + 500 + 340 * (parts + (p.ctas % p.tiles ? 1 : 0)) + 0.73 * p.ctas * p.nt);
+        consider(p, 4000 + time((all + p.ctas - 1) / p.ctas) + 340 * (parts + (p.ctas % p.tiles ? 1 : 0)) + 0.73 * p.ctas * p.nt);
     }
   }
   if (a.T > kSmallTokens) {
@@ -826,7 +832,7 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
       p.ctas = 2 * min(p.tiles, pairs);
       const int waves = (p.tiles + pairs - 1) / pairs;
       const double alone = p.pair == 128 ? 370 : 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
-      consider(p, 1200 + (double)waves * nk * (alone > full ? alone : full));
+      consider(p, 7500 + (double)waves * nk * (alone > full ? alone : full));
     }
   }
   return best;
@@ -871,12 +877,12 @@ size_t tc_workspace_bytes(int K, int T_max) {
   return parts > wide ? parts : wide;
 }
 
-moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
+double tc_estimate(const MatArgs& a, int sms) { return plan(a, a.w[1] != nullptr, sms).ns; }
+
+moe_status_t tc_multiply(const MatArgs& a, int sms, cudaStream_t stream) {
   const bool gated = a.w[1] != nullptr;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(dev)) { cudaGetLastError(); return MOE_ERR_CUDA; }
-  const int sms = moe_internal::num_sms();
-  if (sms <= 1) return MOE_ERR_CUDA;
   const TcPlan p = plan(a, gated, sms);
   CUtensorMap mx, m0, m1;
   const int box_w = p.pair && gated ? 64 : 128;
@@ -900,7 +906,7 @@ moe_status_t tc_multiply(const MatArgs& a, cudaStream_t stream) {
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    widen_kernel<<<min(a.T, sms * 16), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
+    widen_kernel<<<min((a.T + 3) / 4, sms * 16), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;

@@ -1,0 +1,180 @@
+// i8_tile.cu -- product of 8-bit integers (and the gated block) where there is little to do: one small CTA a tile.
+//
+// tcgen05 takes its time to begin (columns of TMEM, barriers, tensor maps, tokens widened by another launch): 6 to 10 us however
+// small the product. Here a CTA of 8 warps has a tile of 64 tokens and 64 channels (gated: 32 of gate, 32 of up) and goes through K 128
+// at a time, six such blocks ahead (cp.async). Four warps have the first 64 of each block, four the others; a warp makes the codes of 32
+// tokens and 32 channels (gated: 16 of gate and the same 16 of up, so that a thread has both) binary16 (exactly) in registers, each lane
+// 16 contiguous ones of its rows, and multiplies them with mma.sync (m16n8k16, tokens as rows). fp32 adds 1024 products
+// exactly; then the accumulators are added to integers. At the end the halves' sums are added up through shared memory.
+#include "i8.cuh"
+
+namespace moe {
+namespace i8 {
+
+constexpr int kTileThreads = 256, kTileStages = 6, kTileStage = 128 * 128;     // rows of tokens and channels, codes
+constexpr int kExactBlocks = 16;                     // blocks of 64 that fp32 adds exactly
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");   // (zeros if not in)
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Where 16-byte unit u of a row is: eight lanes that read four units of two neighbouring rows meet no bank twice
+__device__ __forceinline__ int unit_of(int row, int u) { return u ^ (row & 1) * 4 ^ (row >> 1 & 3); }
+
+template <bool GATED>
+__global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, set = warp >> 2, g = lane >> 2, c = lane & 3;
+  const int n0 = blockIdx.x * (GATED ? 32 : 64);
+  const int64_t t0 = (int64_t)blockIdx.y * 64;
+  const int blocks = (a.K + 127) / 128;
+  const uint32_t base = smem_u32(smem);
+
+  // ---- copies: a thread has unit tid % 8 of rows tid / 8 + 32 j: j = 0, 1 tokens, 2, 3 channels
+  const int cu = tid & 7, cr = tid >> 3;
+  const int8_t* from[4];
+  uint32_t to[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = cr + 32 * (j & 1);
+    if (j < 2) {
+      from[j] = a.x + min(t0 + row, (int64_t)a.T - 1) * a.x_stride + 16 * cu;
+    } else {
+      const int up = GATED ? row >> 4 & 1 : 0, n = min(n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row), a.N - 1);
+      from[j] = a.w[up] + n * a.w_stride[up] + 16 * cu;
+    }
+    to[j] = base + (cr + 32 * j) * 128 + unit_of(cr, cu) * 16;      // (32 rows on the place in a row is the same)
+  }
+  int next = 0, next_slot = 0;
+  auto copy_next = [&]() {
+    if (next < blocks) {
+      const bool in = next * 128 + 16 * cu < a.K;                    // (K is a multiple of 16)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) copy16(to[j] + next_slot * kTileStage, in ? from[j] + next * 128 : from[j], in);
+    }
+    copies_done();
+    ++next;
+    if (++next_slot == kTileStages) next_slot = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < kTileStages - 1; ++i) copy_next();
+
+  // ---- products: the warp's tokens wt .. + 31 and channel rows wn .. + 31
+  const int wt = (warp & 1) * 32, wn = 64 + (warp >> 1 & 1) * 32;
+  // the scales of the lane's outputs: set 0 finishes the warps' first 16 tokens, set 1 the others
+  float xs[2], ws[4][2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) xs[half] = __ldg(a.xs + min(t0 + wt + 16 * set + g + 8 * half, (int64_t)a.T - 1));
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      ws[j][e] = __ldg(a.ws[GATED ? j >> 1 : 0] + min(n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * (GATED ? j & 1 : j) + 2 * c + e, a.N - 1));
+  const uint32_t mine = unit_of(g, 4 * set + c) * 16;                // (eight rows on the same, but for bits 1, 2 of the row: see below)
+  float acc[2][4][4] = {};
+  int sum[2][4][4] = {};
+  auto add = [&]() {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[m][j][e] += __float2int_rn(acc[m][j][e]);
+          acc[m][j][e] = 0.f;
+        }
+  };
+  int slot = 0;
+  for (int i = 0; i < blocks; ++i) {
+    copies_wait<kTileStages - 2>();
+    __syncthreads();                       // block i is there for all, and all are through with block i - 1, whose slot is filled now
+    copy_next();
+    const uint8_t* st = smem + slot * kTileStage;
+    uint32_t x[4][8];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(st + (wt + 8 * r + g) * 128 + mine);
+      convert4(v.x, x[r][0], x[r][1]);
+      convert4(v.y, x[r][2], x[r][3]);
+      convert4(v.z, x[r][4], x[r][5]);
+      convert4(v.w, x[r][6], x[r][7]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 v = *reinterpret_cast<const uint4*>(st + (wn + 8 * j + g) * 128 + mine);
+      uint32_t w[8];
+      convert4(v.x, w[0], w[1]);
+      convert4(v.y, w[2], w[3]);
+      convert4(v.z, w[4], w[5]);
+      convert4(v.w, w[6], w[7]);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          mma_f16(acc[m][j], x[2 * m][2 * s], x[2 * m + 1][2 * s], x[2 * m][2 * s + 1], x[2 * m + 1][2 * s + 1], w[2 * s], w[2 * s + 1],
+                  acc[m][j]);
+    }
+    if (++slot == kTileStages) slot = 0;
+    if (i % kExactBlocks == kExactBlocks - 1) add();
+  }
+  add();
+
+  // ---- outputs
+  copies_wait<0>();
+  __syncthreads();
+  int* part = reinterpret_cast<int*>(smem) + (warp & 3) * 1024 + lane;          // [set that needs it][16][warp of a set][32 lanes]
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[(1 - set) * 512 + (4 * j + e) * 32] = set == 0 ? sum[1][j][e] : sum[0][j][e];
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int64_t tok = t0 + wt + 16 * set + g + 8 * half;
+    if (tok >= a.T) continue;
+    auto at = [&](int j, int e) { return (set == 0 ? sum[0][j][2 * half + e] : sum[1][j][2 * half + e]) + part[set * 512 + (4 * j + 2 * half + e) * 32]; };
+#pragma unroll
+    for (int j = 0; j < (GATED ? 2 : 4); ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ch = n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * j + 2 * c + e;
+        if (ch >= a.N) continue;
+        const float p = product(at(j, e), xs[half], ws[j][e]);
+        put(a, tok, ch, GATED ? silu_mul(p, product(at(GATED ? 2 + j : j, e), xs[half], ws[GATED ? 2 + j : j][e])) : p);
+      }
+  }
+}
+
+// 3.4 us, 0.64 a block and wave of tiles (mma.sync multiplies 512 pairs a cycle and SM), and the weights at 4 TB/s, which so few copies in
+// flight do not hide. (1000 x 512 x 512 6.4 us, tcgen05 10.3; 2000 x 128 x 128 4.3 and 10.5; 300 x 2048 x 2048 22 and 14; 32 x 1024 x
+// 8192 11.1 and 10.0.)
+double tile_estimate(const MatArgs& a, int sms) {
+  if ((a.T + 63) / 64 > 65535) return 1e30;            // (the grid's second dimension)
+  const int channels = a.w[1] ? 32 : 64;
+  const int64_t tiles = (int64_t)((a.N + channels - 1) / channels) * ((a.T + 63) / 64);
+  return 3000 + (double)((tiles + sms - 1) / sms) * ((a.K + 127) / 128 * 640 + 400) +
+         (double)a.N * a.K * (a.w[1] ? 2 : 1) / 4000;
+}
+
+moe_status_t tile_multiply(const MatArgs& a, cudaStream_t stream) {
+  static int configured[64] = {0};
+  int dev = 0;
+  const int smem = kTileStages * kTileStage;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(tile_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(tile_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    configured[dev] = 1;
+  }
+  const dim3 grid((a.N + (a.w[1] ? 31 : 63)) / (a.w[1] ? 32 : 64), (a.T + 63) / 64);
+  if (a.w[1]) tile_kernel<true><<<grid, kTileThreads, smem, stream>>>(a);
+  else tile_kernel<false><<<grid, kTileThreads, smem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace i8
+}  // namespace moe
