@@ -47,8 +47,14 @@ __device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v)
 // tcgen05 (i8_tc.cu), and a small CTA a tile (i8_tile.cu); arguments checked by the caller. The estimates are nanoseconds; the
 // workspace's header is at a.status, then tc_workspace_bytes.
 size_t tc_workspace_bytes(int K, int T_max);
-double tc_estimate(const MatArgs& a, int sms);
-moe_status_t tc_multiply(const MatArgs& a, int sms, cudaStream_t stream);
+struct TcPlan {           // which of tcgen05's kernels, and how the work is cut (see i8_tc.cu's TcArgs)
+  int pair;               // 0: small_kernel; else pair_kernel's TOKENS
+  int nt, tiles_n, tiles, stages, ctas, grain, share, extra;
+  uint32_t smem;
+  double ns;              // estimated
+};
+TcPlan tc_plan(const MatArgs& a, int sms);
+moe_status_t tc_multiply(const MatArgs& a, const TcPlan& p, cudaStream_t stream);
 double tile_estimate(const MatArgs& a, int sms);
 moe_status_t tile_multiply(const MatArgs& a, cudaStream_t stream);
 

@@ -229,15 +229,15 @@ static int rows_stages(int T, int K) {
   return n < 4 ? 0 : n < kMaxRowStages ? n & ~1 : kMaxRowStages;
 }
 // Nanoseconds: the tokens' way into shared memory, then a CTA's groups of channels, a stage 0.375 us with up to 8 tokens (0.5 with 16,
-// 0.8 with 32), a group of one stage twice that; or the weights at 6.5 TB/s. (8 x 4096 x 32768 24.6 us, small_kernel 26.7; 12 x 4096 x
+// 0.8 with 32), a group of one stage up to twice that; or the weights at 6.5 TB/s. (8 x 4096 x 32768 24.6 us, small_kernel 26.7; 12 x 4096 x
 // 32768 30.3 and 26.6; 16 x 2048 x 4096 5.8 and 7.5; 20 x 4096 x 512 8.2 both; 30 x 1024 x 32768 23 and 12.)
 static double rows_estimate(const MatArgs& a, int sms) {
   if (!rows_stages(a.T, a.K)) return 1e30;
   const int nt = rows_tiles(a.T), channels = a.w[1] ? 8 : 16, groups = (a.N + channels - 1) / channels;
-  const double stage = nt == 1 ? 375 : nt == 2 ? 500 : 800, group = nt == 1 ? 780 : nt == 2 ? 900 : 1500;
+  const double stage = nt == 1 ? 375 : nt == 2 ? 500 : 800, group = (nt == 1 ? 450 : nt == 2 ? 800 : 1050) + 0.32 * min(a.K, kRowStageK);
   const double part = (a.K + kRowStageK - 1) / kRowStageK * stage, work = (groups + sms - 1) / sms * (part > group ? part : group);
   const double memory = (double)a.N * a.K * (a.w[1] ? 2 : 1) / 6500;
-  return 2600 + (double)a.T * a.K / 40 + (work > memory ? work : memory);
+  return 2600 + (nt == 4 ? 400 : 0) + (double)a.T * a.K / 40 + (work > memory ? work : memory);
 }
 template <bool GATED, int NT>
 static cudaError_t launch_rows(const MatArgs& a, int ctas, int groups, int stages, const CUtensorMap (&map)[2], const CUtensorMap (&tail)[2],
@@ -302,9 +302,10 @@ static moe_status_t multiply(const moe_i8_rows_t* x, const moe_i8_rows_t* w, con
   // the fastest way by the ways' own estimates
   const int sms = moe_internal::num_sms();
   if (sms <= 1) return MOE_ERR_CUDA;
-  const double rows = rows_estimate(a, sms), tile = tile_estimate(a, sms), tc = tc_estimate(a, sms);
-  if (rows <= tile && rows <= tc) return rows_multiply(a, sms, (cudaStream_t)stream);
-  return tile < tc ? tile_multiply(a, (cudaStream_t)stream) : tc_multiply(a, sms, (cudaStream_t)stream);
+  const double rows = rows_estimate(a, sms), tile = tile_estimate(a, sms);
+  const TcPlan tc = tc_plan(a, sms);
+  if (rows <= tile && rows <= tc.ns) return rows_multiply(a, sms, (cudaStream_t)stream);
+  return tile < tc.ns ? tile_multiply(a, (cudaStream_t)stream) : tc_multiply(a, tc, (cudaStream_t)stream);
 }
 
 }  // namespace i8

@@ -770,22 +770,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
   }
 }
 
-// Which kernel, and how the work is cut
-struct TcPlan {
-  int pair;               // 0, or pair_kernel's TOKENS
-  int nt, tiles_n, tiles, stages, ctas, grain, share, extra;
-  uint32_t smem;
-  double ns;
-};
-
-// small_kernel: 3.5 us; a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3 TB/s. A second
-// launch that adds up `ctas` parts of nt tokens takes 0.5 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x
-// 4096 (16 tiles): 28.2 us a tile a CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6;
-// 16 x 4096 x 32768 (128 tiles): 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
-// pair_kernel: 7.5 us with the widening; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token,
-// or with all SMs at it 2.5 ns a token (the products). (201 x 4096 x 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one
-// warpgroup that converts, 24.5 with 256.)
-static TcPlan plan(const MatArgs& a, bool gated, int sms) {
+// Nanoseconds. small_kernel: 3.2 us; a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3
+// TB/s; a tile's outputs take 55 ns a token, or 80 beside the next tile's stages. A second launch that adds up `ctas` parts of nt tokens
+// takes instead 0.8 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x 4096 (16 tiles): 28.2 us a tile a
+// CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6; 16 x 4096 x 32768 (128 tiles):
+// 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
+// pair_kernel: 3.5 us and the widening; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token, or with all SMs at
+// it 2.5 ns a token (the products); a tile's outputs 39 ns a token (gated 53), beside the next tile's stages. (201 x 4096 x
+// 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one warpgroup that converts, 24.5 with 256.)
+// More than 64 tokens: 154 x 7264 x 584 13.3 us by small_kernel, whose CTAs share tiles, and 30.7 by pair_kernel; 767 x 1936 x 226
+// gated 10.1 and 16.0; 68 x 2224 x 9507 18.1 and 15.1; 294 x 4032 x 8863 43 and 27.
+TcPlan tc_plan(const MatArgs& a, int sms) {
+  const bool gated = a.w[1] != nullptr;
   TcPlan best{};
   const int tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
   auto consider = [&](const TcPlan& p, double ns) {
@@ -794,7 +790,7 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
       best.ns = ns;
     }
   };
-  if (a.T <= 2 * kSmallTokens) {
+  if (a.T <= 16 * kSmallTokens) {
     TcPlan p{};
     const int tiles_t = (a.T + kSmallTokens - 1) / kSmallTokens, most = min(sms, kMaxCtas);
     p.nt = ((a.T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
@@ -805,11 +801,13 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
     p.smem = 1024 + rest + p.stages * stage;
     const double stage_ns = 530 + 4 * p.nt, memory = (double)tiles_n * 256 * a.K / 6300;
     auto time = [&](int stages) { return stages * stage_ns > memory ? stages * stage_ns : memory; };
+    const double out = 55 * p.nt, more = 80 * p.nt;
     p.ctas = min(p.tiles, most);
     p.grain = nk;
     p.share = p.tiles / p.ctas;
     p.extra = p.tiles % p.ctas;
-    consider(p, 3500 + time((p.tiles + p.ctas - 1) / p.ctas * nk));
+    const int waves = (p.tiles + p.ctas - 1) / p.ctas;
+    consider(p, 3200 + out + (time(waves * nk) > (waves - 1) * more ? time(waves * nk) : (waves - 1) * more));
     p.grain = 1;
     for (int m = 1; m <= most / p.tiles + 1; ++m) {           // m CTAs a tile, and all there are
       p.ctas = min(all, m <= most / p.tiles ? m * p.tiles : most);
@@ -832,7 +830,8 @@ static TcPlan plan(const MatArgs& a, bool gated, int sms) {
       p.ctas = 2 * min(p.tiles, pairs);
       const int waves = (p.tiles + pairs - 1) / pairs;
       const double alone = p.pair == 128 ? 370 : 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
-      consider(p, 7500 + (double)waves * nk * (alone > full ? alone : full));
+      const double products = nk * (alone > full ? alone : full), out = (gated ? 53 : 39) * nt;
+      consider(p, 3500 + 6e-4 * a.T * a.K + (products > out ? waves * products + out : products + waves * out));
     }
   }
   return best;
@@ -877,13 +876,10 @@ size_t tc_workspace_bytes(int K, int T_max) {
   return parts > wide ? parts : wide;
 }
 
-double tc_estimate(const MatArgs& a, int sms) { return plan(a, a.w[1] != nullptr, sms).ns; }
-
-moe_status_t tc_multiply(const MatArgs& a, int sms, cudaStream_t stream) {
+moe_status_t tc_multiply(const MatArgs& a, const TcPlan& p, cudaStream_t stream) {
   const bool gated = a.w[1] != nullptr;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(dev)) { cudaGetLastError(); return MOE_ERR_CUDA; }
-  const TcPlan p = plan(a, gated, sms);
   CUtensorMap mx, m0, m1;
   const int box_w = p.pair && gated ? 64 : 128;
   const int pieces = (a.K + 63) / 64 * 4;
@@ -906,7 +902,7 @@ moe_status_t tc_multiply(const MatArgs& a, int sms, cudaStream_t stream) {
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    widen_kernel<<<min((a.T + 3) / 4, sms * 16), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
+    widen_kernel<<<min((a.T + 3) / 4, 2048), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;

@@ -4,15 +4,16 @@
 // small the product. Here a CTA of 8 warps has a tile of 64 tokens and 64 channels (gated: 32 of gate, 32 of up) and goes through K 128
 // at a time, six such blocks ahead (cp.async). Four warps have the first 64 of each block, four the others; a warp makes the codes of 32
 // tokens and 32 channels (gated: 16 of gate and the same 16 of up, so that a thread has both) binary16 (exactly) in registers, each lane
-// 16 contiguous ones of its rows, and multiplies them with mma.sync (m16n8k16, tokens as rows). fp32 adds 1024 products
-// exactly; then the accumulators are added to integers. At the end the halves' sums are added up through shared memory.
+// 16 contiguous ones of its rows, and multiplies them with mma.sync (m16n8k16, tokens as rows). fp32 adds 1024 products exactly, and
+// that is the longest half there is (K up to 2048: beyond it tcgen05 is faster). At the end the halves' sums are added up as
+// integers, through shared memory.
 #include "i8.cuh"
 
 namespace moe {
 namespace i8 {
 
 constexpr int kTileThreads = 256, kTileStages = 6, kTileStage = 128 * 128;     // rows of tokens and channels, codes
-constexpr int kExactBlocks = 16;                     // blocks of 64 that fp32 adds exactly
+constexpr int kMaxTileK = 2048;                      // a half's products, 1024, are added exactly by fp32
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");   // (zeros if not in)
@@ -71,20 +72,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       ws[j][e] = __ldg(a.ws[GATED ? j >> 1 : 0] + min(n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * (GATED ? j & 1 : j) + 2 * c + e, a.N - 1));
-  const uint32_t mine = unit_of(g, 4 * set + c) * 16;                // (eight rows on the same, but for bits 1, 2 of the row: see below)
+  const uint32_t mine = unit_of(g, 4 * set + c) * 16;                // (the same in each eighth row)
   float acc[2][4][4] = {};
-  int sum[2][4][4] = {};
-  auto add = [&]() {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[m][j][e] += __float2int_rn(acc[m][j][e]);
-          acc[m][j][e] = 0.f;
-        }
-  };
   int slot = 0;
   for (int i = 0; i < blocks; ++i) {
     copies_wait<kTileStages - 2>();
@@ -116,9 +105,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
                   acc[m][j]);
     }
     if (++slot == kTileStages) slot = 0;
-    if (i % kExactBlocks == kExactBlocks - 1) add();
   }
-  add();
 
   // ---- outputs
   copies_wait<0>();
@@ -127,13 +114,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[(1 - set) * 512 + (4 * j + e) * 32] = set == 0 ? sum[1][j][e] : sum[0][j][e];
+    for (int e = 0; e < 4; ++e) part[(1 - set) * 512 + (4 * j + e) * 32] = __float2int_rn(set == 0 ? acc[1][j][e] : acc[0][j][e]);
   __syncthreads();
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int64_t tok = t0 + wt + 16 * set + g + 8 * half;
     if (tok >= a.T) continue;
-    auto at = [&](int j, int e) { return (set == 0 ? sum[0][j][2 * half + e] : sum[1][j][2 * half + e]) + part[set * 512 + (4 * j + 2 * half + e) * 32]; };
+    auto at = [&](int j, int e) {
+      return __float2int_rn(set == 0 ? acc[0][j][2 * half + e] : acc[1][j][2 * half + e]) + part[set * 512 + (4 * j + 2 * half + e) * 32];
+    };
 #pragma unroll
     for (int j = 0; j < (GATED ? 2 : 4); ++j)
 #pragma unroll
@@ -146,14 +135,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
   }
 }
 
-// 3.4 us, 0.64 a block and wave of tiles (mma.sync multiplies 512 pairs a cycle and SM), and the weights at 4 TB/s, which so few copies in
-// flight do not hide. (1000 x 512 x 512 6.4 us, tcgen05 10.3; 2000 x 128 x 128 4.3 and 10.5; 300 x 2048 x 2048 22 and 14; 32 x 1024 x
-// 8192 11.1 and 10.0.)
+// 1 us; 2 a wave of tiles and 0.6 a block of it (what mma.sync takes: 512 pairs a cycle and SM); and the weights at 4 TB/s, which so
+// few copies in flight do not hide. (1000 x 512 x 512 5.4 us, tcgen05 10.3; 2000 x 128 x 128 3.4 and 10.5; 1000 x 1024 x 1024 13.7 and
+// 11.4; 65 x 1440 x 322 10.8 and 7.9.)
 double tile_estimate(const MatArgs& a, int sms) {
-  if ((a.T + 63) / 64 > 65535) return 1e30;            // (the grid's second dimension)
+  if (a.K > kMaxTileK || (a.T + 63) / 64 > 65535) return 1e30;            // (65535: the grid's second dimension)
   const int channels = a.w[1] ? 32 : 64;
   const int64_t tiles = (int64_t)((a.N + channels - 1) / channels) * ((a.T + 63) / 64);
-  return 3000 + (double)((tiles + sms - 1) / sms) * ((a.K + 127) / 128 * 640 + 400) +
+  return 1000 + (double)((tiles + sms - 1) / sms) * ((a.K + 127) / 128 * 600 + 2000) +
          (double)a.N * a.K * (a.w[1] ? 2 : 1) / 4000;
 }
 

@@ -22,6 +22,8 @@ def codes(rows, cols, seed, kind="uniform"):
         q = g.integers(-128, 128, (rows, cols))
     elif kind == "normal":
         q = np.clip(np.rint(g.standard_normal((rows, cols)) * 30), -127, 127)
+    elif kind == "near":                             # sums of 1024 products just below 2^24, whose last bit counts
+        q = g.integers(125, 128, (rows, cols)) * np.where(g.random((rows, 1)) < 0.3, -1, 1)
     else:                                            # the largest sums there are, of both signs
         q = np.where(g.random((rows, 1)) < 0.5, -128, 127) * np.ones((1, cols))
     return q.astype(np.int8), np.exp2(g.uniform(-12, 4, rows)).astype(np.float32)
@@ -90,6 +92,18 @@ def test_matmul_largest_sums(m, T, N, K):
     check_matmul(m, T, N, K, kind="largest")
 
 
+@pytest.mark.parametrize("T", [1, 8, 12, 30, 64, 100, 300, 520])
+@pytest.mark.parametrize("N,K", [(300, 1024), (200, 1920), (40, 2048), (1000, 4096)])
+def test_matmul_sums_near_the_limit(m, T, N, K):
+    check_matmul(m, T, N, K, kind="near")
+
+
+@pytest.mark.parametrize("T,N,K", [(1000, 512, 512), (1500, 700, 1024), (2000, 128, 128), (12000, 65, 80), (200, 2000, 336), (16, 2048, 4096),
+                                   (17, 3000, 1040), (32, 700, 2064), (31, 5000, 528), (25, 100, 1280), (32, 1, 32)])
+def test_matmul_small_products(m, T, N, K):
+    check_matmul(m, T, N, K, pad=16, seed=T)
+
+
 def test_tokens_do_not_depend_on_each_other(m):
     """A row alone, in a batch of 8 and in a prompt has the same bits."""
     x, w, want = check_matmul(m, 300, 200, 4096, kind="normal")
@@ -137,6 +151,11 @@ def test_gated_sizes(m, T, N, K):
 @pytest.mark.parametrize("T,N,K", [(1, 2048, 4096), (8, 11008, 4096), (48, 1500, 4096), (333, 640, 2064), (1500, 130, 512)])
 def test_gated_shapes(m, T, N, K):
     check_gated(m, T, N, K)
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 1024, 512), (900, 333, 1040), (4000, 33, 64), (16, 2048, 2048), (30, 2500, 1040), (20, 9, 2064)])
+def test_gated_small_products(m, T, N, K):
+    check_gated(m, T, N, K, pad=16)
 
 
 @pytest.mark.parametrize("T", [1, 8, 20, 200])
@@ -212,7 +231,8 @@ def test_in_a_graph_and_on_two_streams(m, T):
 
 
 @pytest.mark.parametrize("T,N,K,gated", [(1, 6144, 4096, False), (8, 16384, 4096, False), (8, 4096, 2048, True), (5, 4096, 6144, False),
-                                          (30, 8192, 4096, False), (200, 4096, 4096, True)])
+                                          (30, 8192, 4096, False), (200, 4096, 4096, True), (12, 4096, 4096, False), (30, 2048, 3200, False),
+                                          (16, 2048, 2048, True), (900, 512, 1024, False), (400, 512, 512, True)])
 def test_many_launches_one_after_another(m, T, N, K, gated):
     """Weights from memory each time (three sets, more than the cache holds together with what lies between), always the same bits."""
     x = device_rows(m, *codes(T, K, 1, "normal"))
