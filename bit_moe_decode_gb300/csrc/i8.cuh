@@ -38,11 +38,27 @@ struct MatArgs {
 
 __device__ __forceinline__ float scaled(float sum, float xs, float ws) { return __fmul_rn(__fmul_rn(sum, xs), ws); }
 __device__ __forceinline__ float product(int acc, float xs, float ws) { return scaled((float)acc, xs, ws); }
-__device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v) {
-  if (a.base) v = __fadd_rn(v, a.base[t * a.base_stride + n]);
-  if (a.y) a.y[t * a.y_stride + n] = v;
-  if (a.yb) a.yb[t * a.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
+// Where outputs go, in registers. (As kernel parameters they were read again from the constant cache for every value, each read waiting
+// for the branch before it: 60 cycles a value. base may be y: what a thread needs of it is read together, before its outputs are written.)
+struct Outs {
+  __device__ __forceinline__ float at(int64_t t, int n, bool in) const { return base && in ? base[t * base_stride + n] : 0.f; }
+  const float* base;
+  float* y;
+  uint16_t* yb;
+  int64_t base_stride, y_stride, yb_stride;
+  __device__ __forceinline__ explicit Outs(const MatArgs& a)
+      : base(a.base), y(a.y), yb(a.yb), base_stride(a.base_stride), y_stride(a.y_stride), yb_stride(a.yb_stride) {
+    asm volatile("" : "+l"(base), "+l"(y), "+l"(yb));
+    renew();
+  }
+  // (in an unrolled loop: the strides' multiples are formed again in each turn, not held all along)
+  __device__ __forceinline__ void renew() { asm volatile("" : "+l"(base_stride), "+l"(y_stride), "+l"(yb_stride)); }
+  __device__ __forceinline__ void put(int64_t t, int n, float v, float b) const {        // b: base's value
+    if (base) v = __fadd_rn(v, b);
+    if (y) y[t * y_stride + n] = v;
+    if (yb) yb[t * yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+};
 
 // tcgen05 (i8_tc.cu), and a small CTA a tile (i8_tile.cu); arguments checked by the caller. The estimates are nanoseconds; the
 // workspace's header is at a.status, then tc_workspace_bytes.
@@ -58,9 +74,14 @@ moe_status_t tc_multiply(const MatArgs& a, const TcPlan& p, cudaStream_t stream)
 double tile_estimate(const MatArgs& a, int sms);
 moe_status_t tile_multiply(const MatArgs& a, cudaStream_t stream);
 
-// SiLU(g) u in fp32: one exponential (2 units in the last place at the most times |g|'s rounding in its argument), one IEEE
-// reciprocal. g = -inf gives NaN as the formula does; exp(-g) = inf gives the formula's zero.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fmul_rn(__fmul_rn(g, __frcp_rn(1.0f + expf(-g))), u); }
+// SiLU(g) u in fp32: one exponential (2 units in the last place at the most times |g|'s rounding in its argument), one reciprocal
+// (2^-23). g = -inf gives NaN as the formula does; exp(-g) = inf gives the formula's zero. (The reciprocal that is rounded to
+// the nearest branches, which kept the eight of a thread from overlapping.)
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+  return __fmul_rn(__fmul_rn(g, r), u);
+}
 
 }  // namespace i8
 }  // namespace moe

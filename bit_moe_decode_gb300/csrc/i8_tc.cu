@@ -42,7 +42,7 @@ template <int TOKENS> struct Pair {
   static constexpr uint32_t kTmemA = TOKENS;             // accumulators of the halves at 0 and TOKENS / 2, then 64 columns of A a stage
 };
 constexpr int kPairTokens = 256;
-constexpr int kXchgBytes = 16384;      // gated: products on their way between gate's and up's threads
+constexpr int kOutBytes = 16384;       // sums of 16 tokens on their way to the threads that write outputs
 constexpr int kSmemLimit = 232448 - 1024;    // (the static part beside it)
 
 struct TcArgs {
@@ -54,8 +54,9 @@ struct TcArgs {
   // head of one][nt / 4 tokens][256][4] of tiles that are shared
   int grain, share, extra;
   int* parts;
-  const uint32_t* squares;   // pair_kernel: the tokens' sums of squares, and
-  uint32_t most;             //   up to which a tile is one segment: |sum| <= sqrt(sum w^2 sum x^2) <= 128 sqrt(K sum x^2) <= 2^24
+  const uint32_t* squares;   // pair_kernel: the tokens' sums of squares
+  bool wide;                 // base, y and y_bf16 can be taken four channels at a time
+  uint32_t most;             // pair_kernel: up to which a tile is one segment: |sum| <= sqrt(sum w^2 sum x^2) <= 128 sqrt(K sum x^2) <= 2^24
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -100,31 +101,6 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
 }
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// Outputs of channel n for the `count` (up to E) tokens from t on. Loads and stores go in groups, so that their latencies overlap.
-template <int E>
-__device__ __forceinline__ void put_tokens(const MatArgs& a, int64_t t, int count, int n, float (&v)[E]) {
-  if (a.base) {
-    const float* p = a.base + t * a.base_stride + n;
-    float d[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) d[e] = e < count ? p[e * a.base_stride] : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __fadd_rn(v[e], d[e]);
-  }
-  if (a.y) {
-    float* p = a.y + t * a.y_stride + n;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < count) p[e * a.y_stride] = v[e];
-  }
-  if (a.yb) {
-    uint16_t* p = a.yb + t * a.yb_stride + n;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < count) p[e * a.yb_stride] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
-  }
 }
 
 // The rest of a wait: true if it ran out. (Inlined: a call would hold registers that the warpgroups' split has not left.)
@@ -242,64 +218,146 @@ __device__ __forceinline__ void more_sums(uint32_t taddr, int n, int (&sum)[COLS
     }
   tc_fence_before();
 }
-// Tokens 16 c .. of the sums. (A rolled loop over c keeps the code of the outputs small: unrolled it was 130 KB, and a tile's end
-// took 15 us longer, of instruction misses.)
-template <int COLS>
-__device__ __forceinline__ void give_sums(int c, const int (&sum)[COLS], int (&r)[16]) {
-#pragma unroll
-  for (int k = 0; k < COLS / 16; ++k)
-    if (c == k) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) r[e] = sum[16 * k + e];
-    }
-}
-// The scales that a tile's outputs need, loaded long before: tokens t0 + lane, + 32, ... of the warp's lanes, and channel n's.
-template <int COLS>
+// Outputs go through shared memory, 16 tokens at a time (8 where registers are short): a thread has all tokens of one row of the product, and writes four channels
+// of every fourth token (gated: eighth). WIDTH channels are written by the 32 threads that have them, or gated by the 2 WIDTH threads
+// that have gate's (columns 0 .. WIDTH - 1 of the buffer) and up's. Where a tensor's alignment does not allow that (or the group ends
+// beyond N), a channel a thread. Loops are unrolled: a warp alone has no other work to hide an instruction's latency. (Rolled, with
+// the sums selected by the counter, a tile of 256 tokens took 10 us: 2048 x 1024 x 32768 155 us against 103, gated 1945 x 304 x 7288
+// 98 against 49; 1155 x 1376 x 11355, a channel a thread, 84 against 45.) small_kernel with 16 tokens has no buffer for it: a
+// further stage of copies is worth more (12 x 4096 x 32768 26.1 us against 26.9).
+
+// The scales that a tile's outputs need, loaded long before: tokens t0 + lane, + 32, ..., and four channels' from n0 + 4 (id % (WIDTH / 4)).
+template <bool GATED, int COLS, int WIDTH>
 struct Scales {
-  float x[(COLS + 31) / 32], w;
-  __device__ __forceinline__ void load(const MatArgs& a, const float* ws, int t0, int n) {
+  float x[(COLS + 31) / 32], w[GATED ? 2 : 1][4];
+  __device__ __forceinline__ void load(const MatArgs& a, int t0, int n0, int id) {
 #pragma unroll
     for (int i = 0; i < (COLS + 31) / 32; ++i) x[i] = __ldg(a.xs + min(t0 + (int)(threadIdx.x & 31) + 32 * i, a.T - 1));
-    w = __ldg(ws + min(n, a.N - 1));
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[m][e] = __ldg(a.ws[m] + min(n0 + 4 * (id % (WIDTH / 4)) + e, a.N - 1));
   }
 };
-// The outputs of `count` tokens from t0 on, channel n (none if n >= N), from sums that are still fp32 (single) or integers. Gated: the thread has gate's (side 0) or up's sums, and
-// the thread with the other of the same n is at the same idx (of `width`) on the other side; of 16 tokens side 0 finishes the first
-// eight, side 1 the last, and what the other needs goes through shared memory (two buffers in turn), ordered by barrier `bar` among
-// 2 width threads.
-template <bool GATED, int COLS>
-__device__ __forceinline__ void output_sums(const MatArgs& a, const int (&sum)[COLS], bool single, const Scales<COLS>& sc, int t0, int count,
-                                            int n, int side, uint32_t xchg, int idx, int width, int bar) {
-  int r[16];
-#pragma unroll 1
-  for (int c = 0; c * 16 < count; ++c) {
-    give_sums(c, sum, r);
-    const int t1 = t0 + 16 * c;
-    float xs = sc.x[0];
+// The outputs of `count` tokens from t0 on, channels n0 .. n0 + WIDTH - 1, from sums that are still fp32 (single) or integers. id: the
+// thread among those that write together; buf: their buffer; bar (gated): their barrier. PART tokens at a time (gated: 16).
+template <int PART, bool GATED, int COLS, int WIDTH>
+__device__ __forceinline__ void output_sums(const TcArgs& args, const int (&sum)[COLS], bool single, const Scales<GATED, COLS, WIDTH>& sc,
+                                            int t0, int count, int n0, int id, uint32_t buf, int bar) {
+  constexpr int ROW = GATED ? 2 * WIDTH : WIDTH, FOURS = WIDTH / 4;     // columns of the buffer and threads; threads a token
+  const MatArgs& a = args.m;
+  const bool wide = args.wide && n0 + WIDTH <= a.N;
+  const int ch = wide ? 4 * (id % FOURS) : id % WIDTH, n = n0 + ch, first = wide ? id / FOURS : id / WIDTH;
+  const uint32_t from = buf + (uint32_t)(first * ROW + ch) * 4;
+  Outs outs(a);
+  int64_t t = t0 + first;
+  int left = a.T - t0 - first;               // (tokens from t on)
+  auto sync = [&]() {
+    if (GATED) named_bar(bar, ROW);
+    else __syncwarp();
+  };
+  auto real = [&](uint32_t v) { return single ? __uint_as_float(v) : (float)(int)v; };
+  auto give = [&](int from) {
 #pragma unroll
-    for (int i = 1; i < (COLS + 31) / 32; ++i)
-      if (c >> 1 == i) xs = sc.x[i];
-    float v[16];
+    for (int e = 0; e < PART; ++e)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(e * ROW + id) * 4), "r"(sum[from + e]) : "memory");
+  };
+  if (wide) {
+    constexpr int TOKS = PART * FOURS / ROW, STEP = ROW / FOURS;           // of a thread: every STEP-th
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      v[e] = scaled(single ? __int_as_float(r[e]) : (float)r[e], __shfl_sync(0xFFFFFFFFu, xs, 16 * (c & 1) + e), sc.w);
-    if (!GATED) {
-      if (n < a.N) put_tokens<16>(a, t1, a.T - t1, n, v);
-    } else {
-      const uint32_t buf = xchg + ((c & 1) * 16 * width + idx) * 4, mine = buf + side * 32 * width, theirs = buf + (1 - side) * 32 * width;
+    for (int c = 0; c < COLS; c += PART, t += PART, left -= PART) {
+      if (c >= count) break;
+      outs.renew();
+      float4 before[TOKS];
+      if (!GATED && outs.base)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(theirs + e * 4 * width), "f"(side == 0 ? v[8 + e] : v[e]) : "memory");
-      named_bar(bar, 2 * width);
-      float h[8];
+        for (int i = 0; i < TOKS; ++i)
+          if (STEP * i < left) before[i] = *reinterpret_cast<const float4*>(outs.base + (t + STEP * i) * outs.base_stride + n);
+      sync();                                // the buffer has been read
+      give(c);
+      sync();
+      uint4 s0[TOKS], s1[TOKS];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(h[e]) : "r"(mine + e * 4 * width) : "memory");
+      for (int i = 0; i < TOKS; ++i) {
+        s0[i] = ld_shared(from + i * (STEP * ROW * 4));
+        if (GATED) s1[i] = ld_shared(from + i * (STEP * ROW * 4) + 4 * WIDTH);
+      }
+      float v[TOKS][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = side == 0 ? silu_mul(v[e], h[e]) : silu_mul(h[e], v[8 + e]);
-      if (n < a.N) put_tokens<8>(a, t1 + 8 * side, a.T - t1 - 8 * side, n, h);
+      for (int i = 0; i < TOKS; ++i) {
+        const float x = __shfl_sync(0xFFFFFFFFu, sc.x[c / 32], c % 32 + first + STEP * i);
+        v[i][0] = scaled(real(s0[i].x), x, sc.w[0][0]);
+        v[i][1] = scaled(real(s0[i].y), x, sc.w[0][1]);
+        v[i][2] = scaled(real(s0[i].z), x, sc.w[0][2]);
+        v[i][3] = scaled(real(s0[i].w), x, sc.w[0][3]);
+        if (GATED) {
+          constexpr int M = GATED ? 1 : 0;
+          v[i][0] = silu_mul(v[i][0], scaled(real(s1[i].x), x, sc.w[M][0]));
+          v[i][1] = silu_mul(v[i][1], scaled(real(s1[i].y), x, sc.w[M][1]));
+          v[i][2] = silu_mul(v[i][2], scaled(real(s1[i].z), x, sc.w[M][2]));
+          v[i][3] = silu_mul(v[i][3], scaled(real(s1[i].w), x, sc.w[M][3]));
+        } else if (outs.base) {
+          v[i][0] = __fadd_rn(v[i][0], before[i].x);
+          v[i][1] = __fadd_rn(v[i][1], before[i].y);
+          v[i][2] = __fadd_rn(v[i][2], before[i].z);
+          v[i][3] = __fadd_rn(v[i][3], before[i].w);
+        }
+      }
+      if (outs.y)
+#pragma unroll
+        for (int i = 0; i < TOKS; ++i)
+          if (STEP * i < left)
+            *reinterpret_cast<float4*>(outs.y + (t + STEP * i) * outs.y_stride + n) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      if (outs.yb)
+#pragma unroll
+        for (int i = 0; i < TOKS; ++i) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[i][0], v[i][1]), hi = __floats2bfloat162_rn(v[i][2], v[i][3]);
+          if (STEP * i < left)
+            *reinterpret_cast<uint2*>(outs.yb + (t + STEP * i) * outs.yb_stride + n) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+    }
+  } else {
+    // eight tokens at a time: not gated, of those the thread has the sums of
+    constexpr int STEP = ROW / WIDTH;
+    const float w0 = __ldg(a.ws[0] + min(n, a.N - 1)), w1 = GATED ? __ldg(a.ws[1] + min(n, a.N - 1)) : 0.f;
+    if (n >= a.N) left = 0;
+#pragma unroll
+    for (int c = 0; c < COLS / 8; c += STEP, t += 8 * STEP, left -= 8 * STEP) {
+      if (c * 8 >= count) break;
+      outs.renew();
+      float before[8], v[8];
+      if (!GATED && outs.base)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) before[i] = i < left ? outs.base[(t + i) * outs.base_stride + n] : 0.f;
+      if (GATED) {
+        sync();
+        give(8 * c);
+        sync();
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = __shfl_sync(0xFFFFFFFFu, sc.x[c / 4], 8 * (c & 3) + first + STEP * i);
+        if (GATED) {
+          uint32_t s0, s1;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s0) : "r"(from + i * (STEP * ROW * 4)) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s1) : "r"(from + i * (STEP * ROW * 4) + 4 * WIDTH) : "memory");
+          v[i] = silu_mul(scaled(real(s0), x, w0), scaled(real(s1), x, w1));
+        } else {
+          v[i] = scaled(real((uint32_t)sum[8 * c + i]), x, w0);
+          if (outs.base) v[i] = __fadd_rn(v[i], before[i]);
+        }
+      }
+      if (outs.y)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (STEP * i < left) outs.y[(t + STEP * i) * outs.y_stride + n] = v[i];
+      if (outs.yb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (STEP * i < left) outs.yb[(t + STEP * i) * outs.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
     }
   }
-  if (GATED) named_bar(bar, 2 * width);   // the next tile's first buffer is free
 }
 
 // The first stage that a CTA has, and (for a grain of 1) the CTA that has a stage.
@@ -342,7 +400,22 @@ __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
   float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = GATED ? silu_mul(product(g[e], xs[e], w0), product(u[e], xs[e], w1)) : product(g[e], xs[e], w0);
-  put_tokens<4>(a.m, t, a.m.T - t, n, v);
+  const MatArgs& m = a.m;                 // (read where they are used: in registers beforehand 64 x 4096 x 4096 took 0.3 us more)
+  if (m.base) {
+    float before[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) before[e] = t + e < m.T ? m.base[(int64_t)(t + e) * m.base_stride + n] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(v[e], before[e]);
+  }
+  if (m.y)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < m.T) m.y[(int64_t)(t + e) * m.y_stride + n] = v[e];
+  if (m.yb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < m.T) m.yb[(int64_t)(t + e) * m.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
 }
 
 // ------------------------------------------------------------------------------------------------ one CTA, up to 64 tokens
@@ -362,7 +435,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
   const int nt = a.nt, stages = a.stages, T = a.m.T;
   const uint32_t stage_bytes = 32768 + nt * 128, slot_bytes = nt * 256;
-  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, xchg = xring + kSlots * slot_bytes;
+  const uint32_t ring = smem_u32(smem), xring = ring + stages * stage_bytes, obuf = xring + kSlots * slot_bytes;
 
   // ---- this CTA's stages: `total` from stage `s_first` of tile `first` on
   const int nk = (a.m.K + kTileK - 1) / kTileK, cta = blockIdx.x;
@@ -494,17 +567,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   } else {
     // ================================================================ block b's sums and outputs
     regs_more<136>();
-    const int b = wg, row = tid & 127;
+    const int b = wg;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + b * 64;
     int sum[kSmallTokens];
     int seg = 0, tile = first;
-    Scales<kSmallTokens> scales;
+    constexpr int kWidth = GATED ? 128 : 32;
+    const int id = GATED ? tid : lane;
+    Scales<GATED, kSmallTokens, kWidth> scales;
     for (int s0 = s_first, left = total; left > 0; ++tile) {
       const int part = min(nk - s0, left), tn = tile % a.tiles_n, t0 = tile / a.tiles_n * nt;
-      const int n = GATED ? tn * 128 + row : tn * 256 + b * 128 + row;
+      const int n0 = GATED ? tn * 128 : tn * 256 + warp * 32;
       const bool whole = part == nk;
       bool single = part <= kSegment, begun = false;
-      scales.load(a.m, a.m.ws[GATED ? b : 0], t0, n);
+      scales.load(a.m, t0, n0, id);
       for (int s = 0; s < part; ++s) {
         if (!ends_segment(s, part, b, part <= kSegment)) continue;
         wait(bar_d_full + b, seg & 1);
@@ -518,7 +593,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
         begun = true;
       }
       if (whole) {
-        output_sums<GATED>(a.m, sum, single, scales, t0, nt, n, b, xchg, row, 128, 1);
+        output_sums<GATED ? 16 : 8>(a, sum, single, scales, t0, nt, n0, id, GATED ? obuf : obuf + warp * 2048, 1);
       } else {
         int* mine = a.parts + (int64_t)(2 * cta + (s0 == 0)) * 256 * nt + tid * 4;
         const int count = min(nt, T - t0);
@@ -625,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), wg = warp >> 2;
   const int half = a.nt / 2, part = half / 2;                           // tokens of a half, and of it in this CTA
   const uint32_t stage_bytes = 16384 + half * 256;
-  const uint32_t ring = smem_u32(smem), xchg = ring + kStages * stage_bytes;
+  const uint32_t ring = smem_u32(smem), obuf = ring + kStages * stage_bytes;
   const int rank = (int)cluster_rank(), first = blockIdx.x / 2, step_tiles = gridDim.x / 2;
   const int nk = (a.m.K + kTileK - 1) / kTileK;
   const int my_tiles = (a.tiles - first + step_tiles - 1) / step_tiles, total = my_tiles * nk;
@@ -736,13 +811,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
     const int d = wg, row = tid & 127;
     const uint32_t td = tmem + ((uint32_t)(warp & 3) << 21) + d * (TOKENS / 2);
     int sum[TOKENS / 2];
-    Scales<TOKENS / 2> scales;
+    constexpr int kWidth = GATED ? 64 : 32;
+    const int id = GATED ? row : lane;
+    Scales<GATED, TOKENS / 2, kWidth> scales;
     int seg = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int j = 0; j < my_tiles; ++j) {
       const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + d * half;
-      const int n = GATED ? tn * 128 + rank * 64 + (row & 63) : tn * 256 + rank * 128 + row;
-      scales.load(a.m, a.m.ws[GATED ? row >> 6 : 0], t0, n);
+      const int n0 = GATED ? tn * 128 + rank * 64 : tn * 256 + rank * 128 + (warp & 3) * 32;
+      scales.load(a.m, t0, n0, id);
       const bool single = __reduce_max_sync(0xFFFFFFFFu, tile_squares(a, t0 - d * half)) <= a.most;
       bool begun = false;
       for (int s = 0; s < nk; ++s) {
@@ -757,7 +834,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
         if (!begun && !single) integer_sums(half, sum);
         begun = true;
       }
-      output_sums<GATED>(a.m, sum, single, scales, t0, half, n, row >> 6, xchg + d * (kXchgBytes / 2), row & 63, 64, 1 + d);
+      output_sums<16>(a, sum, single, scales, t0, half, n0, id, GATED ? obuf + d * (kOutBytes / 2) : obuf + warp * 2048, 1 + d);
     }
   }
   __syncwarp();
@@ -783,7 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
 TcPlan tc_plan(const MatArgs& a, int sms) {
   const bool gated = a.w[1] != nullptr;
   TcPlan best{};
-  const int tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), nk = (a.K + kTileK - 1) / kTileK, fixed = gated ? kXchgBytes : 0;
+  const int tiles_n = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), nk = (a.K + kTileK - 1) / kTileK;
   auto consider = [&](const TcPlan& p, double ns) {
     if (best.ns == 0 || ns < best.ns) {
       best = p;
@@ -796,7 +873,7 @@ TcPlan tc_plan(const MatArgs& a, int sms) {
     p.nt = ((a.T + tiles_t - 1) / tiles_t + 15) / 16 * 16;
     p.tiles_n = tiles_n;
     p.tiles = tiles_n * tiles_t;
-    const int stage = 32768 + p.nt * 128, rest = fixed + kSlots * p.nt * 256, all = p.tiles * nk;
+    const int stage = 32768 + p.nt * 128, rest = (gated || p.nt > 16 ? kOutBytes : 0) + kSlots * p.nt * 256, all = p.tiles * nk;
     p.stages = min(kMaxStages, (kSmemLimit - 1024 - rest) / stage);
     p.smem = 1024 + rest + p.stages * stage;
     const double stage_ns = 530 + 4 * p.nt, memory = (double)tiles_n * 256 * a.K / 6300;
@@ -826,7 +903,7 @@ TcPlan tc_plan(const MatArgs& a, int sms) {
       p.nt = nt;
       p.tiles_n = tiles_n;
       p.tiles = tiles_n * ((a.T + nt - 1) / nt);
-      p.smem = 1024 + fixed + (p.pair == 128 ? Pair<128>::kStages : Pair<256>::kStages) * (16384 + nt * 128);
+      p.smem = 1024 + kOutBytes + (p.pair == 128 ? Pair<128>::kStages : Pair<256>::kStages) * (16384 + nt * 128);
       p.ctas = 2 * min(p.tiles, pairs);
       const int waves = (p.tiles + pairs - 1) / pairs;
       const double alone = p.pair == 128 ? 370 : 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
@@ -885,24 +962,27 @@ moe_status_t tc_multiply(const MatArgs& a, const TcPlan& p, cudaStream_t stream)
   const int pieces = (a.K + 63) / 64 * 4;
   int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(a.status) + sizeof(WsHeader));
   uint32_t* squares = reinterpret_cast<uint32_t*>(parts);
-  uint8_t* wide = reinterpret_cast<uint8_t*>(squares) + squares_bytes(a.T);
+  uint8_t* halves = reinterpret_cast<uint8_t*>(squares) + squares_bytes(a.T);
   if (!map_rows(&m0, a.w[0], a.N, a.K, a.w_stride[0], box_w)) return MOE_ERR_CUDA;
   if (p.pair) {
     const uint64_t dims[3] = {128, (uint64_t)a.T, (uint64_t)pieces / 4}, strides[2] = {(uint64_t)pieces * 32, 128};
     const uint32_t box[3] = {128, (uint32_t)p.nt / 4, 2};
-    if (!moe_internal::tmap_u8(&mx, wide, 3, dims, strides, box)) return MOE_ERR_CUDA;
+    if (!moe_internal::tmap_u8(&mx, halves, 3, dims, strides, box)) return MOE_ERR_CUDA;
   } else if (!map_rows(&mx, a.x, a.T, a.K, a.x_stride, p.nt)) {
     return MOE_ERR_CUDA;
   }
   m1 = m0;
   if (gated && !map_rows(&m1, a.w[1], a.N, a.K, a.w_stride[1], box_w)) return MOE_ERR_CUDA;
-  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.grain, p.share, p.extra, parts, squares,
+  const bool aligned = ((uintptr_t)a.base % 16 | (uintptr_t)a.y % 16 | (uintptr_t)a.yb % 8) == 0 && (!a.base || a.base_stride % 4 == 0) &&
+                       (!a.y || a.y_stride % 4 == 0) && (!a.yb || a.yb_stride % 4 == 0);
+  const bool wide = aligned && (gated || p.pair || p.nt > 16);
+  const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.grain, p.share, p.extra, parts, squares, wide,
                     (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
   cudaLaunchConfig_t cfg = config(p, stream);
   cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    widen_kernel<<<min((a.T + 3) / 4, 2048), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, wide, squares);
+    widen_kernel<<<min((a.T + 3) / 4, 2048), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, halves, squares);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
