@@ -38,27 +38,13 @@ struct MatArgs {
 
 __device__ __forceinline__ float scaled(float sum, float xs, float ws) { return __fmul_rn(__fmul_rn(sum, xs), ws); }
 __device__ __forceinline__ float product(int acc, float xs, float ws) { return scaled((float)acc, xs, ws); }
-// Where outputs go, in registers. (As kernel parameters they were read again from the constant cache for every value, each read waiting
-// for the branch before it: 60 cycles a value. base may be y: what a thread needs of it is read together, before its outputs are written.)
-struct Outs {
-  __device__ __forceinline__ float at(int64_t t, int n, bool in) const { return base && in ? base[t * base_stride + n] : 0.f; }
-  const float* base;
-  float* y;
-  uint16_t* yb;
-  int64_t base_stride, y_stride, yb_stride;
-  __device__ __forceinline__ explicit Outs(const MatArgs& a)
-      : base(a.base), y(a.y), yb(a.yb), base_stride(a.base_stride), y_stride(a.y_stride), yb_stride(a.yb_stride) {
-    asm volatile("" : "+l"(base), "+l"(y), "+l"(yb));
-    renew();
-  }
-  // (in an unrolled loop: the strides' multiples are formed again in each turn, not held all along)
-  __device__ __forceinline__ void renew() { asm volatile("" : "+l"(base_stride), "+l"(y_stride), "+l"(yb_stride)); }
-  __device__ __forceinline__ void put(int64_t t, int n, float v, float b) const {        // b: base's value
-    if (base) v = __fadd_rn(v, b);
-    if (y) y[t * y_stride + n] = v;
-    if (yb) yb[t * yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  }
-};
+// An output, with base's value for it (unused without base). base may be y: what a thread needs of it is read before any of its outputs
+// is written, so that the reads do not wait for each other.
+__device__ __forceinline__ void put(const MatArgs& a, int64_t t, int n, float v, float base) {
+  if (a.base) v = __fadd_rn(v, base);
+  if (a.y) a.y[t * a.y_stride + n] = v;
+  if (a.yb) a.yb[t * a.yb_stride + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
 
 // tcgen05 (i8_tc.cu), and a small CTA a tile (i8_tile.cu); arguments checked by the caller. The estimates are nanoseconds; the
 // workspace's header is at a.status, then tc_workspace_bytes.

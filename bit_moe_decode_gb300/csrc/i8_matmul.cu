@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
     }
   } else {
     // ================================================================ sums of the warps, outputs: channel r, tokens t, t + 8, ...
-    const Outs outs(a);
     const int id = tid - kRowWarps * 32, r = id & 15, t = id >> 4, up = GATED ? r >> 3 : 0;
     float scale[NT];
 #pragma unroll
@@ -210,13 +209,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sum_empty + buf);
       float before[NT];
+      if (!GATED && a.base)
 #pragma unroll
-      for (int k = 0; k < NT; ++k) before[k] = outs.at(8 * k + t, n, !GATED && 8 * k + t < a.T && n < a.N);
+        for (int k = 0; k < NT; ++k) before[k] = 8 * k + t < a.T && n < a.N && r < channels ? a.base[(8 * k + t) * a.base_stride + n] : 0.f;
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
         float v = product(s[k], scale[k], ws);
         if (GATED) v = silu_mul(v, __shfl_down_sync(0xFFFFFFFFu, v, 8));
-        if (8 * k + t < a.T && n < a.N && r < channels) outs.put(8 * k + t, n, v, before[k]);
+        if (8 * k + t < a.T && n < a.N && r < channels) put(a, 8 * k + t, n, v, before[k]);
       }
     }
   }

@@ -239,6 +239,20 @@ struct Scales {
       for (int e = 0; e < 4; ++e) w[m][e] = __ldg(a.ws[m] + min(n0 + 4 * (id % (WIDTH / 4)) + e, a.N - 1));
   }
 };
+// Where outputs go, in registers. (As kernel parameters they were read from the constant cache for every value, each read waiting for the
+// branch before it.) renew: in an unrolled loop the strides' multiples are formed again in each turn, not held all along.
+struct Outs {
+  const float* base;
+  float* y;
+  uint16_t* yb;
+  int64_t base_stride, y_stride, yb_stride;
+  __device__ __forceinline__ explicit Outs(const MatArgs& a)
+      : base(a.base), y(a.y), yb(a.yb), base_stride(a.base_stride), y_stride(a.y_stride), yb_stride(a.yb_stride) {
+    asm volatile("" : "+l"(base), "+l"(y), "+l"(yb));
+    renew();
+  }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+l"(base_stride), "+l"(y_stride), "+l"(yb_stride)); }
+};
 // The outputs of `count` tokens from t0 on, channels n0 .. n0 + WIDTH - 1, from sums that are still fp32 (single) or integers. id: the
 // thread among those that write together; buf: their buffer; bar (gated): their barrier. PART tokens at a time (gated: 16).
 template <int PART, bool GATED, int COLS, int WIDTH>
@@ -853,8 +867,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
 // CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6; 16 x 4096 x 32768 (128 tiles):
 // 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
 // pair_kernel: 3.5 us and the widening; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token, or with all SMs at
-// it 2.5 ns a token (the products); a tile's outputs 39 ns a token (gated 53), beside the next tile's stages. (201 x 4096 x
-// 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one warpgroup that converts, 24.5 with 256.)
+// it 2.5 ns a token (the products); a tile's outputs 32 ns a token (24 where they are written
+// four channels at a time, 39 where not), beside the next tile's stages. (201 x 4096 x 4096: 20.0 us with 128 tokens a tile,
+// 21.3 with 96 and one warpgroup that converts, 24.5 with 256.)
 // More than 64 tokens: 154 x 7264 x 584 13.3 us by small_kernel, whose CTAs share tiles, and 30.7 by pair_kernel; 767 x 1936 x 226
 // gated 10.1 and 16.0; 68 x 2224 x 9507 18.1 and 15.1; 294 x 4032 x 8863 43 and 27.
 TcPlan tc_plan(const MatArgs& a, int sms) {
@@ -907,7 +922,7 @@ TcPlan tc_plan(const MatArgs& a, int sms) {
       p.ctas = 2 * min(p.tiles, pairs);
       const int waves = (p.tiles + pairs - 1) / pairs;
       const double alone = p.pair == 128 ? 370 : 340 + 0.65 * nt, full = 2.5 * nt * min(p.tiles, pairs) / pairs;
-      const double products = nk * (alone > full ? alone : full), out = (gated ? 53 : 39) * nt;
+      const double products = nk * (alone > full ? alone : full), out = 32 * nt;
       consider(p, 3500 + 6e-4 * a.T * a.K + (products > out ? waves * products + out : products + waves * out));
     }
   }

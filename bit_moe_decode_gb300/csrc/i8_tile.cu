@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
   }
 
   // ---- outputs
-  const Outs outs(a);
   copies_wait<0>();
   __syncthreads();
   int* part = reinterpret_cast<int*>(smem) + (warp & 3) * 1024 + lane;          // [set that needs it][16][warp of a set][32 lanes]
@@ -122,10 +121,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
     const int64_t tok = t0 + wt + 16 * set + g + 8 * half;
     if (tok >= a.T) continue;
     float before[4][2];
+    if (!GATED && a.base)
 #pragma unroll
-    for (int j = 0; j < (GATED ? 0 : 4); ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) before[j][e] = outs.at(tok, n0 + (wn - 64) + 8 * j + 2 * c + e, n0 + (wn - 64) + 8 * j + 2 * c + e < a.N);
+        for (int e = 0; e < 2; ++e) {
+          const int ch = n0 + (wn - 64) + 8 * j + 2 * c + e;
+          before[j][e] = ch < a.N ? a.base[tok * a.base_stride + ch] : 0.f;
+        }
     auto at = [&](int j, int e) {
       return __float2int_rn(set == 0 ? acc[0][j][2 * half + e] : acc[1][j][2 * half + e]) + part[set * 512 + (4 * j + 2 * half + e) * 32];
     };
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
         const int ch = n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * j + 2 * c + e;
         if (ch >= a.N) continue;
         const float p = product(at(j, e), xs[half], ws[j][e]);
-        outs.put(tok, ch, GATED ? silu_mul(p, product(at(GATED ? 2 + j : j, e), xs[half], ws[GATED ? 2 + j : j][e])) : p, GATED ? 0.f : before[j][e]);
+        put(a, tok, ch, GATED ? silu_mul(p, product(at(GATED ? 2 + j : j, e), xs[half], ws[GATED ? 2 + j : j][e])) : p, GATED ? 0.f : before[j][e]);
       }
   }
 }
