@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
   uint8_t* xs = smem + stages * kRowStage;
   int* parts = reinterpret_cast<int*>(xs + (a.T * pitch + 127) / 128 * 128);      // [two groups][warp][8 NT tokens][16]
 
+  next_may_start();
   bool dead = false;
   auto wait = [&](uint64_t* bar, int parity) {
     if (mbar_try_wait(bar, parity) || dead) return;
@@ -77,10 +78,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
     else if (lane >= 30) { mbar_init(bar_sum_full + lane - 30, kRowWarps); mbar_init(bar_sum_empty + lane - 30, kOutWarps); }
     fence_mbar_init();
     __syncwarp();
+    wait_for_prior();
     if (lane == 0)
       for (; issued < stages && c_group < groups; ++issued) copy_next(issued);
   } else {
     // ---- the tokens, in convert4's order, zeros past K
+    wait_for_prior();
     const int pieces = blocks * 8, all = a.T * pieces, threads = (kRowWarps + kOutWarps) * 32;
     const float per = 1.0f / (float)pieces;                      // (i + 1/2) per is never nearer than 1/2 per to an integer
     for (int i0 = tid; i0 < all; i0 += 4 * threads) {
@@ -256,8 +259,7 @@ static cudaError_t launch_rows(const MatArgs& a, int ctas, int groups, int stage
     ready[dev] = true;
   }
   const int smem = 1024 + stages * kRowStage + tokens_bytes(a.T, a.K) + 2 * kRowWarps * 128 * NT * 4;
-  rows_kernel<GATED, NT><<<ctas, kRowThreads, smem, stream>>>(a, groups, stages, map[0], map[1], tail[0], tail[1]);
-  return cudaGetLastError();
+  return launch(rows_kernel<GATED, NT>, ctas, kRowThreads, smem, stream, a, groups, stages, map[0], map[1], tail[0], tail[1]);
 }
 static moe_status_t rows_multiply(const MatArgs& a, int sms, cudaStream_t stream) {
   const int stages = rows_stages(a.T, a.K);
@@ -276,11 +278,9 @@ static moe_status_t rows_multiply(const MatArgs& a, int sms, cudaStream_t stream
     if (whole > 0 && !moe_internal::tmap_u8(&map[i], a.w[m], 3, dims, strides, box)) return MOE_ERR_CUDA;
   }
   const int nt = rows_tiles(a.T), ctas = min(groups, sms);
-  auto* launch = a.w[1] ? (nt == 1 ? launch_rows<true, 1> : nt == 2 ? launch_rows<true, 2> : launch_rows<true, 4>)
-                        : (nt == 1 ? launch_rows<false, 1> : nt == 2 ? launch_rows<false, 2> : launch_rows<false, 4>);
-  if (launch(a, ctas, groups, stages, map, tail, stream) == cudaSuccess) return MOE_OK;
-  cudaGetLastError();
-  return MOE_ERR_CUDA;
+  auto* run = a.w[1] ? (nt == 1 ? launch_rows<true, 1> : nt == 2 ? launch_rows<true, 2> : launch_rows<true, 4>)
+                     : (nt == 1 ? launch_rows<false, 1> : nt == 2 ? launch_rows<false, 2> : launch_rows<false, 4>);
+  return run(a, ctas, groups, stages, map, tail, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 static bool out_ok(const void* p, int64_t stride, int64_t cols, int size) {

@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(512) rows_kernel(RowArgs a) {
   __shared__ uint32_t part[64];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int tid = threadIdx.x, n = a.cols >> 3, warps = blockDim.x >> 5;
+  next_may_start();
+  wait_for_prior();
   if (row >= a.rows) return;                     // (only where a row is a warp's)
   const TH* h = (const TH*)a.h + row * a.h_stride;
   // everything is read before anything is used (a place past the row's end reads its last vector and counts for nothing)
@@ -237,6 +239,8 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(RowArgs a) {
   const int64_t row = blockIdx.x;
   const int n = a.cols >> 3, warps = blockDim.x >> 5;
   const T* h = (const T*)a.h + row * a.h_stride;
+  next_may_start();
+  wait_for_prior();
   float sum = 0.f, most = 0.f;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     Vec8<T> raw;
@@ -266,6 +270,8 @@ __global__ void __launch_bounds__(256) values_kernel(const int8_t* q, int64_t st
   const int per_row = (cols + 1023) / 1024, lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t row = item / per_row;
+  next_may_start();
+  wait_for_prior();
   if (row >= rows) return;
   const int first = (int)(item - row * per_row) * 1024 + 4 * lane;
   char4 w[8];
@@ -292,11 +298,12 @@ static moe_status_t launch_rows(const RowArgs& a, int rows, cudaStream_t st) {
   const int per = (vecs + (warp ? 31 : kPer - 1)) / (warp ? 32 : kPer);
   const int v = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
   const dim3 block(warp ? 32 : ((vecs + v - 1) / v + 31) / 32 * 32, warp ? 8 : 1), grid((rows + block.y - 1) / block.y);
-  if (v == 1) rows_kernel<TH, TR, NORM, 1><<<grid, block, 0, st>>>(a);
-  else if (v == 2) rows_kernel<TH, TR, NORM, 2><<<grid, block, 0, st>>>(a);
-  else if (v == 4) rows_kernel<TH, TR, NORM, 4><<<grid, block, 0, st>>>(a);
-  else rows_kernel<TH, TR, NORM, 8><<<grid, block, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cudaError_t e;
+  if (v == 1) e = launch(rows_kernel<TH, TR, NORM, 1>, grid, block, 0, st, a);
+  else if (v == 2) e = launch(rows_kernel<TH, TR, NORM, 2>, grid, block, 0, st, a);
+  else if (v == 4) e = launch(rows_kernel<TH, TR, NORM, 4>, grid, block, 0, st, a);
+  else e = launch(rows_kernel<TH, TR, NORM, 8>, grid, block, 0, st, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 static bool type_ok(moe_type_t t) { return t == MOE_TYPE_F32 || t == MOE_TYPE_BF16; }
@@ -335,9 +342,8 @@ extern "C" moe_status_t moe_i8_quantize(moe_type_t type, const void* src, int64_
     if (type == MOE_TYPE_F32) return launch_rows<float, None, false>(a, dst->rows, s);
     return launch_rows<__nv_bfloat16, None, false>(a, dst->rows, s);
   }
-  if (type == MOE_TYPE_F32) long_rows_kernel<float><<<dst->rows, 1024, 0, s>>>(a);
-  else long_rows_kernel<__nv_bfloat16><<<dst->rows, 1024, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = launch(type == MOE_TYPE_F32 ? long_rows_kernel<float> : long_rows_kernel<__nv_bfloat16>, dst->rows, 1024, 0, s, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status_t moe_i8_values(const moe_i8_rows_t* src, float* out, void* stream) {
@@ -349,9 +355,9 @@ extern "C" moe_status_t moe_i8_values(const moe_i8_rows_t* src, float* out, void
   st = moe_check_device();
   if (st != MOE_OK) return st;
   const int64_t items = (int64_t)src->rows * ((src->cols + 1023) / 1024);
-  values_kernel<<<(unsigned)((items + 7) / 8), 256, 0, (cudaStream_t)stream>>>(src->q, src->stride, src->scale, out, src->rows,
-                                                                              src->cols);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = launch(values_kernel, (unsigned)((items + 7) / 8), 256, 0, (cudaStream_t)stream, src->q, src->stride, src->scale, out,
+                               src->rows, src->cols);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status_t moe_rms_norm_i8(const moe_norm_t* p, const moe_i8_rows_t* xq, void* stream) {

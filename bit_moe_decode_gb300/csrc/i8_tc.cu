@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
   const bool by_tile = a.tiles < (int)gridDim.x + 1;
   const int tile = by_tile ? blockIdx.x : first_stage(a, blockIdx.x + 1) / nk;
   const int from = cta_of(a, tile * nk), to = cta_of(a, tile * nk + nk - 1);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  next_may_start();
+  wait_for_prior();
   if (from == to || (!by_tile && from != (int)blockIdx.x)) return;
   const int row = threadIdx.x + (GATED ? 0 : blockIdx.z * 128), slab = 256 * a.nt;
   const int n = tile % a.tiles_n * (GATED ? 128 : 256) + row, t = tile / a.tiles_n * a.nt + 4 * blockIdx.y;
@@ -437,7 +438,7 @@ template <bool GATED>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const __grid_constant__ CUtensorMap map_x,
                                                                  const __grid_constant__ CUtensorMap map_w0,
                                                                  const __grid_constant__ CUtensorMap map_w1) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");           // (finish_kernel waits for this grid's end)
+  next_may_start();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ uint64_t bar_full[kMaxStages], bar_empty[kMaxStages];          // packed tiles
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 12); }
     fence_mbar_init();
     __syncwarp();
+    wait_for_prior();
     if (lane == 0)
       for (int i = 0; i < early; ++i) copy_next(i);
   }
@@ -486,6 +488,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   }
   if (warp == 21) tc_alloc(&s_tmem, 512);
   tc_fence_before();
+  wait_for_prior();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -654,7 +657,8 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
 // squares (below 2^31). A warp a row.
 __global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, int pieces, uint8_t* out,
                                                     uint32_t* squares) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // (pair_kernel may set itself up meanwhile)
+  next_may_start();
+  wait_for_prior();
   const int lane = threadIdx.x & 31;
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 4) {
     uint32_t sq = 0;
@@ -735,12 +739,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
   const uint32_t tmem = s_tmem;
   Waits wait{a.m.status, false};
 
+  wait_for_prior();                                       // X in binary16 is there
   if (wg == kControl) {
     regs_less<40>();
     if (warp == kCopier) {
       // ================================================================ copies
       if (lane == 0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // X in binary16 is there
         int stage = 0, phase = 1;                         // (the first pass over the ring finds it empty)
         for (int j = 0; j < my_tiles; ++j) {
           const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + rank * part;
@@ -770,7 +774,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
       const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * (TOKENS / 2);
       const uint64_t dx = umma_desc_sw128(ring + 16384 + d * part * 256);
       int stage = 0, phase = 0, seg = 0;
-      asm volatile("griddepcontrol.wait;" ::: "memory");
       uint32_t squares = tile_squares(a, first / a.tiles_n * a.nt);
       for (int j = 0; j < my_tiles; ++j) {
         const bool single = __reduce_max_sync(0xFFFFFFFFu, squares) <= a.most;
@@ -829,7 +832,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
     const int id = GATED ? row : lane;
     Scales<GATED, TOKENS / 2, kWidth> scales;
     int seg = 0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int j = 0; j < my_tiles; ++j) {
       const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + d * half;
       const int n0 = GATED ? tn * 128 + rank * 64 : tn * 256 + rank * 128 + (warp & 3) * 32;
@@ -935,15 +937,6 @@ static bool map_rows(CUtensorMap* m, const int8_t* q, int rows, int cols, int64_
   return moe_internal::tmap_u8(m, q, 2, dims, strides, box);
 }
 
-static cudaLaunchConfig_t config(const TcPlan& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas);
-  cfg.blockDim = dim3(p.pair == 0 ? kSmallThreads : p.pair == 128 ? Pair<128>::kThreads : Pair<256>::kThreads);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = stream;
-  return cfg;
-}
-
 // Once per device: the kernels' shared memory
 static bool prepare(int dev) {
   static bool ready[64];
@@ -993,34 +986,19 @@ moe_status_t tc_multiply(const MatArgs& a, const TcPlan& p, cudaStream_t stream)
   const bool wide = aligned && (gated || p.pair || p.nt > 16);
   const TcArgs args{a, p.nt, p.tiles_n, p.tiles, p.stages, p.grain, p.share, p.extra, parts, squares, wide,
                     (uint32_t)min((1ll << 34) / a.K, 0xFFFFFFFFll)};
-  cudaLaunchConfig_t cfg = config(p, stream);
-  cudaLaunchAttribute at;
   cudaError_t e;
   if (p.pair) {
-    widen_kernel<<<min((a.T + 3) / 4, 2048), 128, 0, stream>>>(a.x, a.x_stride, a.T, a.K, pieces, halves, squares);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    e = launch(widen_kernel, min((a.T + 3) / 4, 2048), 128, 0, stream, a.x, a.x_stride, a.T, a.K, pieces, halves, squares);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     auto* kernel = p.pair == 128 ? (gated ? pair_kernel<true, 128> : pair_kernel<false, 128>)
                                  : (gated ? pair_kernel<true, 256> : pair_kernel<false, 256>);
-    e = cudaLaunchKernelEx(&cfg, kernel, args, mx, m0, m1);
+    e = launch(kernel, p.ctas, p.pair == 128 ? Pair<128>::kThreads : Pair<256>::kThreads, p.smem, stream, args, mx, m0, m1);
   } else {
-    e = gated ? cudaLaunchKernelEx(&cfg, small_kernel<true>, args, mx, m0, m1) : cudaLaunchKernelEx(&cfg, small_kernel<false>, args, mx, m0, m1);
-    if (e == cudaSuccess && p.grain == 1 && p.ctas > 1) {
-      cfg.gridDim = dim3(min(p.tiles, p.ctas - 1), p.nt / 4, gated ? 1 : 2);
-      cfg.blockDim = dim3(128);
-      cfg.dynamicSmemBytes = 0;
-      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      at.val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = &at;
-      cfg.numAttrs = 1;
-      e = gated ? cudaLaunchKernelEx(&cfg, finish_kernel<true>, args) : cudaLaunchKernelEx(&cfg, finish_kernel<false>, args);
-    }
+    e = launch(gated ? small_kernel<true> : small_kernel<false>, p.ctas, kSmallThreads, p.smem, stream, args, mx, m0, m1);
+    if (e == cudaSuccess && p.grain == 1 && p.ctas > 1)
+      e = launch(gated ? finish_kernel<true> : finish_kernel<false>, dim3(min(p.tiles, p.ctas - 1), p.nt / 4, gated ? 1 : 2), 128, 0, stream, args);
   }
-  if (e != cudaSuccess) { cudaGetLastError(); return MOE_ERR_CUDA; }
-  return MOE_OK;
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace i8

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
     ++next;
     if (++next_slot == kTileStages) next_slot = 0;
   };
+  wait_for_prior();
 #pragma unroll
   for (int i = 0; i < kTileStages - 1; ++i) copy_next();
 
@@ -169,9 +170,7 @@ moe_status_t tile_multiply(const MatArgs& a, cudaStream_t stream) {
     configured[dev] = 1;
   }
   const dim3 grid((a.N + (a.w[1] ? 31 : 63)) / (a.w[1] ? 32 : 64), (a.T + 63) / 64);
-  if (a.w[1]) tile_kernel<true><<<grid, kTileThreads, smem, stream>>>(a);
-  else tile_kernel<false><<<grid, kTileThreads, smem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch(a.w[1] ? tile_kernel<true> : tile_kernel<false>, grid, kTileThreads, smem, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace i8

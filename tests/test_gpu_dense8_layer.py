@@ -217,3 +217,58 @@ def test_many_tokens(m):
     y = torch.empty(T, N, device=DEV)
     m.moe_i8_matmul(x, w, y=y, ws=w.workspace(T))
     assert np.array_equal(y.cpu().numpy(), ref.product(xq, xs, wq, ws))
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 1024, 700), (20, 512, 512), (60, 2048, 900), (200, 1040, 300), (300, 512, 2000), (1000, 256, 256)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_behind_each_other_share_their_buffers(m, T, K, N, graph):
+    """Launches overlap: each call's codes, outputs and workspace are written again by the calls right behind it (ours and torch's),
+    and what was computed in between is what each call computes alone."""
+    g = torch.Generator(DEV).manual_seed(T)
+    src = [torch.randn(T, K, generator=g, device=DEV) for _ in range(3)]
+    w, v = m.I8Rows.of(torch.randn(N, K, generator=g, device=DEV)), m.I8Rows.of(torch.randn(N, K, generator=g, device=DEV))
+    x8, h8, y, h = m.I8Rows(T, K), m.I8Rows(T, K), torch.empty(T, N, device=DEV), torch.empty(T, K, device=DEV)
+    ws = w.workspace(T)
+    keep = torch.empty(24, 2, T, N, device=DEV)
+
+    def step(i, wait):
+        m.moe_i8_quantize(src[i % 3], x8)
+        wait()
+        m.moe_i8_matmul(x8, w, y=y, ws=ws)
+        wait()
+        m.moe_i8_quantize(src[(i + 1) % 3], x8)          # behind the product that read x8
+        wait()
+        m.moe_i8_matmul(x8, v, y=y, base=y, ws=ws)       # onto the product before it
+        wait()
+        keep[i, 0].copy_(y)
+        wait()
+        m.moe_rms_norm_i8(src[i % 3], h8, r=src[(i + 2) % 3], h_out=h)
+        wait()
+        h.mul_(0.5)
+        wait()
+        m.moe_rms_norm_i8(h, h8, h_out=h)
+        wait()
+        m.moe_i8_gated(h8, w, v, y=y, ws=ws)
+        wait()
+        keep[i, 1].copy_(y)
+        wait()
+    for i in range(3):
+        step(i, torch.cuda.synchronize)
+    want = keep[:3].clone()
+    keep.zero_()
+    torch.cuda.synchronize()
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            for i in range(24):
+                step(i, lambda: None)
+        cg.replay()
+        keep.zero_()
+        cg.replay()
+    else:
+        for i in range(24):
+            step(i, lambda: None)
+    torch.cuda.synchronize()
+    assert m.moe_get_device_status(ws) == 0
+    for i in range(24):
+        assert torch.equal(keep[i], want[i % 3]), i
