@@ -6,7 +6,7 @@
 // copies of a row each took 100 cycles apiece to issue, which held the stream at 3 TB/s.) 16 warps (two sets that take stages in
 // turn, 128 codes a warp) make the codes binary16 (exactly), and mma.sync (m16n8k16) multiplies them with the tokens, which the CTA
 // keeps in shared memory in binary16. fp32 adds 1024 products exactly; then the accumulators are added to integers. Four more
-// warps add the 16 warps' sums and write a group's outputs while the next group is under way. (1 x 4096 x 4096 6.7 us; 1 x 4096 x
+// warps add the 16 warps' sums and write a group's outputs while the next group is under way. (1 x 4096 x 4096 6.2 us; 1 x 4096 x
 // 32768 23 us, 5.9 TB/s.)
 // The order of k within a block is the one in which a lane reads its codes: 16 contiguous bytes of two rows.
 // Gated: rows 0-7 of the 16 are gate's, 8-15 up's of the same channels, so that a thread has both.
@@ -267,15 +267,13 @@ static moe_status_t rows_multiply(const MatArgs& a, int sms, cudaStream_t stream
   // 28 us against 23, 1 x 4096 x 4096 with 14 rows 7.7 against 7.1.)
   const int channels = a.w[1] ? 8 : 16, groups = (a.N + channels - 1) / channels;
   const int whole = a.K / 128;
-  CUtensorMap map[2], tail[2];
-  for (int i = 0; i < 2; ++i) {
-    const int m = a.w[1] ? i : 0;
+  CUtensorMap map[2] = {}, tail[2] = {};     // (of which a kernel uses those that K needs)
+  for (int m = 0; m < (a.w[1] ? 2 : 1); ++m) {
     const uint64_t dims[3] = {128, (uint64_t)a.N, (uint64_t)whole}, strides[2] = {(uint64_t)a.w_stride[m], 128};
     const uint32_t box[3] = {128, (uint32_t)channels, 8};
     const uint64_t tdims[2] = {(uint64_t)a.K, (uint64_t)a.N};
-    if (!moe_internal::tmap_u8(&tail[i], a.w[m], 2, tdims, strides, box)) return MOE_ERR_CUDA;
-    map[i] = tail[i];
-    if (whole > 0 && !moe_internal::tmap_u8(&map[i], a.w[m], 3, dims, strides, box)) return MOE_ERR_CUDA;
+    if (whole * 128 < a.K && !moe_internal::tmap_u8(&tail[m], a.w[m], 2, tdims, strides, box)) return MOE_ERR_CUDA;
+    if (whole > 0 && !moe_internal::tmap_u8(&map[m], a.w[m], 3, dims, strides, box)) return MOE_ERR_CUDA;
   }
   const int nt = rows_tiles(a.T), ctas = min(groups, sms);
   auto* run = a.w[1] ? (nt == 1 ? launch_rows<true, 1> : nt == 2 ? launch_rows<true, 2> : launch_rows<true, 4>)

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(256) values_kernel(const int8_t* q, int64_t st
 
 template <typename TH, typename TR, bool NORM>
 static moe_status_t launch_rows(const RowArgs& a, int rows, cudaStream_t st) {
-  // Threads of a row. Up to 1024 columns a warp has a row and a block eight (100,000 x 256: 22.6 us, blocks of one warp 53). The
+  // Threads of a row. Up to 1024 columns a warp has a row and a block eight (100,000 x 256: 22 us, blocks of one warp 53). The
   // norm goes by the row's length alone, so that a token's sum has one order; few threads with several vectors each were slower
   // (1 x 4096 2.8 us with 512 threads, 3.3 with 128; 333 x 7168 7.6 and 8.7). Quantising many rows has no sum, and
   // more rows at a time hide their reductions (32768 x 4096 bf16: 78 us with 128 threads, 126 with 512; 64 x 4096 3.5 and 2.3).
