@@ -135,6 +135,7 @@ struct Waits {
 __device__ __forceinline__ bool ends_segment(int i, int stages, int d, bool single) {
   return i == stages - 1 || (!single && (i + 1 + d * (kSegment / 2)) % kSegment == 0);
 }
+__device__ __forceinline__ int first_end(int d) { return kSegment - 1 - d * (kSegment / 2); }
 
 // 128 codes of a weight row (row: its place in the tile, for the swizzle) -> 64 TMEM columns of the thread's lane
 __device__ __forceinline__ void convert_w(uint32_t from, int row, uint32_t taddr) {
@@ -222,8 +223,8 @@ __device__ __forceinline__ void more_sums(uint32_t taddr, int n, int (&sum)[COLS
 // of every fourth token (gated: eighth). WIDTH channels are written by the 32 threads that have them, or gated by the 2 WIDTH threads
 // that have gate's (columns 0 .. WIDTH - 1 of the buffer) and up's. Where a tensor's alignment does not allow that (or the group ends
 // beyond N), a channel a thread. Loops are unrolled: a warp alone has no other work to hide an instruction's latency. (Rolled, with
-// the sums selected by the counter, a tile of 256 tokens took 10 us: 2048 x 1024 x 32768 155 us against 103, gated 1945 x 304 x 7288
-// 98 against 49; 1155 x 1376 x 11355, a channel a thread, 84 against 45.) small_kernel with 16 tokens has no buffer for it: a
+// the sums selected by the counter, a tile of 256 tokens took 10 us: 2048 x 1024 x 32768 155 us against 96, gated 1945 x 304 x 7288
+// 98 against 47; 1155 x 1376 x 11355, a channel a thread, 84 against 43.) small_kernel with 16 tokens has no buffer for it: a
 // further stage of copies is worth more (12 x 4096 x 32768 26.1 us against 26.9).
 
 // The scales that a tile's outputs need, loaded long before: tokens t0 + lane, + 32, ..., and four channels' from n0 + 4 (id % (WIDTH / 4)).
@@ -689,16 +690,24 @@ __global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t str
   }
 }
 
-// The largest of a tile's sums of squares that a lane has (of its tokens t0 + lane, + 32, ...).
-__device__ __forceinline__ uint32_t tile_squares(const TcArgs& a, int t0) {
-  uint32_t m = 0;
+// A tile's sums of squares, a lane's of tokens t0 + lane, + 32, ...; loaded early, their maximum (of the warp's) taken late
+template <int TOKENS>
+struct Squares {
+  uint32_t v[TOKENS / 32];
+  __device__ __forceinline__ void load(const TcArgs& a, int t0) {
 #pragma unroll
-  for (int i = 0; i < kPairTokens / 32; ++i) {
-    const int t = t0 + 32 * i + (int)(threadIdx.x & 31);
-    if (32 * i < a.nt && t < a.m.T) m = max(m, a.squares[t]);
+    for (int i = 0; i < TOKENS / 32; ++i) {
+      const int t = t0 + 32 * i + (int)(threadIdx.x & 31);
+      v[i] = 32 * i < a.nt && t < a.m.T ? a.squares[t] : 0;
+    }
   }
-  return m;
-}
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < TOKENS / 32; ++i) m = max(m, v[i]);
+    return __reduce_max_sync(0xFFFFFFFFu, m);
+  }
+};
 
 template <bool GATED, int TOKENS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThreads, 1)
@@ -774,10 +783,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
       const uint32_t idesc = (1u << 4) | ((uint32_t)(half >> 3) << 17) | (16u << 24), td = tmem + d * (TOKENS / 2);
       const uint64_t dx = umma_desc_sw128(ring + 16384 + d * part * 256);
       int stage = 0, phase = 0, seg = 0;
-      uint32_t squares = tile_squares(a, first / a.tiles_n * a.nt);
+      Squares<TOKENS> squares;
+      squares.load(a, first / a.tiles_n * a.nt);
       for (int j = 0; j < my_tiles; ++j) {
-        const bool single = __reduce_max_sync(0xFFFFFFFFu, squares) <= a.most;
-        squares = tile_squares(a, (first + (j + 1) * step_tiles) / a.tiles_n * a.nt);     // the next tile's
+        const bool single = squares.most() <= a.most;
+        squares.load(a, (first + (j + 1) * step_tiles) / a.tiles_n * a.nt);     // the next tile's
         bool fresh = true;
         for (int s = 0; s < nk; ++s) {
           if (fresh) wait(bar_d_empty + d, (seg & 1) ^ 1);
@@ -832,14 +842,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
     const int id = GATED ? row : lane;
     Scales<GATED, TOKENS / 2, kWidth> scales;
     int seg = 0;
-    for (int j = 0; j < my_tiles; ++j) {
-      const int tile = first + j * step_tiles, tn = tile % a.tiles_n, t0 = tile / a.tiles_n * a.nt + d * half;
-      const int n0 = GATED ? tn * 128 + rank * 64 : tn * 256 + rank * 128 + (warp & 3) * 32;
+    // a tile's scales and squares are loaded before the outputs of the one before it
+    int tile = first, t0 = 0, n0 = 0;
+    Squares<TOKENS> squares;
+    auto load = [&]() {
+      const int tn = tile % a.tiles_n, tt = tile / a.tiles_n * a.nt;
+      t0 = tt + d * half;
+      n0 = GATED ? tn * 128 + rank * 64 : tn * 256 + rank * 128 + (warp & 3) * 32;
       scales.load(a.m, t0, n0, id);
-      const bool single = __reduce_max_sync(0xFFFFFFFFu, tile_squares(a, t0 - d * half)) <= a.most;
+      squares.load(a, tt);
+    };
+    load();
+    for (int j = 0; j < my_tiles; ++j) {
+      const bool single = squares.most() <= a.most;
       bool begun = false;
-      for (int s = 0; s < nk; ++s) {
-        if (!ends_segment(s, nk, d, single)) continue;
+      for (int s = single ? nk - 1 : min(first_end(d), nk - 1);; s = min(s + kSegment, nk - 1)) {       // the segments' last stages
         wait(bar_d_full + d, seg & 1);
         ++seg;
         tc_fence_after();
@@ -849,8 +866,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
         if (lane == 0) arrive_first(bar_d_empty + d);
         if (!begun && !single) integer_sums(half, sum);
         begun = true;
+        if (s == nk - 1) break;
       }
-      output_sums<16>(a, sum, single, scales, t0, half, n0, id, GATED ? obuf + d * (kOutBytes / 2) : obuf + warp * 2048, 1 + d);
+      const Scales<GATED, TOKENS / 2, kWidth> now = scales;
+      const int t_now = t0, n_now = n0;
+      tile += step_tiles;
+      if (j + 1 < my_tiles) load();
+      output_sums<16>(a, sum, single, now, t_now, half, n_now, id, GATED ? obuf + d * (kOutBytes / 2) : obuf + warp * 2048, 1 + d);
     }
   }
   __syncwarp();
