@@ -272,3 +272,52 @@ def test_calls_behind_each_other_share_their_buffers(m, T, K, N, graph):
     assert m.moe_get_device_status(ws) == 0
     for i in range(24):
         assert torch.equal(keep[i], want[i % 3]), i
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("T", [4, 100, 400])
+def test_calls_on_streams_that_wait_for_each_other(m, T, graph):
+    """A call behind an event of another stream, whose kernels are still under way, and one behind two streams."""
+    K, N = 1024, 768
+    g = torch.Generator(DEV).manual_seed(T)
+    src, w, v = torch.randn(T, K, generator=g, device=DEV), *(m.I8Rows.of(torch.randn(N, K, generator=g, device=DEV)) for _ in range(2))
+    big = torch.randn(4096, 4096, generator=g, device=DEV)
+    x, x8, z8 = torch.zeros(T, K, device=DEV), m.I8Rows(T, K), m.I8Rows(T, N)
+    y, z, out = (torch.zeros(T, N, device=DEV) for _ in range(3))
+    ws, ws2 = w.workspace(T), v.workspace(T)
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        big.mul_(1.0)                                    # something long before it
+        torch.mul(src, 2.0, out=x)
+        m.moe_i8_quantize(x, x8)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            m.moe_i8_matmul(x8, v, y=z, ws=ws2)
+            big.add_(0.0)
+            m.moe_i8_quantize(z, z8)
+        m.moe_i8_matmul(x8, w, y=y, ws=ws)
+        main.wait_stream(side)
+        m.moe_i8_values(z8, out)
+        out.add_(y)
+        m.moe_i8_matmul(x8, w, y=out, base=out, ws=ws2)
+    run()
+    torch.cuda.synchronize()
+    q, sc, _ = ref.quantize((2 * src).cpu().numpy())
+    a = ref.product(q, sc, w.q.cpu().numpy(), w.scale.cpu().numpy())
+    b = ref.product(q, sc, v.q.cpu().numpy(), v.scale.cpu().numpy())
+    zq, zs, _ = ref.quantize(b)
+    want = torch.from_numpy((zq.astype(np.float32) * zs[:, None] + a) + a)
+    assert torch.equal(out.cpu(), want)
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            run()
+    for _ in range(20):
+        for t in (x, y, z, out):
+            t.zero_()
+        cg.replay() if graph else run()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want)
+    assert m.moe_get_device_status(ws) == 0 and m.moe_get_device_status(ws2) == 0

@@ -268,3 +268,50 @@ def test_products_refuse(m):
         m.moe_i8_matmul(x, w, y=torch.empty(4, 9, device=DEV), ws=ws)
     with pytest.raises(m.MoeError):
         m.moe_i8_gated(x, w, m.I8Rows(9, 64), y=torch.empty(4, 8, device=DEV), ws=ws)
+
+
+WIDE = [(40, 40004, 128), (64, 20008, 512), (100, 9000, 512), (200, 2996, 1040), (300, 10004, 256), (600, 4100, 2064), (30, 33000, 1024), (64, 4096, 4096)]
+
+
+@pytest.mark.parametrize("T,N,K", WIDE)
+def test_matmul_aligned_outputs(m, T, N, K):
+    """Rows that four channels at a time can be written to, N not a multiple of a group's channels: each output alone and all
+    together, onto a base of their own and in place, with nothing written between the rows."""
+    (xq, xs), (wq, ws) = codes(T, K, 1, "normal"), codes(N, K, 2, "normal")
+    x, w = device_rows(m, xq, xs), device_rows(m, wq, ws)
+    want = ref.product(xq, xs, wq, ws)
+    wsp = w.workspace(T)
+    base = np.random.default_rng(3).standard_normal((T, N)).astype(np.float32) * np.abs(want).mean()
+    y, b = Out(T, N, torch.float32, pad=8, off=0), Out(T, N, torch.float32, pad=4, off=0)
+    h = Out(T, N, torch.bfloat16, pad=4, off=0)
+    m.moe_i8_matmul(x, w, y=y.t, ws=wsp)
+    m.moe_i8_matmul(x, w, y_bf16=h.t, ws=wsp)
+    assert np.array_equal(y.t.cpu().numpy(), want) and np.array_equal(h.t.float().cpu().numpy(), ref.bf16(want))
+    assert y.intact() and h.intact()
+    b.t.copy_(torch.from_numpy(base))
+    m.moe_i8_matmul(x, w, y=y.t, y_bf16=h.t, base=b.t, ws=wsp)
+    m.moe_i8_matmul(x, w, y=b.t, base=b.t, ws=wsp)
+    for o in (y, b):
+        assert np.array_equal(o.t.cpu().numpy(), base + want) and o.intact()
+    assert np.array_equal(h.t.float().cpu().numpy(), ref.bf16(base + want)) and h.intact()
+    assert m.moe_get_device_status(wsp) == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 20004, 128), (64, 10008, 512), (100, 4500, 512), (200, 1500, 1040), (300, 5004, 256), (600, 2052, 2064)])
+def test_gated_aligned_outputs(m, T, N, K):
+    (xq, xs), (gq, gs), (uq, us) = codes(T, K, 1, "normal"), codes(N, K, 2, "normal"), codes(N, K, 3, "normal")
+    xs, gs = xs * np.float32(2.0 ** -8), gs * np.float32(2.0 ** -8)
+    x, gate, up = device_rows(m, xq, xs), device_rows(m, gq, gs), device_rows(m, uq, us)
+    g, u = ref.product(xq, xs, gq, gs), ref.product(xq, xs, uq, us)
+    want = ref.gated(g, u)
+    wsp = gate.workspace(T)
+    y, h = Out(T, N, torch.float32, pad=4, off=0), Out(T, N, torch.bfloat16, pad=4, off=0)
+    m.moe_i8_gated(x, gate, up, y=y.t, ws=wsp)
+    m.moe_i8_gated(x, gate, up, y_bf16=h.t, ws=wsp)
+    got = y.t.cpu().numpy()
+    assert np.all(np.abs(got - want) <= gated_bound(g, u, want))
+    assert np.array_equal(h.t.float().cpu().numpy(), ref.bf16(got))
+    y2, odd = Out(T, N, torch.float32), Out(T, N, torch.bfloat16)          # the same bits a channel a thread
+    m.moe_i8_gated(x, gate, up, y=y2.t, y_bf16=odd.t, ws=wsp)
+    assert torch.equal(y2.t, y.t) and torch.equal(odd.t, h.t)
+    assert y.intact() and h.intact() and y2.intact() and odd.intact() and m.moe_get_device_status(wsp) == 0
