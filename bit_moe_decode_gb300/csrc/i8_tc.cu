@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
     if (lane < kSlots) { mbar_init(bar_x_full + lane, 4); mbar_init(bar_x_empty + lane, 2); }
     fence_mbar_init();
   }
+  wait_for_prior();                                        // (before columns are taken: a kernel that still runs may want some)
   if (warp == 21) tc_alloc(&s_tmem, 512);
   tc_fence_before();
-  wait_for_prior();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -658,8 +658,8 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
 // squares (below 2^31). A warp a row.
 __global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t stride, int rows, int K, int pieces, uint8_t* out,
                                                     uint32_t* squares) {
-  next_may_start();
   wait_for_prior();
+  next_may_start();                                        // (pair_kernel takes columns at once: only when no kernel before this still runs)
   const int lane = threadIdx.x & 31;
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 4) {
     uint32_t sq = 0;
