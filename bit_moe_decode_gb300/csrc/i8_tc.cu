@@ -401,6 +401,10 @@ __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
   float xs[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) xs[e] = __ldg(a.m.xs + min(t + e, a.m.T - 1));
+  float before[4];
+  if (!GATED && a.m.base)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) before[e] = t + e < a.m.T ? a.m.base[(int64_t)(t + e) * a.m.base_stride + n] : 0.f;
   const int* p = a.parts + (blockIdx.y * 256 + row) * 4;
   int g[4] = {}, u[4] = {};
 #pragma unroll 4
@@ -416,14 +420,10 @@ __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
   float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = GATED ? silu_mul(product(g[e], xs[e], w0), product(u[e], xs[e], w1)) : product(g[e], xs[e], w0);
-  const MatArgs& m = a.m;                 // (read where they are used: in registers beforehand 64 x 4096 x 4096 took 0.3 us more)
-  if (m.base) {
-    float before[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) before[e] = t + e < m.T ? m.base[(int64_t)(t + e) * m.base_stride + n] : 0.f;
+  const MatArgs& m = a.m;                 // (read where they are used: in registers beforehand 64 x 4096 x 4096 took 0.4 us more)
+  if (!GATED && m.base)
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(v[e], before[e]);
-  }
   if (m.y)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
