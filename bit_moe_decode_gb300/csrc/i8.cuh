@@ -19,11 +19,17 @@ inline moe_status_t check_rows(const moe_i8_rows_t* r) {
 
 // Launches overlap: a kernel's CTAs start while the one before it in the stream ends, set themselves up, and wait for its end (and its
 // writes) before they touch memory. Every CTA of every kernel here waits, so that a kernel's end implies the ends of all before it.
-// (1 x 4096 x 4096 6.7 -> 6.3 us, called one after another from the host 8 x 4096 x 4096 8.8 -> 6.9. Not where a grid leaves SMs free
-// or CTAs share one: the next kernel's CTAs then crowd there. With next_may_start in tile_kernel 1000 x 512 x 512 took 6.9 us, 5.5
-// without; in pair_kernel 512 x 4096 x 4096 23.0, 19.0 without.)
+// (1 x 4096 x 4096 6.7 -> 6.3 us, called one after another from the host 8 x 4096 x 4096 8.8 -> 6.9.) next_may_start lets the next
+// kernel in as soon as all CTAs have started, not only when they end: where a CTA fills its SM and for a launch that belongs to
+// the same call. Elsewhere the next kernel's CTAs crowd the SMs that happen to be free: with it in tile_kernel 1000 x 512 x 512 took 6.9
+// us, 5.5 without; in pair_kernel 512 x 4096 x 4096 23.0 and 19.0.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// What may be done before that: the weights' lines that a CTA needs first are asked for in L2, which is always current, whoever still
+// writes them; and descriptors, which are parameters, are fetched. (64 x 4096 x 4096 12.0 -> 11.2 us; the layer of i8_rows.cu with 20
+// tokens 69.3 -> 66.4. In pair_kernel it took 1 % of a layer of 300 tokens: not there.)
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 template <typename... P, typename... A>
 inline cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};

@@ -77,11 +77,26 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(MatArgs a, int gro
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 8); }
     else if (lane >= 30) { mbar_init(bar_sum_full + lane - 30, kRowWarps); mbar_init(bar_sum_empty + lane - 30, kOutWarps); }
     fence_mbar_init();
+    if (lane == 0) {
+      if (whole > 0) prefetch_map(&map0);
+      if (GATED && whole > 0) prefetch_map(&map1);
+      if (whole < blocks) prefetch_map(&tail0);
+      if (GATED && whole < blocks) prefetch_map(&tail1);
+    }
     __syncwarp();
     wait_for_prior();
     if (lane == 0)
       for (; issued < stages && c_group < groups; ++issued) copy_next(issued);
   } else {
+    // ---- the lines of the first stages (a stage: 16 rows of 8)
+    for (int s = tid >> 7, group = blockIdx.x, part = s; s < stages; s += (kRowWarps + kOutWarps) / 4, part += (kRowWarps + kOutWarps) / 4) {
+      while (part >= per_group) {
+        part -= per_group;
+        group += gridDim.x;
+      }
+      const int r = tid >> 3 & 15, up = GATED ? r >> 3 : 0, n = group * channels + (GATED ? r & 7 : r), k = part * kRowStageK + (tid & 7) * 128;
+      if (group < groups && n < a.N && k < a.K) prefetch_line(a.w[up] + n * a.w_stride[up] + k);
+    }
     // ---- the tokens, in convert4's order, zeros past K
     wait_for_prior();
     const int pieces = blocks * 8, all = a.T * pieces, threads = (kRowWarps + kOutWarps) * 32;

@@ -17,6 +17,10 @@ namespace moe {
 namespace i8 {
 
 constexpr float kFloor = 7.888609052210118e-31f;    // 2^-100
+// Rows up to which the next kernel is let in at once: most SMs are free for it then, and it is one whose CTAs fill them (a layer of 8
+// calls, 4096 wide, I 8192, in a graph: 1 token 44 us, 50 without; 64 tokens 76 and 78). With more the next one's CTAs crowd the SMs
+// that are free: 300 tokens 188 us, 129 without.
+constexpr int kEarlyRows = 64;
 constexpr float kNear = 3.0517578125e-05f;          // 2^-15
 
 struct RowArgs {
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(512) rows_kernel(RowArgs a) {
   __shared__ uint32_t part[64];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int tid = threadIdx.x, n = a.cols >> 3, warps = blockDim.x >> 5;
-  next_may_start();
+  if (a.rows <= kEarlyRows) next_may_start();
   wait_for_prior();
   if (row >= a.rows) return;                     // (only where a row is a warp's)
   const TH* h = (const TH*)a.h + row * a.h_stride;
@@ -239,7 +243,6 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(RowArgs a) {
   const int64_t row = blockIdx.x;
   const int n = a.cols >> 3, warps = blockDim.x >> 5;
   const T* h = (const T*)a.h + row * a.h_stride;
-  next_may_start();
   wait_for_prior();
   float sum = 0.f, most = 0.f;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -270,7 +273,6 @@ __global__ void __launch_bounds__(256) values_kernel(const int8_t* q, int64_t st
   const int per_row = (cols + 1023) / 1024, lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t row = item / per_row;
-  next_may_start();
   wait_for_prior();
   if (row >= rows) return;
   const int first = (int)(item - row * per_row) * 1024 + 4 * lane;

@@ -476,10 +476,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(TcArgs a, const
   if (warp == 20) {
     if (lane < stages) { mbar_init(bar_full + lane, 1); mbar_init(bar_empty + lane, 12); }
     fence_mbar_init();
+    if (lane == 0) {
+      prefetch_map(&map_w0);
+      if (GATED) prefetch_map(&map_w1);
+      prefetch_map(&map_x);
+    }
     __syncwarp();
     wait_for_prior();
     if (lane == 0)
       for (int i = 0; i < early; ++i) copy_next(i);
+  }
+  if (warp < 20 && early <= nk - s_first) {                  // the lines of the first stages' weights (of one tile)
+    const int tn = first % a.tiles_n;
+    for (int i = tid; i < early * 256; i += 640) {
+      const int row = i & 255, up = GATED ? row >> 7 : 0, n = GATED ? tn * 128 + (row & 127) : tn * 256 + row;
+      if (n < a.m.N) prefetch_line(a.m.w[up] + n * a.m.w_stride[up] + (s_first + (i >> 8)) * kTileK);
+    }
   }
   if (warp == 0) {
     if (lane < 2 * kSmallA) { mbar_init(&bar_a_full[0][0] + lane, 4); mbar_init(&bar_a_empty[0][0] + lane, 1); }

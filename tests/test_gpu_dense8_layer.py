@@ -321,3 +321,30 @@ def test_calls_on_streams_that_wait_for_each_other(m, T, graph):
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), want)
     assert m.moe_get_device_status(ws) == 0 and m.moe_get_device_status(ws2) == 0
+
+
+@pytest.mark.parametrize("T", [1, 8, 20, 64, 100])
+@pytest.mark.parametrize("N,K", [(768, 1024), (100, 208), (4096, 4096)])
+def test_weights_written_right_before_their_product(m, T, N, K):
+    """Weights that the kernel before a product writes, time after time in the same place."""
+    g = torch.Generator(DEV).manual_seed(T + N)
+    x = m.I8Rows.of(torch.randn(T, K, generator=g, device=DEV))
+    src = [torch.randn(N, K, generator=g, device=DEV) for _ in range(3)]
+    w, ws, y = m.I8Rows(N, K), m.I8Rows(N, K).workspace(T), torch.empty(3, 2, T, N, device=DEV)
+    want = torch.empty_like(y)
+    for i in range(3):
+        v = m.I8Rows.of(src[i])
+        torch.cuda.synchronize()
+        m.moe_i8_matmul(x, v, y=want[i, 0], ws=ws)
+        m.moe_i8_gated(x, v, v, y=want[i, 1], ws=ws)
+        torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(3):
+            m.moe_i8_quantize(src[i], w)
+            m.moe_i8_matmul(x, w, y=y[i, 0], ws=ws)
+            m.moe_i8_quantize(src[(i + 1) % 3], w)
+            m.moe_i8_quantize(src[i], w)
+            m.moe_i8_gated(x, w, w, y=y[i, 1], ws=ws)
+        assert torch.equal(y, want)
+        y.zero_()
+    assert m.moe_get_device_status(ws) == 0
