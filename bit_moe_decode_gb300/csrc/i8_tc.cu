@@ -899,13 +899,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<TOKENS>::kThrea
 
 // Nanoseconds. small_kernel: 3.2 us; a stage takes 0.53 us and 4 ns a token of the tile; with nothing else to do the weights come at 6.3
 // TB/s; a tile's outputs take 55 ns a token, or 80 beside the next tile's stages. A second launch that adds up `ctas` parts of nt tokens
-// takes instead 0.8 us, 0.34 a part of a tile and 0.73 ns a CTA and token. (Measured: 64 x 4096 x 4096 (16 tiles): 28.2 us a tile a
-// CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6; 16 x 4096 x 32768 (128 tiles):
+// takes instead 0.3 us, 0.34 a part of a tile and 0.45 ns a CTA and token. (Measured, before launches overlapped: 64 x 4096 x 4096
+// (16 tiles): 28.2 us a tile a CTA, 13.1 with 64 CTAs, 14.3 with 128, 15.9 with 152; 16 x 4096 x 4096: 21.1, 10.9, 10.6, 11.6; 16 x 4096 x 32768 (128 tiles):
 // 26.8 a tile a CTA, 30.7 with 152; gated 48 x 4096 x 11008 (86 tiles): 28.5, 24.6 with 152.)
 // pair_kernel: 3.5 us and the widening; a stage takes 0.37 us with up to 128 tokens, else 0.34 us and 0.65 ns a token, or with all SMs at
-// it 2.5 ns a token (the products); a tile's outputs 32 ns a token (24 where they are written
-// four channels at a time, 39 where not), beside the next tile's stages. (201 x 4096 x 4096: 20.0 us with 128 tokens a tile,
-// 21.3 with 96 and one warpgroup that converts, 24.5 with 256.)
+// it 2.5 ns a token (the products); a tile's outputs 32 ns a token (24 where they are written four channels at a time, 39 where not),
+// beside the next tile's stages. (201 x 4096 x 4096: 20.0 us with 128 tokens a tile, 21.3 with 96 and one warpgroup that converts,
+// 24.5 with 256.)
 // More than 64 tokens: 154 x 7264 x 584 13.3 us by small_kernel, whose CTAs share tiles, and 30.7 by pair_kernel; 767 x 1936 x 226
 // gated 10.1 and 16.0; 68 x 2224 x 9507 18.1 and 15.1; 294 x 4032 x 8863 43 and 27.
 TcPlan tc_plan(const MatArgs& a, int sms) {
@@ -941,9 +941,10 @@ TcPlan tc_plan(const MatArgs& a, int sms) {
       p.ctas = min(all, m <= most / p.tiles ? m * p.tiles : most);
       p.share = all / p.ctas;
       p.extra = all % p.ctas;
-      const double parts = (p.ctas + p.tiles - 1) / p.tiles;
+      if (p.extra == 0 && p.share % nk == 0) continue;        // no tile is shared
+      const double parts = (p.ctas + p.tiles - 1) / p.tiles, stages = time((all + p.ctas - 1) / p.ctas), outs = p.tiles / p.ctas * more;
       if (p.ctas > p.tiles || m > most / p.tiles)
-        consider(p, 4000 + time((all + p.ctas - 1) / p.ctas) + 340 * (parts + (p.ctas % p.tiles ? 1 : 0)) + 0.73 * p.ctas * p.nt);
+        consider(p, 3500 + (stages > outs ? stages : outs) + 340 * (parts + (p.ctas % p.tiles ? 1 : 0)) + 0.45 * p.ctas * p.nt);
     }
   }
   if (a.T > kSmallTokens) {

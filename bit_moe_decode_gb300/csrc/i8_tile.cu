@@ -34,15 +34,20 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
 
   // ---- copies: a thread has unit tid % 8 of rows tid / 8 + 32 j: j = 0, 1 tokens, 2, 3 channels
   const int cu = tid & 7, cr = tid >> 3;
+  // (Rows past T or N are not copied: what stands in their place makes outputs that are not written. Repeating the last row, the CTAs
+  // asked for the same lines thousands of times: gated 7 x 176 x 4496 9.7 us, with 64 tokens 4.4.)
   const int8_t* from[4];
   uint32_t to[4];
+  bool have[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int row = cr + 32 * (j & 1);
     if (j < 2) {
-      from[j] = a.x + min(t0 + row, (int64_t)a.T - 1) * a.x_stride + 16 * cu;
+      have[j] = t0 + row < a.T;
+      from[j] = a.x + (t0 + row) * a.x_stride + 16 * cu;
     } else {
-      const int up = GATED ? row >> 4 & 1 : 0, n = min(n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row), a.N - 1);
+      const int up = GATED ? row >> 4 & 1 : 0, n = n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row);
+      have[j] = n < a.N;
       from[j] = a.w[up] + n * a.w_stride[up] + 16 * cu;
     }
     to[j] = base + (cr + 32 * j) * 128 + unit_of(cr, cu) * 16;      // (32 rows on the place in a row is the same)
@@ -52,7 +57,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
     if (next < blocks) {
       const bool in = next * 128 + 16 * cu < a.K;                    // (K is a multiple of 16)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) copy16(to[j] + next_slot * kTileStage, in ? from[j] + next * 128 : from[j], in);
+      for (int j = 0; j < 4; ++j)
+        if (have[j]) copy16(to[j] + next_slot * kTileStage, in ? from[j] + next * 128 : from[j], in);
     }
     copies_done();
     ++next;
@@ -145,14 +151,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
   }
 }
 
-// 1 us; 2 a wave of tiles and 0.6 a block of it (what mma.sync takes: 512 pairs a cycle and SM); and the weights at 4 TB/s, which so
+// 1 us; 1.6 a wave of tiles and 0.6 a block of it (what mma.sync takes: 512 pairs a cycle and SM); and the weights at 4 TB/s, which so
 // few copies in flight do not hide. (1000 x 512 x 512 5.1 us, tcgen05 10; 2000 x 128 x 128 3.2 and 10; 1000 x 1024 x 1024 13.7 and
 // 9.3; 65 x 1440 x 322 10.8 and 7.9.)
 double tile_estimate(const MatArgs& a, int sms) {
   if (a.K > kMaxTileK || (a.T + 63) / 64 > 65535) return 1e30;            // (65535: the grid's second dimension)
   const int channels = a.w[1] ? 32 : 64;
   const int64_t tiles = (int64_t)((a.N + channels - 1) / channels) * ((a.T + 63) / 64);
-  return 1000 + (double)((tiles + sms - 1) / sms) * ((a.K + 127) / 128 * 600 + 2000) +
+  return 1000 + (double)((tiles + sms - 1) / sms) * ((a.K + 127) / 128 * 600 + 1600) +
          (double)a.N * a.K * (a.w[1] ? 2 : 1) / 4000;
 }
 
