@@ -219,8 +219,8 @@ __device__ __forceinline__ void more_sums(uint32_t taddr, int n, int (&sum)[COLS
     }
   tc_fence_before();
 }
-// Outputs go through shared memory, 16 tokens at a time (8 where registers are short): a thread has all tokens of one row of the product, and writes four channels
-// of every fourth token (gated: eighth). WIDTH channels are written by the 32 threads that have them, or gated by the 2 WIDTH threads
+// Outputs go through shared memory, 16 tokens at a time (8 where registers are short): a thread has all tokens of one row of the
+// product, and writes four channels of every fourth token (gated: eighth). WIDTH channels are written by the 32 threads that have them, or gated by the 2 WIDTH threads
 // that have gate's (columns 0 .. WIDTH - 1 of the buffer) and up's. Where a tensor's alignment does not allow that (or the group ends
 // beyond N), a channel a thread. Loops are unrolled: a warp alone has no other work to hide an instruction's latency. (Rolled, with
 // the sums selected by the counter, a tile of 256 tokens took 10 us: 2048 x 1024 x 32768 155 us against 96, gated 1945 x 304 x 7288
@@ -233,11 +233,11 @@ struct Scales {
   float x[(COLS + 31) / 32], w[GATED ? 2 : 1][4];
   __device__ __forceinline__ void load(const MatArgs& a, int t0, int n0, int id) {
 #pragma unroll
-    for (int i = 0; i < (COLS + 31) / 32; ++i) x[i] = __ldg(a.xs + min(t0 + (int)(threadIdx.x & 31) + 32 * i, a.T - 1));
+    for (int i = 0; i < (COLS + 31) / 32; ++i) x[i] = a.xs[min(t0 + (int)(threadIdx.x & 31) + 32 * i, a.T - 1)];
 #pragma unroll
     for (int m = 0; m < (GATED ? 2 : 1); ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[m][e] = __ldg(a.ws[m] + min(n0 + 4 * (id % (WIDTH / 4)) + e, a.N - 1));
+      for (int e = 0; e < 4; ++e) w[m][e] = a.ws[m][min(n0 + 4 * (id % (WIDTH / 4)) + e, a.N - 1)];
   }
 };
 // Where outputs go, in registers. (As kernel parameters they were read from the constant cache for every value, each read waiting for the
@@ -335,7 +335,7 @@ __device__ __forceinline__ void output_sums(const TcArgs& args, const int (&sum)
   } else {
     // eight tokens at a time: not gated, of those the thread has the sums of
     constexpr int STEP = ROW / WIDTH;
-    const float w0 = __ldg(a.ws[0] + min(n, a.N - 1)), w1 = GATED ? __ldg(a.ws[1] + min(n, a.N - 1)) : 0.f;
+    const float w0 = a.ws[0][min(n, a.N - 1)], w1 = GATED ? a.ws[1][min(n, a.N - 1)] : 0.f;
     if (n >= a.N) left = 0;
 #pragma unroll
     for (int c = 0; c < COLS / 8; c += STEP, t += 8 * STEP, left -= 8 * STEP) {
@@ -397,10 +397,10 @@ __global__ void __launch_bounds__(128) finish_kernel(TcArgs a) {
   const int row = threadIdx.x + (GATED ? 0 : blockIdx.z * 128), slab = 256 * a.nt;
   const int n = tile % a.tiles_n * (GATED ? 128 : 256) + row, t = tile / a.tiles_n * a.nt + 4 * blockIdx.y;
   if (n >= a.m.N || t >= a.m.T) return;
-  const float w0 = __ldg(a.m.ws[0] + n), w1 = GATED ? __ldg(a.m.ws[1] + n) : 0.f;
+  const float w0 = a.m.ws[0][n], w1 = GATED ? a.m.ws[1][n] : 0.f;
   float xs[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) xs[e] = __ldg(a.m.xs + min(t + e, a.m.T - 1));
+  for (int e = 0; e < 4; ++e) xs[e] = a.m.xs[min(t + e, a.m.T - 1)];
   float before[4];
   if (!GATED && a.m.base)
 #pragma unroll
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(128) widen_kernel(const int8_t* x, int64_t str
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = make_uint4(0, 0, 0, 0);
-        if (16 * (k0 + 32 * j) < K) v[j] = __ldg(reinterpret_cast<const uint4*>(x + row * stride) + k0 + 32 * j);
+        if (16 * (k0 + 32 * j) < K) v[j] = reinterpret_cast<const uint4*>(x + row * stride)[k0 + 32 * j];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

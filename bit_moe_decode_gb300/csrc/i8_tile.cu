@@ -73,12 +73,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_kernel(MatArgs a) {
   // the scales of the lane's outputs: set 0 finishes the warps' first 16 tokens, set 1 the others
   float xs[2], ws[4][2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) xs[half] = __ldg(a.xs + min(t0 + wt + 16 * set + g + 8 * half, (int64_t)a.T - 1));
+  for (int half = 0; half < 2; ++half) xs[half] = a.xs[min(t0 + wt + 16 * set + g + 8 * half, (int64_t)a.T - 1)];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      ws[j][e] = __ldg(a.ws[GATED ? j >> 1 : 0] + min(n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * (GATED ? j & 1 : j) + 2 * c + e, a.N - 1));
+      ws[j][e] = a.ws[GATED ? j >> 1 : 0][min(n0 + (wn - 64) / (GATED ? 2 : 1) + 8 * (GATED ? j & 1 : j) + 2 * c + e, a.N - 1)];
   const uint32_t mine = unit_of(g, 4 * set + c) * 16;                // (the same in each eighth row)
   float acc[2][4][4] = {};
   int slot = 0;
