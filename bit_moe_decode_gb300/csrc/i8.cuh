@@ -27,8 +27,8 @@ inline moe_status_t check_rows(const moe_i8_rows_t* r) {
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // What may be done before that: the weights' lines that a CTA needs first are asked for in L2, which is always current, whoever still
-// writes them; and descriptors, which are parameters, are fetched. (64 x 4096 x 4096 12.0 -> 11.2 us; the layer of i8_rows.cu with 20
-// tokens 69.3 -> 66.4. In pair_kernel it took 1 % of a layer of 300 tokens: not there.)
+// writes them; and descriptors, which are parameters, are fetched. (64 x 4096 x 4096 12.0 -> 11.2 us; the layer of i8_rows.cu with 1
+// token 43.8 -> 41.0, with 20 69.4 -> 65.5. In pair_kernel it took 1 % of a layer of 300 tokens: not there.)
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 template <typename... P, typename... A>
